@@ -91,6 +91,20 @@ _SIGS = {
     "pg_row_rms_step": (_i32, [_P(PgLayout), _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _f32,
                                _f32, _f32, _f32, _vp]),
     "pg_row_rms_flush": (_i32, [_P(PgLayout), _vp, _vp, _vp, _i64, _f32, _f32, _f32, _vp]),
+    "pg_embed": (_i32, [_P(PgTable), _i32, _f32, _vp, _i64, _i32, _vp, _i64, _vp, _vp]),
+    "pg_embed_workspace_size": (_i64, [_i64, _i64, _i32]),
+    "pg_embed_backward": (_i32, [_vp, _i32, _i64, _vp, _i64, _i64, _i32, _f32, _vp, _vp, _vp,
+                                 _vp, _i64, _vp]),
+    "pg_embed_backward_dense": (_i32, [_vp, _i32, _i64, _vp, _i64, _i64, _i32, _f32, _vp, _i32,
+                                       _vp, _i64, _vp]),
+    "pg_layer_norm": (_i32, [_vp, _i32, _i64, _i32, _i64, _vp, _vp, _f32, _vp, _i64, _vp, _vp,
+                             _vp]),
+    "pg_layer_norm_workspace_size": (_i64, [_i64, _i32]),
+    "pg_layer_norm_backward": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i32, _vp, _vp, _vp, _vp,
+                                      _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
+    "pg_orthogonalize_workspace_size": (_i64, [_i64, _i32, _i32]),
+    "pg_orthogonalize": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _f32, _f32, _f32, _f32, _f32,
+                                _vp, _vp, _i64, _vp]),
     "pg_flash_blocks": (_i32, [_P(PgLayout), _i32, _vp, _i64, _vp]),
     "pg_lru_cache_sim": (_i32, [_vp, _i64, _i32, _i64, _P(PgCacheStats)]),
 }
@@ -422,6 +436,209 @@ def pg_row_rms_flush(layout, table, vhat, last_step, step, lr, beta2=0.95, weigh
     _check("pg_row_rms_flush", lib().pg_row_rms_flush(
         ctypes.byref(layout), _ptr(table), _ptr(vhat), _ptr(last_step), int(step), float(lr),
         float(beta2), float(weight_decay), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------
+# The training step around the memory: token embedding, layer norm,
+# orthogonalised update. Rows are the last dimension; a tensor of rows may be a
+# slice of wider rows (any one row stride). Every tensor of a call lives on one
+# GPU; the work goes to that GPU's current stream, or to `stream`.
+
+
+def _dtype(fn, name, t):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return PG_BF16
+    if t.dtype == torch.float32:
+        return PG_F32
+    raise ValueError(f"{fn}: {name} is {t.dtype}, not float32 or bfloat16")
+
+
+def _rows(fn, name, t):
+    """(rows, row stride) of t, whose last dimension is a row."""
+    d = t.shape[-1]
+    if t.dim() != 2:
+        try:
+            t = t.view(-1, d)
+        except RuntimeError:
+            raise ValueError(f"{fn}: the rows of {name} have no single stride") from None
+    n = t.shape[0]
+    if n and d > 1 and t.stride(1) != 1:
+        raise ValueError(f"{fn}: the rows of {name} are not contiguous")
+    return n, t.stride(0) if n > 1 else d
+
+
+def _flat(fn, name, t, dtype, size, dev, at_least=False):
+    """t is contiguous, of dtype, with size elements, on dev."""
+    n = t.numel()
+    if t.dtype != dtype or t.device != dev or not t.is_contiguous() or \
+            (n < size if at_least else n != size):
+        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of {size} elements "
+                         f"on {dev}")
+
+
+def _like(fn, name, t, ref):
+    if t.shape != ref.shape or t.dtype != ref.dtype or t.device != ref.device:
+        raise ValueError(f"{fn}: {name} must be a {ref.dtype} tensor of shape "
+                         f"{tuple(ref.shape)} on {ref.device}")
+
+
+def _gpu(fn, name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on a GPU")
+    return t.device
+
+
+def _call(fn, dev, stream, *args):
+    import torch
+    f = getattr(lib(), fn)
+    if dev.index == torch.cuda.current_device():
+        _check(fn, f(*args, _stream(stream)))
+        return
+    with torch.cuda.device(dev):
+        _check(fn, f(*args, _stream(stream)))
+
+
+def _size(fn, *args):
+    v = getattr(lib(), fn)(*(int(a) for a in args))
+    if v < 0:
+        raise PagegramError(fn, v)
+    return v
+
+
+def pg_embed(table, tokens, out, scale=1.0, dev_status=None, stream=None):
+    """out [..., d] = scale * table[tokens]; tokens int32, contiguous. table (make_table) must
+    hold [n_rows, d] of float32 or bfloat16 on out's GPU."""
+    import torch
+    dev = _gpu("pg_embed", "out", out)
+    n, ld = _rows("pg_embed", "out", out)
+    _flat("pg_embed", "tokens", tokens, torch.int32, n, dev)
+    if dev_status is not None:
+        _flat("pg_embed", "dev_status", dev_status, torch.int32, 1, dev, at_least=True)
+    d = out.shape[-1]
+    data = table._keep[0] if hasattr(table, "_keep") else None
+    if hasattr(data, "numel") and table.dtype != PG_NF4:
+        want = torch.float32 if table.dtype == PG_F32 else torch.bfloat16
+        _flat("pg_embed", "table data", data, want, table.n_rows * d, dev)
+    _call("pg_embed", dev, stream, ctypes.byref(table), d, float(scale), _ptr(tokens), n,
+          _dtype("pg_embed", "out", out), _ptr(out), ld, _ptr(dev_status))
+
+
+def pg_embed_workspace_size(n_tok, V, d):
+    return _size("pg_embed_workspace_size", n_tok, V, d)
+
+
+def _embed_dout(fn, dout, tokens, workspace):
+    import torch
+    dev = _gpu(fn, "dout", dout)
+    n, ld = _rows(fn, "dout", dout)
+    _flat(fn, "tokens", tokens, torch.int32, n, dev)
+    _flat(fn, "workspace", workspace, torch.uint8, 0, dev, at_least=True)
+    return dev, n, ld, dout.shape[-1], _dtype(fn, "dout", dout)
+
+
+def pg_embed_backward(dout, tokens, V, urows, ugrad, n_unique, workspace, scale=1.0,
+                      stream=None):
+    """Touched rows of the table gradient: urows int64 and ugrad float32 with room for
+    min(n_tok, V) rows, n_unique int64 [1]; workspace uint8."""
+    import torch
+    fn = "pg_embed_backward"
+    dev, n, ld, d, dt = _embed_dout(fn, dout, tokens, workspace)
+    cap = min(n, int(V))
+    _flat(fn, "urows", urows, torch.int64, cap, dev, at_least=True)
+    _flat(fn, "ugrad", ugrad, torch.float32, cap * d, dev, at_least=True)
+    _flat(fn, "n_unique", n_unique, torch.int64, 1, dev, at_least=True)
+    _call(fn, dev, stream, _ptr(dout), dt, ld, _ptr(tokens), n, int(V), d, float(scale),
+          _ptr(urows), _ptr(ugrad), _ptr(n_unique), _ptr(workspace), _ws_bytes(workspace))
+
+
+def pg_embed_backward_dense(dout, tokens, dtable, workspace, scale=1.0, accumulate=0,
+                            stream=None):
+    """dtable float32 [V, d], written whole or (accumulate=1) added to."""
+    import torch
+    fn = "pg_embed_backward_dense"
+    dev, n, ld, d, dt = _embed_dout(fn, dout, tokens, workspace)
+    V = dtable.shape[0]
+    _flat(fn, "dtable", dtable, torch.float32, V * d, dev)
+    _call(fn, dev, stream, _ptr(dout), dt, ld, _ptr(tokens), n, V, d, float(scale),
+          _ptr(dtable), int(accumulate), _ptr(workspace), _ws_bytes(workspace))
+
+
+def pg_layer_norm(x, gamma, beta, y, eps=1e-5, mean=None, rstd=None, stream=None):
+    """y = layer norm of the rows of x (y may be x); gamma, beta float32 [d] (beta or None);
+    mean, rstd float32 [rows] or None."""
+    import torch
+    fn = "pg_layer_norm"
+    dev = _gpu(fn, "x", x)
+    n, ldx = _rows(fn, "x", x)
+    _like(fn, "y", y, x)
+    ldy = _rows(fn, "y", y)[1]
+    d = x.shape[-1]
+    _flat(fn, "gamma", gamma, torch.float32, d, dev)
+    if beta is not None:
+        _flat(fn, "beta", beta, torch.float32, d, dev)
+    if mean is not None:
+        _flat(fn, "mean", mean, torch.float32, n, dev)
+    if rstd is not None:
+        _flat(fn, "rstd", rstd, torch.float32, n, dev)
+    _call(fn, dev, stream, _ptr(x), _dtype(fn, "x", x), n, d, ldx, _ptr(gamma), _ptr(beta),
+          float(eps), _ptr(y), ldy, _ptr(mean), _ptr(rstd))
+
+
+def pg_layer_norm_workspace_size(n, d):
+    return _size("pg_layer_norm_workspace_size", n, d)
+
+
+def pg_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace, add=None,
+                           stream=None):
+    """dx (may be dy or add), dgamma and dbeta (or None) from pg_layer_norm's mean and rstd; add:
+    a gradient added to dx, or None."""
+    import torch
+    fn = "pg_layer_norm_backward"
+    dev = _gpu(fn, "x", x)
+    n, ldx = _rows(fn, "x", x)
+    d = x.shape[-1]
+    _like(fn, "dy", dy, x)
+    _like(fn, "dx", dx, x)
+    ldadd = 0
+    if add is not None:
+        _like(fn, "add", add, x)
+        ldadd = _rows(fn, "add", add)[1]
+    _flat(fn, "gamma", gamma, torch.float32, d, dev)
+    _flat(fn, "mean", mean, torch.float32, n, dev)
+    _flat(fn, "rstd", rstd, torch.float32, n, dev)
+    _flat(fn, "dgamma", dgamma, torch.float32, d, dev)
+    if dbeta is not None:
+        _flat(fn, "dbeta", dbeta, torch.float32, d, dev)
+    _flat(fn, "workspace", workspace, torch.uint8, 0, dev, at_least=True)
+    _call(fn, dev, stream, _ptr(dy), _rows(fn, "dy", dy)[1], _ptr(x), ldx, _dtype(fn, "x", x), n,
+          d, _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(add), ldadd, _ptr(dx),
+          _rows(fn, "dx", dx)[1], _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
+          _ws_bytes(workspace))
+
+
+def pg_orthogonalize_workspace_size(n_mat, rows, cols):
+    return _size("pg_orthogonalize_workspace_size", n_mat, rows, cols)
+
+
+def pg_orthogonalize(G, out, workspace, steps=5, coef=(3.4445, -4.7750, 2.0315), eps=1e-7,
+                     scale=1.0, stream=None):
+    """out (bfloat16) = scale * the Newton-Schulz iterate of each matrix of G [..., rows, cols]
+    (float32 or bfloat16, contiguous)."""
+    import torch
+    fn = "pg_orthogonalize"
+    dev = _gpu(fn, "G", G)
+    if G.dim() < 2 or not G.is_contiguous() or out.shape != G.shape:
+        raise ValueError(f"{fn}: G must be contiguous [..., rows, cols], out of its shape")
+    rows, cols = G.shape[-2:]
+    n_mat = 1
+    for s in G.shape[:-2]:
+        n_mat *= s
+    _flat(fn, "out", out, torch.bfloat16, G.numel(), dev)
+    _flat(fn, "workspace", workspace, torch.uint8, 0, dev, at_least=True)
+    a, b, c = (float(v) for v in coef)
+    _call(fn, dev, stream, _ptr(G), _dtype(fn, "G", G), n_mat, rows, cols, int(steps), a, b, c,
+          float(eps), float(scale), _ptr(out), _ptr(workspace), _ws_bytes(workspace))
 
 
 # ----------------------------------------------------------------------------

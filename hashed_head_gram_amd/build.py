@@ -11,7 +11,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpagegram.so")
 SOURCES = ["api.hip", "index.hip", "gemm.hip", "gemm_slots.hip", "engram.hip", "backward.hip", "stage.hip",
-           "probe.hip", "pagesim.cpp"]
+           "probe.hip", "api_train.hip", "embed.hip", "norm.hip", "orthogonalize.hip",
+           "pagesim.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

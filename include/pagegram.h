@@ -593,6 +593,137 @@ PG_API int pg_row_rms_flush(const pg_layout* layout, float* table, float* vhat,
                             float weight_decay, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * The training step around the memory: the token embedding whose output is
+ * the residual stream the memory is added to, the layer norm that reads that
+ * stream, and the orthogonalised update of the projection weights (the rows
+ * of W_V and of the W_K^(m); their gradient is pg_backward_scalar's dW).
+ * Besides the conventions above: `dtype` is PG_F32 or PG_BF16; ld_* is a row
+ * stride in elements, at least d (rows may be slices of wider ones, and
+ * pointers need no more than their element's alignment unless stated);
+ * nothing outside the d columns of the given rows is written; sums are fp32
+ * or wider and taken in a fixed order (no floating-point atomics), so equal
+ * calls give equal bits. Outputs overlap no input and no other output except
+ * where stated. Calls that may run at the same time need workspaces of their
+ * own, captured graphs that may replay at the same time too; a workspace
+ * holds nothing between calls.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * pg_embed -- out[t] = scale * T[tokens[t]], one fp32 product rounded once to
+ * out_dtype. Tokens outside [0, V), V = table->n_rows, give a zero row and
+ * set bit 0 of *dev_status (nullable).
+ *   table   PG_F32 or PG_BF16 data [V][d] (NF4: PG_EUNSUPPORTED); 1 <= d <=
+ *           16384 (wider: PG_EUNSUPPORTED)
+ *   tokens  int32 [n_tok] (device), n_tok < 2^26 (PG_ERANGE)
+ *   out     [n_tok] rows of d elements, stride ld_out
+ */
+PG_API int pg_embed(const pg_table* table, int32_t d, float scale,
+                    const int32_t* tokens, int64_t n_tok, int32_t out_dtype,
+                    void* out, int64_t ld_out, int32_t* dev_status,
+                    hipStream_t stream);
+
+/*
+ * pg_embed_workspace_size -- device workspace bytes of either gradient call
+ * (negative pg_status for unsupported sizes: those of pg_embed, and V < 2^31
+ * - 1).
+ */
+PG_API int64_t pg_embed_workspace_size(int64_t n_tok, int64_t V, int32_t d);
+
+/*
+ * pg_embed_backward -- the table gradient of pg_embed restricted to the rows
+ * the tokens touch, in pg_backward_scalar's form: urows int64 [*n_unique]
+ * ascending, ugrad fp32 [*n_unique][d] with
+ *   ugrad[u] = scale * sum over t with tokens[t] = urows[u] of dout[t],
+ * summed in fp32 over runs of tokens in token order, the runs then in order.
+ * Tokens outside [0, V) add nothing.
+ *   dout   [n_tok] rows of d elements of dtype, stride ld
+ *   urows / ugrad need room for min(n_tok, V) entries; what lies behind
+ *   *n_unique (a device int64) is left as it was
+ *   workspace of pg_embed_workspace_size bytes, 256-byte aligned
+ */
+PG_API int pg_embed_backward(const void* dout, int32_t dtype, int64_t ld,
+                             const int32_t* tokens, int64_t n_tok, int64_t V,
+                             int32_t d, float scale, int64_t* urows,
+                             float* ugrad, int64_t* n_unique, void* workspace,
+                             int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * pg_embed_backward_dense -- the same gradient as a dense table: dtable fp32
+ * [V][d] is written whole (zeros in untouched rows), or with accumulate = 1
+ * the gradient is added to the touched rows and the others are left alone.
+ */
+PG_API int pg_embed_backward_dense(const void* dout, int32_t dtype, int64_t ld,
+                                   const int32_t* tokens, int64_t n_tok,
+                                   int64_t V, int32_t d, float scale,
+                                   float* dtable, int32_t accumulate,
+                                   void* workspace, int64_t workspace_bytes,
+                                   hipStream_t stream);
+
+/*
+ * pg_layer_norm -- for each of n rows of d elements:
+ *   mu = mean(x), rstd = 1 / sqrt(mean((x - mu)^2) + eps),
+ *   y = (x - mu) rstd gamma + beta.
+ *   gamma fp32 [d]; beta fp32 [d], nullable (zero); mean, rstd fp32 [n],
+ *   nullable, what the backward pass takes; 1 <= d <= 16384
+ *   (PG_EUNSUPPORTED beyond); n <= 2^31; x and y of dtype. y may be x itself
+ *   (same stride).
+ */
+PG_API int pg_layer_norm(const void* x, int32_t dtype, int64_t n, int32_t d,
+                         int64_t ld_x, const float* gamma, const float* beta,
+                         float eps, void* y, int64_t ld_y, float* mean,
+                         float* rstd, hipStream_t stream);
+
+/* Device workspace bytes of pg_layer_norm_backward (negative pg_status). */
+PG_API int64_t pg_layer_norm_workspace_size(int64_t n, int32_t d);
+
+/*
+ * pg_layer_norm_backward -- gradients of pg_layer_norm's y given dy, with
+ * xh = (x - mean) rstd and g = gamma dy:
+ *   dx = rstd (g - mean(g) - xh mean(g xh)) + add     (rounded once)
+ *   dgamma fp32 [d] = sum over rows of dy xh
+ *   dbeta  fp32 [d] = sum over rows of dy              (nullable)
+ * add (nullable) is the gradient that reaches x past the norm, as in a
+ * residual stream. dy, x, add, dx of dtype; dx may be dy or add itself (same
+ * stride), not x. n = 0 writes zeros to dgamma and dbeta. workspace of
+ * pg_layer_norm_workspace_size bytes, 256-byte aligned.
+ */
+PG_API int pg_layer_norm_backward(const void* dy, int64_t ld_dy, const void* x,
+                                  int64_t ld_x, int32_t dtype, int64_t n,
+                                  int32_t d, const float* gamma,
+                                  const float* mean, const float* rstd,
+                                  const void* add, int64_t ld_add, void* dx,
+                                  int64_t ld_dx, float* dgamma, float* dbeta,
+                                  void* workspace, int64_t workspace_bytes,
+                                  hipStream_t stream);
+
+/* Device workspace bytes of pg_orthogonalize (negative pg_status). */
+PG_API int64_t pg_orthogonalize_workspace_size(int64_t n_mat, int32_t rows,
+                                               int32_t cols);
+
+/*
+ * pg_orthogonalize -- n_mat update matrices (gradients or their momentum) of
+ * rows x cols each, made near-orthogonal by Newton-Schulz products, for each
+ * one:
+ *   X = G / (||G||_F + eps), transposed if rows > cols; `steps` times
+ *   A = X X^T, X <- a X + (b A + c A A) X; out = scale X (transposed back).
+ * The usual coefficients are a = 3.4445, b = -4.7750, c = 2.0315 with 5
+ * steps. A zero matrix gives zeros, one with a NaN or an infinity gives NaN.
+ *   G    [n_mat][rows][cols] of dtype; out bf16 of the same shape
+ *   1 <= rows, cols <= 16384 (PG_EUNSUPPORTED beyond); n_mat <= 65535;
+ *   1 <= steps <= 64. The products run in fp16 with fp32 accumulation, the
+ *   iterate and the diagonals in fp32 (matrices small enough for one compute
+ *   unit's memory: all of it in fp32). Coefficients under which a singular
+ *   value in [0, 1] could pass 3 before a step, or b s^2 + c s^4 pass 100 in
+ *   magnitude, are refused (PG_EUNSUPPORTED).
+ *   workspace of pg_orthogonalize_workspace_size bytes, 256-byte aligned
+ */
+PG_API int pg_orthogonalize(const void* G, int32_t dtype, int64_t n_mat,
+                            int32_t rows, int32_t cols, int32_t steps, float a,
+                            float b, float c, float eps, float scale, void* out,
+                            void* workspace, int64_t workspace_bytes,
+                            hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Flash page-cache simulation (host code; PageGram tech report §2.3, §3.3,
  * §8 Fig. 4a and appendix D). A table kept on flash is read in 4 KiB blocks;
  * a RAM page cache with LRU replacement holds whole blocks; each lookup whose
