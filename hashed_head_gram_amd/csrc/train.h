@@ -103,7 +103,7 @@ struct EmbedPlan {
   int chunk;                  // sorted positions per reduction chunk
   int64_t nblk;               // blocks of a sort pass
   int64_t nchunk;
-  int64_t off_keys[2], off_vals[2], off_counts, off_totals, off_heads, off_part, off_present;
+  int64_t off_keys[2], off_vals[2], off_counts, off_totals, off_heads, off_part, off_list;
   int64_t bytes;
 };
 EmbedPlan embed_plan(int64_t n, int64_t V, int d);

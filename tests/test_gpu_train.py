@@ -120,6 +120,12 @@ ROWS = [  # n, V, d, dtype, pad, shift, tokens
     (5000, 3, 130, "f32", 0, 0, "one_row"), (1000, 10, 40, "bf16", 0, 0, "none"),
     (9000, 700, 1025, "bf16", 7, 0, "some"), (20000, 128000, 2560, "bf16", 0, 0, "zipf"),
     (70000, 100, 33, "f32", 0, 0, "zipf"), (3, 5, 16384, "f32", 0, 0, "two_rows"),
+    # both sides of each way to sort
+    (1024, 900, 16, "f32", 0, 0, "zipf"), (1025, 900, 100, "bf16", 0, 0, "some"),
+    (2048, 70000, 200, "f32", 0, 0, "zipf"), (4096, 70000, 96, "f32", 0, 0, "zipf"), (16384, 50304, 256, "bf16", 0, 0, "zipf"),
+    (65536, 300, 9, "f32", 0, 0, "some"), (65537, 128000, 20, "bf16", 0, 0, "zipf"),
+    (1 << 18, 512, 8, "bf16", 0, 0, "zipf"), ((1 << 18) + 1, 5000, 8, "f32", 0, 0, "some"),
+    (300000, 300000, 5, "f32", 0, 0, "distinct"), (270000, 2, 12, "bf16", 0, 0, "two_rows"),
 ]
 
 
