@@ -21,11 +21,29 @@
 namespace pg {
 namespace {
 
+// Sum over the group of L lanes, in every lane.
 template <int L>
 __device__ __forceinline__ float group_sum(float x) {
 #pragma unroll
   for (int s = L / 2; s >= 1; s >>= 1) x += __shfl_xor(x, s, 64);
   return x;
+}
+// A whole wave: six adds on the vector unit's own lane moves (four shifts in
+// rows of 16, two row broadcasts) leave the sum in lane 63.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float add_moved(float x) {
+  return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                           0, __builtin_bit_cast(int, x), CTRL, ROWS, 0xF, true));
+}
+template <>
+__device__ __forceinline__ float group_sum<64>(float x) {
+  x = add_moved<0x111, 0xF>(x);        // row_shr:1
+  x = add_moved<0x112, 0xF>(x);
+  x = add_moved<0x114, 0xF>(x);
+  x = add_moved<0x118, 0xF>(x);
+  x = add_moved<0x142, 0xA>(x);        // row_bcast:15 into rows 1 and 3
+  x = add_moved<0x143, 0xC>(x);        // row_bcast:31 into rows 2 and 3
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
 }
 
 // Threads of a block: one row's waves, or four waves of rows of their own.
@@ -111,10 +129,18 @@ __global__ __launch_bounds__(kNormThreads<W>) void norm_kernel(
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int left = d - (c0 + G::STEP * k);
+      if (left >= 8) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float t = i < left ? v[k].get(i) - mu : 0.f;
-        q += t * t;
+        for (int i = 0; i < 8; ++i) {
+          const float t = v[k].get(i) - mu;
+          q += t * t;
+        }
+      } else if (left > 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float t = i < left ? v[k].get(i) - mu : 0.f;
+          q += t * t;
+        }
       }
     }
     const float var = join(group_sum<L>(q), 1) / fd;
@@ -132,7 +158,7 @@ __global__ __launch_bounds__(kNormThreads<W>) void norm_kernel(
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = (v[k].get(i) - mu) * rs * g.v[i] + b.v[i];
-        store8(y + r * ldy + c, o, d - c);
+        store8<true>(y + r * ldy + c, o, d - c);
       }
     }
 #pragma unroll
@@ -171,9 +197,9 @@ __global__ __launch_bounds__(kNormThreads<W>) void norm_backward_kernel(
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int c = c0 + G::STEP * k, left = live ? d - c : 0;
-      v.x[k] = load8(x + rc * ldx + c, left);
-      v.y[k] = load8(dy + rc * lddy + c, left);
-      if constexpr (ADD) v.a[k] = load8(add + rc * ldadd + c, left);
+      v.x[k] = load8<true>(x + rc * ldx + c, left);
+      v.y[k] = load8<true>(dy + rc * lddy + c, left);
+      if constexpr (ADD) v.a[k] = load8<true>(add + rc * ldadd + c, left);
     }
   };
   Row v;
@@ -191,16 +217,21 @@ __global__ __launch_bounds__(kNormThreads<W>) void norm_backward_kernel(
     for (int k = 0; k < CH; ++k) {
       const int c = c0 + G::STEP * k;
       const Raw8<float> gm = staged(sg, c >> 3);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        // dy and gamma are zero behind the row's end, dy for rows past n;
-        // xh is finite there only if mu and rs are, so it is selected away
-        const float xh = c + i < d && live ? (v.x[k].get(i) - v.mu) * v.rs : 0.f;
+      auto take = [&](int i, float xh) {
         const float g = v.y[k].get(i) * gm.v[i];
         s1 += g;
         s2 += g * xh;
         ag[k][i] += v.y[k].get(i) * xh;
         ab[k][i] += v.y[k].get(i);
+      };
+      // dy and gamma are zero behind the row's end, dy for rows past n; xh is
+      // finite there only if mu and rs are, so it is selected away
+      if (c + 8 <= d && live) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) take(i, (v.x[k].get(i) - v.mu) * v.rs);
+      } else if (c < d && live) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) take(i, c + i < d ? (v.x[k].get(i) - v.mu) * v.rs : 0.f);
       }
     }
     s1 = group_sum<L>(s1);
@@ -233,7 +264,7 @@ __global__ __launch_bounds__(kNormThreads<W>) void norm_backward_kernel(
           o[i] = v.rs * (v.y[k].get(i) * gm.v[i] - m1 - xh * m2);
           if constexpr (ADD) o[i] += v.a[k].get(i);
         }
-        store8(dx + r * lddx + c, o, d - c);
+        store8<true>(dx + r * lddx + c, o, d - c);
       }
     }
     v = next;

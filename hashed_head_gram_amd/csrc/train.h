@@ -40,21 +40,48 @@ struct Raw8<uint16_t> {
 __device__ __forceinline__ float elt_f32(float x) { return x; }
 __device__ __forceinline__ float elt_f32(uint16_t x) { return bf16_to_f32(x); }
 
+// Part vectors move single elements, whole ones 16 bytes at a time. STREAM
+// marks data that this call touches once and that is larger than the caches
+// when speed matters: non-temporal stores and loads.
+typedef uint32_t u32v4_any __attribute__((ext_vector_type(4), aligned(2)));
+template <bool STREAM>
+__device__ __forceinline__ void load16(const void* p, uint32_t (&w)[4]) {
+  const auto* q = static_cast<const u32v4_any*>(p);
+  const u32v4_any v = STREAM ? __builtin_nontemporal_load(q) : *q;
+  w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+}
+template <bool STREAM>
+__device__ __forceinline__ void store16(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  auto* q = static_cast<u32v4_any*>(p);
+  const u32v4_any v = {a, b, c, d};
+  if constexpr (STREAM) __builtin_nontemporal_store(v, q);
+  else *q = v;
+}
+
 // p[0 .. min(8, left)) with zeros behind; left <= 0 reads nothing.
+template <bool STREAM = false>
 __device__ __forceinline__ Raw8<float> load8(const float* p, int left) {
   Raw8<float> r;
   if (left >= 8) {
-    __builtin_memcpy(r.v, p, 32);
+    uint32_t a[4], b[4];
+    load16<STREAM>(p, a);
+    load16<STREAM>(p + 4, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.v[i] = __uint_as_float(a[i]);
+      r.v[4 + i] = __uint_as_float(b[i]);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) r.v[i] = i < left ? p[i] : 0.f;
   }
   return r;
 }
+template <bool STREAM = false>
 __device__ __forceinline__ Raw8<uint16_t> load8(const uint16_t* p, int left) {
   Raw8<uint16_t> r;
   if (left >= 8) {
-    __builtin_memcpy(r.w, p, 16);
+    load16<STREAM>(p, r.w);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -67,21 +94,26 @@ __device__ __forceinline__ Raw8<uint16_t> load8(const uint16_t* p, int left) {
 }
 
 // p[0 .. min(8, left)) = x, rounded to nearest even for bf16.
+template <bool STREAM = false>
 __device__ __forceinline__ void store8(float* p, const float (&x)[8], int left) {
   if (left >= 8) {
-    __builtin_memcpy(p, x, 32);
+#pragma unroll
+    for (int i = 0; i < 8; i += 4)
+      store16<STREAM>(p + i, __float_as_uint(x[i]), __float_as_uint(x[i + 1]),
+                      __float_as_uint(x[i + 2]), __float_as_uint(x[i + 3]));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < left) p[i] = x[i];
   }
 }
+template <bool STREAM = false>
 __device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8], int left) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = pack2_bf16(x[2 * i], x[2 * i + 1]);
   if (left >= 8) {
-    __builtin_memcpy(p, w, 16);
+    store16<STREAM>(p, w[0], w[1], w[2], w[3]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
