@@ -355,7 +355,9 @@ void with_geometry(int d, F f) {
 }
 
 // Blocks that walk n rows: enough to fill the chip's 256 compute units
-// `waves` waves deep, no more than there are rows.
+// `waves` waves deep, no more than there are rows. 131,072 rows of 2,560 bf16:
+// forward 296, 264 and 316 us at 15, 20 and 30 waves, backward 511, 490, 512
+// and 542 us at 10, 15, 20 and 30.
 template <int L, int W>
 int64_t norm_blocks(int64_t n, int waves) {
   constexpr int NT = kNormThreads<W>;
@@ -363,7 +365,7 @@ int64_t norm_blocks(int64_t n, int waves) {
   const int64_t need = (n + ROWS - 1) / ROWS, cap = 256 * (int64_t)(waves * 64 / NT);
   return need < cap ? need : cap;
 }
-constexpr int kForwardWaves = 32, kBackwardWaves = 20;
+constexpr int kForwardWaves = 20, kBackwardWaves = 15;
 
 }  // namespace
 

@@ -18,6 +18,21 @@
 //     from overflow for every iterate the entry point admits (singular values
 //     at most 3, |b s^2 + c s^4| at most 100) and with subnormals below 2^-33.
 // bf16 operands, the usual choice, would be eight times coarser.
+//
+// A and B are symmetric: only tiles on and below the diagonal are computed,
+// the others are their mirror images. The products run as tiles of P Q^T with
+// both operands K-contiguous: A = Xh Xh^T, O O^T, and F Yh^T with Yh the
+// transpose of Xh, which the update writes beside it.
+//
+// The tile kernel: K advances 64 at a time through an LDS ring filled by
+// direct global-to-LDS loads, rows swizzled so that fragment reads meet no
+// bank conflicts; v_mfma_f32_32x32x16_f16, with the Q fragment as its A
+// operand, so a lane's accumulators are runs of four consecutive columns of
+// one row. The epilogue works on the accumulators where they are: rows leave
+// as 16-byte stores after one exchange between the half waves, transposed
+// ones as 8-byte stores after a 4 x 4 transpose inside quads of lanes.
+#include <type_traits>
+
 #include "train.h"
 
 namespace pg {
@@ -25,7 +40,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPad = 128;                 // padded sides are multiples of this
-constexpr int kNormBlocks = 64;
+constexpr int kNormBlocks = 256;           // most partial sums of a matrix's norm
 constexpr float kSX = 1024.f, kSO = 4096.f, kSF = 512.f;   // fp16 placements
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -33,6 +48,18 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ float g_at(const float* G, int64_t i) { return G[i]; }
 __device__ __forceinline__ float g_at(const uint16_t* G, int64_t i) { return bf16_to_f32(G[i]); }
+
+// Sum over the block in a fixed order, in every thread.
+__device__ __forceinline__ double block_sum(double s, double* sh) {
+  sh[threadIdx.x] = s;
+  __syncthreads();
+#pragma unroll
+  for (int o = kThreads / 2; o >= 1; o >>= 1) {
+    if ((int)threadIdx.x < o) sh[threadIdx.x] += sh[threadIdx.x + o];
+    __syncthreads();
+  }
+  return sh[0];
+}
 
 // Sum of squares of matrix blockIdx.y in double (no overflow for any fp32
 // input), one partial per block.
@@ -42,18 +69,18 @@ __global__ __launch_bounds__(kThreads) void ns_norm_kernel(const T* __restrict__
   __shared__ double sh[kThreads];
   const T* g = G + (int64_t)blockIdx.y * count;
   double s = 0.0;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < count;
-       i += (int64_t)gridDim.x * kThreads) {
-    const double v = (double)g_at(g, i);
-    s += v * v;
+  const int64_t step = (int64_t)gridDim.x * kThreads * 8;
+#pragma unroll 4
+  for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8; i < count; i += step) {
+    const Raw8<T> x = load8(g + i, (int)(count - i < 8 ? count - i : 8));
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const double v = (double)x.get(u);
+      s += v * v;
+    }
   }
-  sh[threadIdx.x] = s;
-  __syncthreads();
-  for (int o = kThreads / 2; o >= 1; o >>= 1) {
-    if (threadIdx.x < o) sh[threadIdx.x] += sh[threadIdx.x + o];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = sh[0];
+  s = block_sum(s, sh);
+  if (threadIdx.x == 0) part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
 }
 
 // X, its fp16 copy and the copy's transpose from G, 64 x 64 tiles of X with
@@ -64,9 +91,9 @@ __global__ __launch_bounds__(kThreads) void ns_load_kernel(
     float eps, int mp, int np, float* __restrict__ X, _Float16* __restrict__ Xh,
     _Float16* __restrict__ Yh) {
   __shared__ float t[64][65];
+  __shared__ double sh[kThreads];
   const int64_t mat = blockIdx.z;
-  double s = 0.0;
-  for (int q = 0; q < parts; ++q) s += part[mat * parts + q];
+  const double s = block_sum((int)threadIdx.x < parts ? part[mat * parts + threadIdx.x] : 0.0, sh);
   const double inv = s == 0.0 ? 0.0 : 1.0 / (sqrt(s) + (double)eps);
   const T* g = G + mat * rows * cols;
   const bool tall = rows > cols;                 // X = G^T
@@ -98,6 +125,8 @@ struct NsArgs {
   const _Float16* P;      // left operand rows, K contiguous
   const _Float16* Q;      // right operand rows, K contiguous
   int K, mp, np;
+  int tiles;              // tiles of one matrix
+  int cols_t;             // update: tiles along a row
   float a, b, c, scale;
   float* X;               // fp32 iterate [mp][np]
   _Float16 *Xh, *Yh;      // next copies (update)
@@ -109,71 +138,295 @@ struct NsArgs {
   int rows, cols;
 };
 
-// 64 x 64 tile of P Q^T, four waves of one 32 x 32 block each.
-template <int MODE>
-__global__ __launch_bounds__(kThreads) void ns_gemm_kernel(NsArgs g) {
-  __shared__ __attribute__((aligned(16))) _Float16 sp[64][72], sq[64][72];
-  const int64_t mat = blockIdx.z;
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+// s_waitcnt with only a vmcnt limit (vmcnt[3:0], expcnt[6:4], lgkmcnt[11:8],
+// vmcnt[5:4] in bits [15:14]).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
+// Direct global-to-LDS load: each lane moves 16 bytes from base + off; the
+// wave writes 1 KiB at LDS address lds + 16 lane. No memory clobber: the ring
+// orders it with counted waits and barriers.
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds));
+}
+
+__device__ __forceinline__ void ring_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)a) |
+         ((uint32_t)__builtin_bit_cast(uint16_t, (_Float16)b) << 16);
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t quad_move(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
+}
+
+// 4 x 4 transpose of 16-bit values inside quads of lanes: lane q holds its
+// row's columns 0..3 as (lo, hi) pairs and gets column q of rows 0..3.
+__device__ __forceinline__ uint2 quad_transpose(uint32_t lo, uint32_t hi, int lane) {
+  const uint32_t nl = quad_move<0xB1>(lo), nh = quad_move<0xB1>(hi);   // lane ^ 1
+  const bool odd = lane & 1;
+  const uint32_t l = odd ? (nl >> 16) | (lo & 0xFFFF0000u) : (lo & 0xFFFFu) | (nl << 16);
+  const uint32_t h = odd ? (nh >> 16) | (hi & 0xFFFF0000u) : (hi & 0xFFFFu) | (nh << 16);
+  const uint32_t fl = quad_move<0x4E>(l), fh = quad_move<0x4E>(h);     // lane ^ 2
+  return (lane & 2) ? make_uint2(fh, h) : make_uint2(l, fl);
+}
+
+// The 16 accumulators of one lane of a 32 x 32 tile, as 16-bit pairs
+// w[g][0..1]: row lane % 32, columns 8 g + 4 (lane / 32) + 0..3.
+struct Tile16 {
+  uint32_t w[4][2];
+};
+
+// dst[row][col..]: 16-byte stores, two 32-byte runs a row. ld in elements.
+__device__ __forceinline__ void store_rows(uint16_t* dst, int64_t ld, const Tile16& t, int lane) {
+#pragma unroll
+  for (int g = 0; g < 4; g += 2) {
+    // lanes below 32 get columns 8 g .. 8 g + 7, the others the next eight
+    const auto a = __builtin_amdgcn_permlane32_swap(t.w[g][0], t.w[g + 1][0], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(t.w[g][1], t.w[g + 1][1], false, false);
+    *reinterpret_cast<uint4*>(dst + (lane & 31) * ld + 8 * g + 8 * (lane >> 5)) =
+        make_uint4(a[0], b[0], a[1], b[1]);
+  }
+}
+
+// dst[col][row..]: 8-byte stores, 64-byte runs a column.
+__device__ __forceinline__ void store_cols(uint16_t* dst, int64_t ld, const Tile16& t, int lane) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const uint2 v = quad_transpose(t.w[g][0], t.w[g][1], lane);
+    const int c = 8 * g + 4 * (lane >> 5) + (lane & 3);
+    *reinterpret_cast<uint2*>(dst + c * ld + (lane & 28)) = v;
+  }
+}
+
+// BM x BN tile of P Q^T by WM x WN waves, S stages of 64 in the ring.
+template <int MODE, int BM, int BN, int WM, int WN, int S>
+__global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
+  constexpr int NW = WM * WN;
+  constexpr int TM = BM / WM, TN = BN / WN;          // a wave's part
+  constexpr int FM = TM / 32, FN = TN / 32;
+  constexpr int PL = BM / 8 / NW, QL = BN / 8 / NW;  // loads of 8 rows a wave and stage
+  constexpr int L = PL + QL;
+  constexpr int kStage = (BM + BN) * 128;
+  static_assert(PL >= 1 && QL >= 1 && TM % 32 == 0 && TN % 32 == 0 && (S - 1) * L < 64, "tile");
+  static_assert(MODE == NS_UPDATE || BM == BN, "mirrored tiles are square");
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[S * kStage];
+
+  // consecutive tiles run on one of the 8 XCDs and share operands in its L2
+  const int64_t total = gridDim.x, per = total / 8;
+  int64_t id = blockIdx.x;
+  if (id < per * 8) id = (id & 7) * per + (id >> 3);
+  const int64_t mat = id / g.tiles;
+  const int t = (int)(id - mat * g.tiles);
+  int bi, bj;
+  if constexpr (MODE == NS_UPDATE) {
+    bi = t / g.cols_t;
+    bj = t - bi * g.cols_t;
+  } else {                                           // t = bi (bi + 1) / 2 + bj, bj <= bi
+    bi = (int)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
+    while (bi * (bi + 1) / 2 > t) --bi;
+    while ((bi + 1) * (bi + 2) / 2 <= t) ++bi;
+    bj = t - bi * (bi + 1) / 2;
+  }
+  const int i0 = bi * BM, j0 = bj * BN;
   const int64_t mm = mat * g.mp * g.mp, mn = mat * g.mp * g.np;
-  const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
-  const int K = g.K;
-  const _Float16* P = g.P + (MODE == NS_GRAM ? mn : mm) + (int64_t)i0 * K;
-  const _Float16* Q = g.Q + (MODE == NS_POLY ? mm : mn) + (int64_t)j0 * K;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wi = (wave >> 1) * 32, wj = (wave & 1) * 32;
-  f32x16_t acc = {};
-  for (int k0 = 0; k0 < K; k0 += 64) {
-    __syncthreads();
+  const int64_t K = g.K;
+  const auto* P = reinterpret_cast<const uint8_t*>(g.P + (MODE == NS_GRAM ? mn : mm) + i0 * K);
+  const auto* Q = reinterpret_cast<const uint8_t*>(g.Q + (MODE == NS_POLY ? mm : mn) + j0 * K);
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wm = wave / WN, wn = wave % WN;
+
+  // A stage's row is 128 bytes, eight 16-byte chunks, chunk c at position
+  // c ^ ((row / 2) % 8): the 16 lanes a 16-byte read serves together then
+  // touch 16 different slots of a 256-byte line. A load covers 8 rows.
+  const int dr = lane >> 3;
+  const uint32_t chunk = (uint32_t)(((lane & 7) ^ (dr >> 1)) * 16);
+  const uint32_t ring0 = (uint32_t)(uintptr_t)(const lds_void_t*)ring;
+  auto issue = [&](int kt) {
+    const uint32_t at = ring0 + (kt % S) * kStage;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int e = threadIdx.x + q * kThreads, r = e >> 3, c = (e & 7) * 8;
-      *reinterpret_cast<uint4*>(&sp[r][c]) =
-          *reinterpret_cast<const uint4*>(P + (int64_t)r * K + k0 + c);
-      *reinterpret_cast<uint4*>(&sq[r][c]) =
-          *reinterpret_cast<const uint4*>(Q + (int64_t)r * K + k0 + c);
+    for (int q = 0; q < PL; ++q) {
+      const int grp = wave * PL + q;
+      load_to_lds(P + (grp * 8 * K + kt * 64) * 2,
+                  (uint32_t)(dr * K * 2) + (chunk ^ (uint32_t)((grp & 1) * 64)), at + grp * 1024);
     }
-    __syncthreads();
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int kc = s * 16 + 8 * (lane >> 5);
-      const f16x8_t pf = *reinterpret_cast<const f16x8_t*>(&sp[wi + (lane & 31)][kc]);
-      const f16x8_t qf = *reinterpret_cast<const f16x8_t*>(&sq[wj + (lane & 31)][kc]);
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(pf, qf, acc, 0, 0, 0);
+    for (int q = 0; q < QL; ++q) {
+      const int grp = wave * QL + q;
+      load_to_lds(Q + (grp * 8 * K + kt * 64) * 2,
+                  (uint32_t)(dr * K * 2) + (chunk ^ (uint32_t)((grp & 1) * 64)),
+                  at + BM * 128 + grp * 1024);
+    }
+  };
+  const int fr = lane & 31;
+  auto frags = [&](int kt, int st, f16x8_t (&pf)[FM], f16x8_t (&qf)[FN]) {
+    const uint8_t* sp = ring + (kt % S) * kStage;
+    const uint8_t* sq = sp + BM * 128;
+    const int c = ((st * 2 + (lane >> 5)) ^ ((fr >> 1) & 7)) * 16;
+#pragma unroll
+    for (int a = 0; a < FM; ++a)
+      pf[a] = *reinterpret_cast<const f16x8_t*>(sp + (wm * TM + a * 32 + fr) * 128 + c);
+#pragma unroll
+    for (int b = 0; b < FN; ++b)
+      qf[b] = *reinterpret_cast<const f16x8_t*>(sq + (wn * TN + b * 32 + fr) * 128 + c);
+  };
+
+  f32x16_t acc[FM][FN] = {};
+  const int KT = (int)(K / 64);
+  constexpr int PD = S - 1;                          // stages in flight
+#pragma unroll
+  for (int st = 0; st < PD; ++st)
+    if (st < KT) issue(st);
+  for (int kt = 0; kt < KT; ++kt) {
+    // stage kt has landed when at most the later issued ones are outstanding;
+    // behind the barrier every wave is done with stage kt - 1, whose place
+    // stage kt + PD takes
+    const int later = KT - 1 - kt < PD - 1 ? KT - 1 - kt : PD - 1;
+    if (PD >= 3 && later >= 2) wait_loads<PD >= 3 ? 2 * L : 0>();
+    else if (PD >= 2 && later >= 1) wait_loads<PD >= 2 ? L : 0>();
+    else wait_loads<0>();
+    ring_barrier();
+    if (kt + PD < KT) issue(kt + PD);
+    f16x8_t pf[2][FM], qf[2][FN];
+    frags(kt, 0, pf[0], qf[0]);
+#pragma unroll
+    for (int st = 0; st < 4; ++st) {
+      if (st < 3) frags(kt, st + 1, pf[(st + 1) & 1], qf[(st + 1) & 1]);
+#pragma unroll
+      for (int a = 0; a < FM; ++a)
+#pragma unroll
+        for (int b = 0; b < FN; ++b)
+          acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(qf[st & 1][b], pf[st & 1][a],
+                                                             acc[a][b], 0, 0, 0);
     }
   }
+
+  // Epilogue, one 32 x 32 tile after the other.
+  const int half = lane >> 5;
 #pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    const int i = i0 + wi + 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3);
-    const int j = j0 + wj + (lane & 31);
-    if constexpr (MODE == NS_GRAM) {
-      const float v = acc[q] * (1.f / (kSX * kSX));
-      g.O[mm + (int64_t)i * g.mp + j] = (_Float16)(i == j ? 0.f : v * kSO);
-      if (i == j) g.D[mat * g.mp + i] = v;
-    } else if constexpr (MODE == NS_POLY) {
-      const float aa = acc[q] * (1.f / (kSO * kSO));
-      const float di = g.D[mat * g.mp + i], dj = g.D[mat * g.mp + j];
-      const float o = (float)g.O[mm + (int64_t)i * g.mp + j] * (1.f / kSO);
-      const float f = (g.b + g.c * (di + dj)) * o + g.c * aa;
-      g.F[mm + (int64_t)i * g.mp + j] = (_Float16)(i == j ? 0.f : f * kSF);
-      if (i == j) g.E[mat * g.mp + i] = g.b * di + g.c * (aa + di * di);
-    } else {
-      const int64_t at = mn + (int64_t)i * g.np + j;
-      const float x = (g.a + g.E[mat * g.mp + i]) * g.X[at] + acc[q] * (1.f / (kSF * kSX));
-      if (g.out) {
-        const bool tall = g.rows > g.cols;
-        const int r = tall ? j : i, c = tall ? i : j;
-        if (r < g.rows && c < g.cols)
-          g.out[(mat * g.rows + r) * g.cols + c] = (uint16_t)pack2_bf16(g.scale * x, 0.f);
+  for (int a = 0; a < FM; ++a) {
+    const int ib = i0 + wm * TM + a * 32, i = ib + fr;
+    float di = 0.f;
+    if constexpr (MODE == NS_POLY) di = g.D[mat * g.mp + i];
+    if constexpr (MODE == NS_UPDATE) di = g.a + g.E[mat * g.mp + i];
+#pragma unroll
+    for (int b = 0; b < FN; ++b) {
+      const int jb = j0 + wn * TN + b * 32;
+      Tile16 w;
+      if constexpr (MODE == NS_GRAM) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const int j = jb + 8 * (q >> 2) + 4 * half + (q & 3);
+          if (i == j) {
+            g.D[mat * g.mp + i] = acc[a][b][q] * (1.f / (kSX * kSX));
+            acc[a][b][q] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            w.w[q][u] = pack_half(acc[a][b][4 * q + 2 * u] * (kSO / (kSX * kSX)),
+                                  acc[a][b][4 * q + 2 * u + 1] * (kSO / (kSX * kSX)));
+      } else if constexpr (MODE == NS_POLY) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int jq = jb + 8 * q + 4 * half;
+          const uint2 ow = *reinterpret_cast<const uint2*>(g.O + mm + (int64_t)i * g.mp + jq);
+          const float4 dj = *reinterpret_cast<const float4*>(g.D + mat * g.mp + jq);
+          const float djs[4] = {dj.x, dj.y, dj.z, dj.w};
+          float f[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t bits = ((u & 2) ? ow.y : ow.x) >> (16 * (u & 1));
+            const float o = (float)__builtin_bit_cast(_Float16, (uint16_t)bits) * (1.f / kSO);
+            const float aa = acc[a][b][4 * q + u] * (1.f / (kSO * kSO));
+            f[u] = ((g.b + g.c * (di + djs[u])) * o + g.c * aa) * kSF;
+            if (i == jq + u) {
+              g.E[mat * g.mp + i] = g.b * di + g.c * (aa + di * di);
+              f[u] = 0.f;
+            }
+          }
+          w.w[q][0] = pack_half(f[0], f[1]);
+          w.w[q][1] = pack_half(f[2], f[3]);
+        }
       } else {
-        g.X[at] = x;
-        g.Xh[at] = (_Float16)(x * kSX);
-        g.Yh[mn + (int64_t)j * g.mp + i] = (_Float16)(x * kSX);
+        float* X = g.X + mn + (int64_t)i * g.np;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int jq = jb + 8 * q + 4 * half;
+          const float4 x = *reinterpret_cast<const float4*>(X + jq);
+          const float y[4] = {di * x.x + acc[a][b][4 * q] * (1.f / (kSF * kSX)),
+                              di * x.y + acc[a][b][4 * q + 1] * (1.f / (kSF * kSX)),
+                              di * x.z + acc[a][b][4 * q + 2] * (1.f / (kSF * kSX)),
+                              di * x.w + acc[a][b][4 * q + 3] * (1.f / (kSF * kSX))};
+          if (g.out) {                               // bf16 result, no more copies
+            w.w[q][0] = pack2_bf16(g.scale * y[0], g.scale * y[1]);
+            w.w[q][1] = pack2_bf16(g.scale * y[2], g.scale * y[3]);
+          } else {
+            *reinterpret_cast<float4*>(X + jq) = make_float4(y[0], y[1], y[2], y[3]);
+            w.w[q][0] = pack_half(y[0] * kSX, y[1] * kSX);
+            w.w[q][1] = pack_half(y[2] * kSX, y[3] * kSX);
+          }
+        }
+      }
+      if constexpr (MODE == NS_UPDATE) {
+        if (g.out) {
+          // rows x cols without padding: X or, for a tall matrix, its transpose
+          const bool tall = g.rows > g.cols;
+          uint16_t* o = g.out + mat * g.rows * g.cols;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint2 v = make_uint2(w.w[q][0], w.w[q][1]);
+            int r = i, c = jb + 8 * q + 4 * half;
+            if (tall) {
+              v = quad_transpose(v.x, v.y, lane);
+              r = c + (lane & 3);
+              c = ib + (lane & 28);
+            }
+            if (r >= g.rows) continue;
+            uint16_t* dst = o + (int64_t)r * g.cols + c;
+            if (c + 4 <= g.cols) {
+              __builtin_memcpy(dst, &v, 8);
+            } else {
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (c + u < g.cols)
+                  dst[u] = (uint16_t)(((u & 2) ? v.y : v.x) >> (16 * (u & 1)));
+            }
+          }
+        } else {
+          store_rows(reinterpret_cast<uint16_t*>(g.Xh + mn + (int64_t)ib * g.np + jb), g.np, w,
+                     lane);
+          store_cols(reinterpret_cast<uint16_t*>(g.Yh + mn + (int64_t)jb * g.mp + ib), g.mp, w,
+                     lane);
+        }
+      } else {
+        _Float16* m = (MODE == NS_GRAM ? g.O : g.F) + mm;
+        store_rows(reinterpret_cast<uint16_t*>(m + (int64_t)ib * g.mp + jb), g.mp, w, lane);
+        if (bi != bj)                                // the mirrored tile
+          store_cols(reinterpret_cast<uint16_t*>(m + (int64_t)jb * g.mp + ib), g.mp, w, lane);
       }
     }
   }
 }
 
 int64_t al(int64_t x) { return (x + 255) / 256 * 256; }
+
+template <int V>
+using IC = std::integral_constant<int, V>;
 
 }  // namespace
 
@@ -183,7 +436,8 @@ OrthoPlan ortho_plan(int64_t n_mat, int64_t rows, int64_t cols) {
   p.n = (int)(rows < cols ? cols : rows);
   p.mp = (p.m + kPad - 1) / kPad * kPad;
   p.np = (p.n + kPad - 1) / kPad * kPad;
-  p.norm_blocks = kNormBlocks;
+  const int64_t need = (rows * cols + kThreads * 32 - 1) / (kThreads * 32);
+  p.norm_blocks = (int)(need < kNormBlocks ? need : kNormBlocks);
   const int64_t mn = n_mat * p.mp * p.np, mm = n_mat * p.mp * p.mp;
   int64_t off = 0;
   p.off_norm = off; off += al(n_mat * p.norm_blocks * 8);
@@ -222,7 +476,29 @@ hipError_t launch_orthogonalize(const OrthoPlan& p, const void* G, int32_t dtype
   };
   if (dtype == PG_F32) load(static_cast<const float*>(G));
   else load(static_cast<const uint16_t*>(G));
-  const dim3 sq((unsigned)(p.mp / 64), (unsigned)(p.mp / 64), nm);
+  // Tile of a product with at most `tiles(B)` tiles of B x B a matrix: the
+  // largest that still gives the chip's 256 compute units about a tile each.
+  // Larger tiles read their operands less often, smaller ones start more work
+  // at once.
+  auto launch = [&](auto MODE, const NsArgs& args) {
+    NsArgs g = args;
+    auto tiles = [&](int B) {
+      const int64_t ti = p.mp / B, tj = (MODE() == NS_UPDATE ? p.np : p.mp) / B;
+      return MODE() == NS_UPDATE ? ti * tj : ti * (ti + 1) / 2;
+    };
+    auto go = [&](auto B, auto WM, auto WN, auto S) {
+      g.tiles = (int)tiles(B());
+      g.cols_t = p.np / B();
+      hipLaunchKernelGGL((ns_tile_kernel<MODE(), B(), B(), WM(), WN(), S()>),
+                         dim3((unsigned)(n_mat * g.tiles)), dim3(64 * WM() * WN()), 0, s, g);
+    };
+    if (p.mp % 256 == 0 && p.np % 256 == 0 && n_mat * tiles(256) >= 192)
+      go(IC<256>{}, IC<2>{}, IC<4>{}, IC<2>{});
+    else if (n_mat * tiles(128) >= 192)
+      go(IC<128>{}, IC<2>{}, IC<2>{}, IC<2>{});
+    else
+      go(IC<64>{}, IC<2>{}, IC<2>{}, IC<4>{});
+  };
   for (int k = 0; k < oa.steps; ++k) {
     NsArgs g{};
     g.mp = p.mp; g.np = p.np;
@@ -230,12 +506,12 @@ hipError_t launch_orthogonalize(const OrthoPlan& p, const void* G, int32_t dtype
     g.X = X; g.Xh = Xh; g.O = O; g.D = D; g.F = F; g.E = E;
     g.rows = rows; g.cols = cols;
     g.P = Xh; g.Q = Xh; g.K = p.np;
-    hipLaunchKernelGGL(ns_gemm_kernel<NS_GRAM>, sq, block, 0, s, g);
+    launch(IC<NS_GRAM>{}, g);
     g.P = O; g.Q = O; g.K = p.mp;
-    hipLaunchKernelGGL(ns_gemm_kernel<NS_POLY>, sq, block, 0, s, g);
+    launch(IC<NS_POLY>{}, g);
     g.P = F; g.Q = Yh[k & 1]; g.Yh = Yh[(k + 1) & 1];
     g.out = k + 1 == oa.steps ? out : nullptr;
-    hipLaunchKernelGGL(ns_gemm_kernel<NS_UPDATE>, lgrid, block, 0, s, g);
+    launch(IC<NS_UPDATE>{}, g);
   }
   return hipGetLastError();
 }

@@ -367,7 +367,10 @@ def test_layer_norm_empty_constant_and_non_finite():
 ORTHO = [(1, 1, 1, "f32"), (2, 1, 9, "f32"), (1, 5, 3, "bf16"), (3, 16, 16, "f32"),
          (1, 64, 128, "f32"), (2, 100, 37, "bf16"), (1, 129, 130, "f32"), (1, 257, 128, "bf16"),
          (2, 200, 333, "f32"), (1, 520, 390, "f32"), (1, 640, 1000, "bf16"), (5, 96, 160, "f32"),
-         (1, 24, 700, "f32"), (1, 1500, 130, "f32")]
+         (1, 24, 700, "f32"), (1, 1500, 130, "f32"),
+         # enough matrices for the larger tiles
+         (200, 256, 256, "bf16"), (64, 256, 200, "f32"), (50, 300, 384, "bf16"),
+         (65, 250, 500, "f32")]
 
 
 def spectrum(rng, n, r, c):
@@ -405,8 +408,10 @@ def check_ortho(got, G, steps=5, coef=COEF, eps=1e-7, scale=1.0):
 def test_orthogonalize(n, r, c, dt):
     print(f"[orthogonalize] {n} {r} {c} {dt}", flush=True)
     G = to(spectrum(np.random.default_rng(r + c), n, r, c) * 1e-3, dt)
-    check_ortho(ortho(G), G)
-    assert torch.equal(ortho(G), ortho(G))
+    out = ortho(G)
+    some = sorted({0, n // 2, n - 1}) if n > 5 else range(n)
+    check_ortho(out[list(some)], G[list(some)])
+    assert bool(torch.isfinite(out).all()) and torch.equal(ortho(G), out)
 
 
 @pytest.mark.parametrize("shape", [(40, 70), (200, 150)])
