@@ -446,33 +446,41 @@ def pg_row_rms_flush(layout, table, vhat, last_step, step, lr, beta2=0.95, weigh
 
 
 def _dtype(fn, name, t):
-    import torch
-    if t.dtype == torch.bfloat16:
-        return PG_BF16
-    if t.dtype == torch.float32:
-        return PG_F32
-    raise ValueError(f"{fn}: {name} is {t.dtype}, not float32 or bfloat16")
+    code = _dtype_codes().get(t.dtype)
+    if code is None:
+        raise ValueError(f"{fn}: {name} is {t.dtype}, not float32 or bfloat16")
+    return code
+
+
+_codes = {}
+
+
+def _dtype_codes():
+    if not _codes:
+        import torch
+        _codes.update({torch.float32: PG_F32, torch.bfloat16: PG_BF16})
+    return _codes
 
 
 def _rows(fn, name, t):
     """(rows, row stride) of t, whose last dimension is a row."""
-    d = t.shape[-1]
     if t.dim() != 2:
         try:
-            t = t.view(-1, d)
-        except RuntimeError:
+            t = t.view(-1, t.shape[-1])
+        except (RuntimeError, IndexError):
             raise ValueError(f"{fn}: the rows of {name} have no single stride") from None
-    n = t.shape[0]
-    if n and d > 1 and t.stride(1) != 1:
+    n, d = t.shape
+    ld, one = t.stride()
+    if one != 1 and d > 1 and n:
         raise ValueError(f"{fn}: the rows of {name} are not contiguous")
-    return n, t.stride(0) if n > 1 else d
+    return n, ld if n > 1 else d
 
 
 def _flat(fn, name, t, dtype, size, dev, at_least=False):
     """t is contiguous, of dtype, with size elements, on dev."""
     n = t.numel()
-    if t.dtype != dtype or t.device != dev or not t.is_contiguous() or \
-            (n < size if at_least else n != size):
+    if (n != size and not (at_least and n > size)) or t.dtype != dtype or t.device != dev or \
+            not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of {size} elements "
                          f"on {dev}")
 
@@ -490,13 +498,19 @@ def _gpu(fn, name, t):
 
 
 def _call(fn, dev, stream, *args):
+    """fn(*args, stream) with dev the current device; without a stream, on dev's current one
+    (its raw handle: building a torch.cuda.Stream takes longer than a small kernel's launch)."""
     import torch
-    f = getattr(lib(), fn)
-    if dev.index == torch.cuda.current_device():
-        _check(fn, f(*args, _stream(stream)))
-        return
-    with torch.cuda.device(dev):
-        _check(fn, f(*args, _stream(stream)))
+    f = getattr(_lib or lib(), fn)
+    index = dev.index
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    if index == torch._C._cuda_getDevice():
+        status = f(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, raw)
+    if status != PG_OK:
+        raise PagegramError(fn, status)
 
 
 def _size(fn, *args):

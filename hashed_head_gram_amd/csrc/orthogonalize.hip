@@ -119,6 +119,12 @@ __global__ __launch_bounds__(kThreads) void ns_load_kernel(
   }
 }
 
+#ifndef UPD256
+#define UPD256 0
+#endif
+#ifndef UPD128
+#define UPD128 0
+#endif
 enum { NS_GRAM, NS_POLY, NS_UPDATE };
 
 struct NsArgs {
@@ -218,9 +224,10 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
   constexpr int FM = TM / 32, FN = TN / 32;
   constexpr int PL = BM / 8 / NW, QL = BN / 8 / NW;  // loads of 8 rows a wave and stage
   constexpr int L = PL + QL;
+  constexpr int R = BM / BN;                         // tiles of a diagonal block
   constexpr int kStage = (BM + BN) * 128;
   static_assert(PL >= 1 && QL >= 1 && TM % 32 == 0 && TN % 32 == 0 && (S - 1) * L < 64, "tile");
-  static_assert(MODE == NS_UPDATE || BM == BN, "mirrored tiles are square");
+  static_assert(MODE == NS_UPDATE || BM == BN || BM == 2 * BN, "mirrored tiles");
   __shared__ __attribute__((aligned(1024))) uint8_t ring[S * kStage];
 
   // consecutive tiles run on one of the 8 XCDs and share operands in its L2
@@ -233,11 +240,12 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
   if constexpr (MODE == NS_UPDATE) {
     bi = t / g.cols_t;
     bj = t - bi * g.cols_t;
-  } else {                                           // t = bi (bi + 1) / 2 + bj, bj <= bi
-    bi = (int)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
-    while (bi * (bi + 1) / 2 > t) --bi;
-    while ((bi + 1) * (bi + 2) / 2 <= t) ++bi;
-    bj = t - bi * (bi + 1) / 2;
+  } else {                                           // row bi has R (bi + 1) tiles
+    const int h = t / R;
+    bi = (int)((sqrtf(8.f * (float)h + 1.f) - 1.f) * 0.5f);
+    while (bi * (bi + 1) / 2 > h) --bi;
+    while ((bi + 1) * (bi + 2) / 2 <= h) ++bi;
+    bj = t - R * (bi * (bi + 1) / 2);
   }
   const int i0 = bi * BM, j0 = bj * BN;
   const int64_t mm = mat * g.mp * g.mp, mn = mat * g.mp * g.np;
@@ -247,6 +255,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = wave / WN, wn = wave % WN;
+  const int fr = lane & 31;
 
   // A stage's row is 128 bytes, eight 16-byte chunks, chunk c at position
   // c ^ ((row / 2) % 8): the 16 lanes a 16-byte read serves together then
@@ -270,7 +279,6 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
                   at + BM * 128 + grp * 1024);
     }
   };
-  const int fr = lane & 31;
   auto frags = [&](int kt, int st, f16x8_t (&pf)[FM], f16x8_t (&qf)[FN]) {
     const uint8_t* sp = ring + (kt % S) * kStage;
     const uint8_t* sq = sp + BM * 128;
@@ -282,6 +290,32 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
     for (int b = 0; b < FN; ++b)
       qf[b] = *reinterpret_cast<const f16x8_t*>(sq + (wn * TN + b * 32 + fr) * 128 + c);
   };
+
+  // What the epilogue reads is fetched before the first stage: a load behind
+  // the epilogue's stores would wait for them, tile after tile (20 us a call).
+  const int half = lane >> 5;
+  uint2 oin[MODE == NS_POLY ? FM : 1][MODE == NS_POLY ? FN : 1][4];
+  float4 xin[MODE == NS_UPDATE ? FM : 1][MODE == NS_UPDATE ? FN : 1][4];
+  float4 djin[MODE == NS_POLY ? FN : 1][4];
+  float din[FM];
+#pragma unroll
+  for (int a = 0; a < FM; ++a) {
+    const int i = i0 + wm * TM + a * 32 + fr;
+    if constexpr (MODE == NS_POLY) din[a] = g.D[mat * g.mp + i];
+    if constexpr (MODE == NS_UPDATE) din[a] = g.a + g.E[mat * g.mp + i];
+#pragma unroll
+    for (int b = 0; b < FN; ++b)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int jq = j0 + wn * TN + b * 32 + 8 * q + 4 * half;
+        if constexpr (MODE == NS_POLY) {
+          oin[a][b][q] = *reinterpret_cast<const uint2*>(g.O + mm + (int64_t)i * g.mp + jq);
+          if (a == 0) djin[b][q] = *reinterpret_cast<const float4*>(g.D + mat * g.mp + jq);
+        }
+        if constexpr (MODE == NS_UPDATE)
+          xin[a][b][q] = *reinterpret_cast<const float4*>(g.X + mn + (int64_t)i * g.np + jq);
+      }
+  }
 
   f32x16_t acc[FM][FN] = {};
   const int KT = (int)(K / 64);
@@ -301,6 +335,8 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
     if (kt + PD < KT) issue(kt + PD);
     f16x8_t pf[2][FM], qf[2][FN];
     frags(kt, 0, pf[0], qf[0]);
+    // the reads of step st + 1 go out between the products of step st
+    constexpr int RD = FM + FN, MF = FM * FN, RPM = (RD + MF - 1) / MF;
 #pragma unroll
     for (int st = 0; st < 4; ++st) {
       if (st < 3) frags(kt, st + 1, pf[(st + 1) & 1], qf[(st + 1) & 1]);
@@ -310,28 +346,44 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
         for (int b = 0; b < FN; ++b)
           acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(qf[st & 1][b], pf[st & 1][a],
                                                              acc[a][b], 0, 0, 0);
+      if (st == 0) __builtin_amdgcn_sched_group_barrier(0x100, RD, 0);
+      if (st < 3) {
+        constexpr int FULL = RD / RPM, REM = RD - FULL * RPM;
+#pragma unroll
+        for (int q = 0; q < FULL; ++q) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     // one product
+          __builtin_amdgcn_sched_group_barrier(0x100, RPM, 0);   // RPM reads
+        }
+        if constexpr (REM > 0) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, REM, 0);
+        }
+        constexpr int REST = MF - FULL - (REM > 0 ? 1 : 0);
+        if constexpr (REST > 0) __builtin_amdgcn_sched_group_barrier(0x008, REST, 0);
+      } else {
+        __builtin_amdgcn_sched_group_barrier(0x008, MF, 0);
+      }
     }
   }
 
-  // Epilogue, one 32 x 32 tile after the other.
-  const int half = lane >> 5;
+  // Epilogue, one 32 x 32 tile after the other: stores only.
 #pragma unroll
   for (int a = 0; a < FM; ++a) {
     const int ib = i0 + wm * TM + a * 32, i = ib + fr;
-    float di = 0.f;
-    if constexpr (MODE == NS_POLY) di = g.D[mat * g.mp + i];
-    if constexpr (MODE == NS_UPDATE) di = g.a + g.E[mat * g.mp + i];
+    const float di = MODE == NS_GRAM ? 0.f : din[a];
 #pragma unroll
     for (int b = 0; b < FN; ++b) {
       const int jb = j0 + wn * TN + b * 32;
       Tile16 w;
       if constexpr (MODE == NS_GRAM) {
+        if (ib == jb) {                              // the tile of the diagonal
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const int j = jb + 8 * (q >> 2) + 4 * half + (q & 3);
-          if (i == j) {
-            g.D[mat * g.mp + i] = acc[a][b][q] * (1.f / (kSX * kSX));
-            acc[a][b][q] = 0.f;
+          for (int q = 0; q < 16; ++q) {
+            const int j = jb + 8 * (q >> 2) + 4 * half + (q & 3);
+            if (i == j) {
+              g.D[mat * g.mp + i] = acc[a][b][q] * (1.f / (kSX * kSX));
+              acc[a][b][q] = 0.f;
+            }
           }
         }
 #pragma unroll
@@ -344,8 +396,8 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int jq = jb + 8 * q + 4 * half;
-          const uint2 ow = *reinterpret_cast<const uint2*>(g.O + mm + (int64_t)i * g.mp + jq);
-          const float4 dj = *reinterpret_cast<const float4*>(g.D + mat * g.mp + jq);
+          const uint2 ow = oin[a][b][q];
+          const float4 dj = djin[b][q];
           const float djs[4] = {dj.x, dj.y, dj.z, dj.w};
           float f[4];
 #pragma unroll
@@ -354,7 +406,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
             const float o = (float)__builtin_bit_cast(_Float16, (uint16_t)bits) * (1.f / kSO);
             const float aa = acc[a][b][4 * q + u] * (1.f / (kSO * kSO));
             f[u] = ((g.b + g.c * (di + djs[u])) * o + g.c * aa) * kSF;
-            if (i == jq + u) {
+            if (ib == jb && i == jq + u) {
               g.E[mat * g.mp + i] = g.b * di + g.c * (aa + di * di);
               f[u] = 0.f;
             }
@@ -367,7 +419,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int jq = jb + 8 * q + 4 * half;
-          const float4 x = *reinterpret_cast<const float4*>(X + jq);
+          const float4 x = xin[a][b][q];
           const float y[4] = {di * x.x + acc[a][b][4 * q] * (1.f / (kSF * kSX)),
                               di * x.y + acc[a][b][4 * q + 1] * (1.f / (kSF * kSX)),
                               di * x.z + acc[a][b][4 * q + 2] * (1.f / (kSF * kSX)),
@@ -416,7 +468,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
       } else {
         _Float16* m = (MODE == NS_GRAM ? g.O : g.F) + mm;
         store_rows(reinterpret_cast<uint16_t*>(m + (int64_t)ib * g.mp + jb), g.mp, w, lane);
-        if (bi != bj)                                // the mirrored tile
+        if (bj < R * bi)                             // the mirrored tile
           store_cols(reinterpret_cast<uint16_t*>(m + (int64_t)jb * g.mp + ib), g.mp, w, lane);
       }
     }
@@ -476,28 +528,31 @@ hipError_t launch_orthogonalize(const OrthoPlan& p, const void* G, int32_t dtype
   };
   if (dtype == PG_F32) load(static_cast<const float*>(G));
   else load(static_cast<const uint16_t*>(G));
-  // Tile of a product with at most `tiles(B)` tiles of B x B a matrix: the
-  // largest that still gives the chip's 256 compute units about a tile each.
-  // Larger tiles read their operands less often, smaller ones start more work
-  // at once.
+  // Tile of a product: TODO
   auto launch = [&](auto MODE, const NsArgs& args) {
     NsArgs g = args;
-    auto tiles = [&](int B) {
-      const int64_t ti = p.mp / B, tj = (MODE() == NS_UPDATE ? p.np : p.mp) / B;
-      return MODE() == NS_UPDATE ? ti * tj : ti * (ti + 1) / 2;
-    };
-    auto go = [&](auto B, auto WM, auto WN, auto S) {
-      g.tiles = (int)tiles(B());
-      g.cols_t = p.np / B();
-      hipLaunchKernelGGL((ns_tile_kernel<MODE(), B(), B(), WM(), WN(), S()>),
+    auto go = [&](auto BM, auto BN, auto WM, auto WN, auto S) {
+      const int ti = p.mp / BM(), r = BM() / BN();
+      g.cols_t = p.np / BN();
+      g.tiles = MODE() == NS_UPDATE ? ti * g.cols_t : r * (ti * (ti + 1) / 2);
+      hipLaunchKernelGGL((ns_tile_kernel<MODE(), BM(), BN(), WM(), WN(), S()>),
                          dim3((unsigned)(n_mat * g.tiles)), dim3(64 * WM() * WN()), 0, s, g);
     };
-    if (p.mp % 256 == 0 && p.np % 256 == 0 && n_mat * tiles(256) >= 192)
-      go(IC<256>{}, IC<2>{}, IC<4>{}, IC<2>{});
-    else if (n_mat * tiles(128) >= 192)
-      go(IC<128>{}, IC<2>{}, IC<2>{}, IC<2>{});
+    auto count = [&](int BM, int BN) {
+      const int64_t ti = p.mp / BM;
+      return n_mat * (MODE() == NS_UPDATE ? ti * (p.np / BN) : BM / BN * (ti * (ti + 1) / 2));
+    };
+    if (p.mp % 256 == 0 && count(256, 128) >= 128) {
+      if (MODE() == NS_UPDATE && p.np % 256 == 0 && UPD256)
+        go(IC<256>{}, IC<256>{}, IC<2>{}, IC<4>{}, IC<2>{});
+      else if (MODE() == NS_UPDATE && UPD128)
+        go(IC<128>{}, IC<128>{}, IC<2>{}, IC<2>{}, IC<2>{});
+      else go(IC<256>{}, IC<128>{}, IC<4>{}, IC<2>{}, IC<3>{});
+    }
+    else if (count(128, 128) >= 192)
+      go(IC<128>{}, IC<128>{}, IC<2>{}, IC<2>{}, IC<2>{});
     else
-      go(IC<64>{}, IC<2>{}, IC<2>{}, IC<4>{});
+      go(IC<64>{}, IC<64>{}, IC<2>{}, IC<2>{}, IC<4>{});
   };
   for (int k = 0; k < oa.steps; ++k) {
     NsArgs g{};
