@@ -31,6 +31,11 @@
 // one row. The epilogue works on the accumulators where they are: rows leave
 // as 16-byte stores after one exchange between the half waves, transposed
 // ones as 8-byte stores after a 4 x 4 transpose inside quads of lanes.
+//
+// Matrices of up to 64 x 256 take one launch instead of 3 steps + 2: a block
+// holds its matrix in LDS through all steps. There the operands are split
+// into two fp16 values each (22 bits; three products for one), for with few
+// columns less averages out and the products cost next to nothing.
 #include <type_traits>
 
 #include "train.h"
@@ -42,6 +47,9 @@ constexpr int kThreads = 256;
 constexpr int kPad = 128;                 // padded sides are multiples of this
 constexpr int kNormBlocks = 256;           // most partial sums of a matrix's norm
 constexpr float kSX = 1024.f, kSO = 4096.f, kSF = 512.f;   // fp16 placements
+
+template <int V>
+using IC = std::integral_constant<int, V>;
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
@@ -475,10 +483,159 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Small matrices: one block each
+
+constexpr int kSmallM = 64, kSmallN = 256, kSmallThreads = 512;
+
+struct Split {
+  _Float16 hi, lo;
+};
+__device__ __forceinline__ Split split_half(float x) {
+  const _Float16 h = (_Float16)x;
+  return {h, (_Float16)(x - (float)h)};
+}
+
+typedef float f32x4s_t __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
+
+// X is 64 x 32 NT with zeros in the padding. v_mfma_f32_16x16x32_f16: lane l
+// holds row l % 16, K elements 8 (l / 16) .. + 7 of each operand, and of the
+// result rows 4 (l / 16) + 0..3 (left operand), column l % 16 (right). Wave w
+// owns tiles (w / 2, 2 (w % 2) + 0..1) of A and B, whose fp32 A it keeps, and
+// tiles (w % 4, w / 4 + 2 t) of X, whose fp32 values it keeps throughout. A
+// and B are symmetric, so a lane's four rows of one column are written as
+// four columns of one row.
+template <typename T, int NT>
+__global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(
+    const T* __restrict__ G, int rows, int cols, OrthoArgs oa, uint16_t* __restrict__ out) {
+  constexpr int NP = 32 * NT;
+  constexpr int LX = NP + 8, LM = kSmallM + 8;       // padded rows: no bank conflicts
+  __shared__ __attribute__((aligned(16))) _Float16 x_hi[kSmallM * LX], x_lo[kSmallM * LX];
+  __shared__ __attribute__((aligned(16))) _Float16 y_hi[NP * LM], y_lo[NP * LM];
+  __shared__ __attribute__((aligned(16))) _Float16 s_hi[kSmallM * LM], s_lo[kSmallM * LM];
+  __shared__ double red[kSmallThreads / 64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int l16 = lane & 15, l4 = lane >> 4;
+  const bool tall = rows > cols;
+  const T* g = G + (int64_t)blockIdx.x * rows * cols;
+  uint16_t* o = out + (int64_t)blockIdx.x * rows * cols;
+  const int m = tall ? cols : rows, n = tall ? rows : cols;
+  const int xi = (wave & 3) * 16 + 4 * l4;           // first of the lane's rows of X
+  auto xj = [&](int t) { return ((wave >> 2) + 2 * t) * 16 + l16; };
+  auto at = [&](int i, int j) { return tall ? (int64_t)j * cols + i : (int64_t)i * cols + j; };
+
+  float x[NT][4];
+  double ss = 0.0;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      x[t][q] = xi + q < m && xj(t) < n ? g_at(g, at(xi + q, xj(t))) : 0.f;
+      ss += (double)x[t][q] * (double)x[t][q];
+    }
+#pragma unroll
+  for (int w = 32; w >= 1; w >>= 1) ss += __shfl_xor(ss, w, 64);
+  if (lane == 0) red[wave] = ss;
+  __syncthreads();
+  ss = 0.0;
+#pragma unroll
+  for (int w = 0; w < kSmallThreads / 64; ++w) ss += red[w];
+  const double inv = ss == 0.0 ? 0.0 : 1.0 / (sqrt(ss) + (double)oa.eps);
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[t][q] = (float)((double)x[t][q] * inv);
+
+  // four values of one column of a tile into row `r` of a symmetric or
+  // transposed matrix
+  auto put4 = [&](_Float16* hi, _Float16* lo, int r, int c, const float (&v)[4], float f) {
+    f16x4_t h, l;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const Split s = split_half(v[q] * f);
+      h[q] = s.hi;
+      l[q] = s.lo;
+    }
+    *reinterpret_cast<f16x4_t*>(hi + r * LM + c) = h;
+    *reinterpret_cast<f16x4_t*>(lo + r * LM + c) = l;
+  };
+  auto put_x = [&] {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      put4(y_hi, y_lo, xj(t), xi, x[t], kSX);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const Split s = split_half(x[t][q] * kSX);
+        x_hi[(xi + q) * LX + xj(t)] = s.hi;
+        x_lo[(xi + q) * LX + xj(t)] = s.lo;
+      }
+    }
+  };
+  // rows p of one split matrix times rows q of another, K elements each
+  auto product = [&](const _Float16* ph, const _Float16* pl, int pld, int p, const _Float16* qh,
+                     const _Float16* ql, int qld, int q, auto K) {
+    f32x4s_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k0 = 0; k0 < K(); k0 += 32) {
+      const int k = k0 + 8 * l4;
+      const f16x8_t ah = *reinterpret_cast<const f16x8_t*>(ph + (p + l16) * pld + k);
+      const f16x8_t al = *reinterpret_cast<const f16x8_t*>(pl + (p + l16) * pld + k);
+      const f16x8_t bh = *reinterpret_cast<const f16x8_t*>(qh + (q + l16) * qld + k);
+      const f16x8_t bl = *reinterpret_cast<const f16x8_t*>(ql + (q + l16) * qld + k);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah, bh, acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah, bl, acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(al, bh, acc, 0, 0, 0);
+    }
+    return acc;
+  };
+  const int ai = (wave >> 1) * 16;
+  auto aj = [&](int t) { return (2 * (wave & 1) + t) * 16; };
+
+  put_x();
+  __syncthreads();
+  for (int step = 0; step < oa.steps; ++step) {
+    float A[2][4], B[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {                    // A = X X^T
+      const f32x4s_t acc = product(x_hi, x_lo, LX, ai, x_hi, x_lo, LX, aj(t), IC<NP>{});
+#pragma unroll
+      for (int q = 0; q < 4; ++q) A[t][q] = acc[q] * (1.f / (kSX * kSX));
+      put4(s_hi, s_lo, aj(t) + l16, ai + 4 * l4, A[t], kSO);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {                    // B = b A + c A A
+      const f32x4s_t acc = product(s_hi, s_lo, LM, ai, s_hi, s_lo, LM, aj(t), IC<kSmallM>{});
+#pragma unroll
+      for (int q = 0; q < 4; ++q) B[t][q] = oa.b * A[t][q] + oa.c * (acc[q] * (1.f / (kSO * kSO)));
+    }
+    __syncthreads();                                 // A is read; B takes its place
+#pragma unroll
+    for (int t = 0; t < 2; ++t) put4(s_hi, s_lo, aj(t) + l16, ai + 4 * l4, B[t], kSF);
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {                   // X <- a X + B X
+      const f32x4s_t acc = product(s_hi, s_lo, LM, (wave & 3) * 16, y_hi, y_lo, LM,
+                                   ((wave >> 2) + 2 * t) * 16, IC<kSmallM>{});
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[t][q] = oa.a * x[t][q] + acc[q] * (1.f / (kSF * kSX));
+    }
+    if (step + 1 == oa.steps) break;
+    __syncthreads();                                 // X's copies are read
+    put_x();
+    __syncthreads();
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (xi + q < m && xj(t) < n)
+        o[at(xi + q, xj(t))] = (uint16_t)pack2_bf16(oa.scale * x[t][q], 0.f);
+}
+
 int64_t al(int64_t x) { return (x + 255) / 256 * 256; }
 
-template <int V>
-using IC = std::integral_constant<int, V>;
 
 }  // namespace
 
@@ -486,6 +643,11 @@ OrthoPlan ortho_plan(int64_t n_mat, int64_t rows, int64_t cols) {
   OrthoPlan p{};
   p.m = (int)(rows < cols ? rows : cols);
   p.n = (int)(rows < cols ? cols : rows);
+  p.small = p.m <= kSmallM && p.n <= kSmallN;
+  if (p.small) {
+    p.bytes = 256;                                   // not used; a size of its own all the same
+    return p;
+  }
   p.mp = (p.m + kPad - 1) / kPad * kPad;
   p.np = (p.n + kPad - 1) / kPad * kPad;
   const int64_t need = (rows * cols + kThreads * 32 - 1) / (kThreads * 32);
@@ -507,6 +669,20 @@ OrthoPlan ortho_plan(int64_t n_mat, int64_t rows, int64_t cols) {
 hipError_t launch_orthogonalize(const OrthoPlan& p, const void* G, int32_t dtype, int64_t n_mat,
                                 int rows, int cols, const OrthoArgs& oa, uint16_t* out,
                                 void* workspace, hipStream_t s) {
+  if (p.small) {
+    auto small = [&](auto* g, auto NT) {
+      hipLaunchKernelGGL((ns_small_kernel<std::remove_const_t<std::remove_pointer_t<decltype(g)>>, NT()>),
+                         dim3((unsigned)n_mat), dim3(kSmallThreads), 0, s, g, rows, cols, oa, out);
+    };
+    auto by_width = [&](auto* g) {
+      if (p.n <= 64) small(g, IC<2>{});
+      else if (p.n <= 128) small(g, IC<4>{});
+      else small(g, IC<8>{});
+    };
+    if (dtype == PG_F32) by_width(static_cast<const float*>(G));
+    else by_width(static_cast<const uint16_t*>(G));
+    return hipGetLastError();
+  }
   auto* ws = static_cast<uint8_t*>(workspace);
   auto* norm = reinterpret_cast<double*>(ws + p.off_norm);
   auto* X = reinterpret_cast<float*>(ws + p.off_x);

@@ -368,6 +368,8 @@ ORTHO = [(1, 1, 1, "f32"), (2, 1, 9, "f32"), (1, 5, 3, "bf16"), (3, 16, 16, "f32
          (1, 64, 128, "f32"), (2, 100, 37, "bf16"), (1, 129, 130, "f32"), (1, 257, 128, "bf16"),
          (2, 200, 333, "f32"), (1, 520, 390, "f32"), (1, 640, 1000, "bf16"), (5, 96, 160, "f32"),
          (1, 24, 700, "f32"), (1, 1500, 130, "f32"),
+         (3, 64, 256, "f32"), (2, 63, 255, "bf16"), (1, 65, 256, "f32"), (2, 64, 257, "f32"),
+         (7, 2, 2, "f32"), (300, 40, 64, "bf16"), (4, 65, 64, "f32"), (2, 129, 33, "f32"),
          # enough matrices for the larger tiles
          (200, 256, 256, "bf16"), (64, 256, 200, "f32"), (50, 300, 384, "bf16"),
          (65, 250, 500, "f32")]
