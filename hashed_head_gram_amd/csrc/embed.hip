@@ -402,19 +402,17 @@ __global__ __launch_bounds__(kSortThreads) void embed_pass_kernel(
       const int m = digits - 1;
       const int da = (to_key(x[u].x) >> shift) & m, db = (to_key(x[u].y) >> shift) & m;
       const int dc = (to_key(x[u].z) >> shift) & m, dd = (to_key(x[u].w) >> shift) & m;
-      // a pass over sorted keys meets long runs of one digit, whose adds
-      // would queue on one address: a wave of one digit adds once
+      // a hot token fills most of a wave, whose adds would queue on one
+      // address: the digit of the first lane is counted by ballots and added
+      // once (the wave lies on one side of t0)
       const int d0 = __builtin_amdgcn_readfirstlane(da);
-      const bool same = da == d0 && db == d0 && dc == d0 && dd == d0;
-      const uint64_t live = __ballot(true);
-      if (__ballot(same) == live) {                      // one wave lies on one side of t0
-        if (lane == 0) atomicAdd(&c[d0], 4 * __popcll(live));
-      } else {
-        atomicAdd(&c[da], 1);
-        atomicAdd(&c[db], 1);
-        atomicAdd(&c[dc], 1);
-        atomicAdd(&c[dd], 1);
-      }
+      const int peeled = __popcll(__ballot(da == d0)) + __popcll(__ballot(db == d0)) +
+                         __popcll(__ballot(dc == d0)) + __popcll(__ballot(dd == d0));
+      if (lane == __ffsll((unsigned long long)__ballot(true)) - 1) atomicAdd(&c[d0], peeled);
+      if (da != d0) atomicAdd(&c[da], 1);
+      if (db != d0) atomicAdd(&c[db], 1);
+      if (dc != d0) atomicAdd(&c[dc], 1);
+      if (dd != d0) atomicAdd(&c[dd], 1);
     }
   }
   if ((int)threadIdx.x < (n & 3))                        // the last tile's or behind it
@@ -775,7 +773,7 @@ EmbedPlan embed_plan(int64_t n, int64_t V, int d) {
   const int64_t slabs = ((int64_t)d + 511) / 512;
   p.chunk = 64;
   const int64_t groups = 64 / embed_lanes(d);        // a wave's
-  while (p.chunk > 8 && n / p.chunk * slabs < 4096 * groups) p.chunk /= 2;
+  while (p.chunk > 8 && n / p.chunk * slabs < 2048 * groups) p.chunk /= 2;
   p.nchunk = (n + p.chunk - 1) / p.chunk;
   int64_t off = 0;
   for (int i = 0; i < 2; ++i) { p.off_keys[i] = off; off += al((n + 8) * 4); }

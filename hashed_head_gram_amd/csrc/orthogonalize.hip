@@ -1,3 +1,9 @@
+#ifndef WMX
+#define WMX 4
+#endif
+#ifndef S64
+#define S64 4
+#endif
 // Orthogonalised update: Newton-Schulz products (gfx950).
 //
 // X_0 = G / (||G||_F + eps) with its smaller side first (X is m x n, m <= n;
@@ -101,19 +107,21 @@ __global__ __launch_bounds__(kThreads) void ns_load_kernel(
   __shared__ float t[64][65];
   __shared__ double sh[kThreads];
   const int64_t mat = blockIdx.z;
-  const double s = block_sum((int)threadIdx.x < parts ? part[mat * parts + threadIdx.x] : 0.0, sh);
-  const double inv = s == 0.0 ? 0.0 : 1.0 / (sqrt(s) + (double)eps);
   const T* g = G + mat * rows * cols;
   const bool tall = rows > cols;                 // X = G^T
   const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;     // tile of X
   const int g0 = tall ? j0 : i0, h0 = tall ? i0 : j0;       // the same tile of G
   const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-#pragma unroll 4
+  float v[16];
+#pragma unroll
   for (int q = 0; q < 16; ++q) {
     const int r = g0 + ty + 4 * q, c = h0 + tx;
-    t[ty + 4 * q][tx] =
-        r < rows && c < cols ? (float)((double)g_at(g, (int64_t)r * cols + c) * inv) : 0.f;
+    v[q] = r < rows && c < cols ? g_at(g, (int64_t)r * cols + c) : 0.f;
   }
+  const double s = block_sum((int)threadIdx.x < parts ? part[mat * parts + threadIdx.x] : 0.0, sh);
+  const double inv = s == 0.0 ? 0.0 : 1.0 / (sqrt(s) + (double)eps);
+#pragma unroll
+  for (int q = 0; q < 16; ++q) t[ty + 4 * q][tx] = (float)((double)v[q] * inv);
   __syncthreads();
   const int64_t base = mat * mp * np;
 #pragma unroll 4
@@ -335,10 +343,8 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
     // stage kt has landed when at most the later issued ones are outstanding;
     // behind the barrier every wave is done with stage kt - 1, whose place
     // stage kt + PD takes
-    const int later = KT - 1 - kt < PD - 1 ? KT - 1 - kt : PD - 1;
-    if (PD >= 3 && later >= 2) wait_loads<PD >= 3 ? 2 * L : 0>();
-    else if (PD >= 2 && later >= 1) wait_loads<PD >= 2 ? L : 0>();
-    else wait_loads<0>();
+    if (KT - 1 - kt >= PD - 1) wait_loads<(PD - 1) * L>();
+    else wait_loads<0>();                            // the last stages: all of them
     ring_barrier();
     if (kt + PD < KT) issue(kt + PD);
     f16x8_t pf[2][FM], qf[2][FN];
@@ -723,12 +729,12 @@ hipError_t launch_orthogonalize(const OrthoPlan& p, const void* G, int32_t dtype
         go(IC<256>{}, IC<256>{}, IC<2>{}, IC<4>{}, IC<2>{});
       else if (MODE() == NS_UPDATE && UPD128)
         go(IC<128>{}, IC<128>{}, IC<2>{}, IC<2>{}, IC<2>{});
-      else go(IC<256>{}, IC<128>{}, IC<4>{}, IC<2>{}, IC<3>{});
+      else go(IC<256>{}, IC<128>{}, IC<WMX>{}, IC<2>{}, IC<3>{});
     }
     else if (count(128, 128) >= 192)
       go(IC<128>{}, IC<128>{}, IC<2>{}, IC<2>{}, IC<2>{});
     else
-      go(IC<64>{}, IC<64>{}, IC<2>{}, IC<2>{}, IC<4>{});
+      go(IC<64>{}, IC<64>{}, IC<2>{}, IC<2>{}, IC<S64>{});
   };
   for (int k = 0; k < oa.steps; ++k) {
     NsArgs g{};
