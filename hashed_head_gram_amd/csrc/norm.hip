@@ -359,13 +359,17 @@ void with_geometry(int d, F f) {
 // forward 296, 264 and 316 us at 15, 20 and 30 waves, backward 511, 490, 512
 // and 542 us at 10, 15, 20 and 30.
 template <int L, int W>
-int64_t norm_blocks(int64_t n, int waves) {
+int64_t norm_blocks(int64_t n, int waves, int per) {
   constexpr int NT = kNormThreads<W>;
   constexpr int64_t ROWS = NT / (L * W);
-  const int64_t need = (n + ROWS - 1) / ROWS, cap = 256 * (int64_t)(waves * 64 / NT);
+  const int64_t need = (n + ROWS * per - 1) / (ROWS * per), cap = 256 * (int64_t)(waves * 64 / NT);
   return need < cap ? need : cap;
 }
 constexpr int kForwardWaves = 20, kBackwardWaves = 15;
+// Rows a backward group takes before another block starts: each block's
+// partial row costs as much as two thirds of a bf16 row of all four tensors
+// (4,095 rows of 1,001 fp32: 22, 20, 23 and 31 us at 2, 4, 8 and 16).
+constexpr int kBackwardRows = 4;
 
 }  // namespace
 
@@ -373,7 +377,7 @@ hipError_t launch_layer_norm(const void* x, int32_t dtype, int64_t n, int d, int
                              const float* gamma, const float* beta, float eps, void* y,
                              int64_t ldy, float* mean, float* rstd, hipStream_t s) {
   with_geometry(d, [&](auto L, auto W, auto CH) {
-    const dim3 grid((unsigned)norm_blocks<L(), W()>(n, kForwardWaves)), block(kNormThreads<W()>);
+    const dim3 grid((unsigned)norm_blocks<L(), W()>(n, kForwardWaves, 1)), block(kNormThreads<W()>);
     if (dtype == PG_F32)
       hipLaunchKernelGGL((norm_kernel<float, L(), W(), CH()>), grid, block, 0, s,
                          static_cast<const float*>(x), n, d, ldx, gamma, beta, eps,
@@ -388,7 +392,7 @@ hipError_t launch_layer_norm(const void* x, int32_t dtype, int64_t n, int d, int
 
 int64_t layer_norm_partials(int64_t n, int d) {
   int64_t blocks = 0;
-  with_geometry(d, [&](auto L, auto W, auto) { blocks = norm_blocks<L(), W()>(n, kBackwardWaves); });
+  with_geometry(d, [&](auto L, auto W, auto) { blocks = norm_blocks<L(), W()>(n, kBackwardWaves, kBackwardRows); });
   return blocks;
 }
 

@@ -1,9 +1,3 @@
-#ifndef WMX
-#define WMX 4
-#endif
-#ifndef S64
-#define S64 4
-#endif
 // Orthogonalised update: Newton-Schulz products (gfx950).
 //
 // X_0 = G / (||G||_F + eps) with its smaller side first (X is m x n, m <= n;
@@ -63,6 +57,11 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ float g_at(const float* G, int64_t i) { return G[i]; }
 __device__ __forceinline__ float g_at(const uint16_t* G, int64_t i) { return bf16_to_f32(G[i]); }
 
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)a) |
+         ((uint32_t)__builtin_bit_cast(uint16_t, (_Float16)b) << 16);
+}
+
 // Sum over the block in a fixed order, in every thread.
 __device__ __forceinline__ double block_sum(double s, double* sh) {
   sh[threadIdx.x] = s;
@@ -119,28 +118,34 @@ __global__ __launch_bounds__(kThreads) void ns_load_kernel(
     v[q] = r < rows && c < cols ? g_at(g, (int64_t)r * cols + c) : 0.f;
   }
   const double s = block_sum((int)threadIdx.x < parts ? part[mat * parts + threadIdx.x] : 0.0, sh);
-  const double inv = s == 0.0 ? 0.0 : 1.0 / (sqrt(s) + (double)eps);
+  // 1 / (norm + eps) as f 2^e: it may lie outside fp32's range, the products
+  // with G's values do not; fp64 products took 9 us of 54 at 5 x 2560 x 1280
+  int e = 0;
+  const float f = (float)frexp(s == 0.0 ? 0.0 : 1.0 / (sqrt(s) + (double)eps), &e);
 #pragma unroll
-  for (int q = 0; q < 16; ++q) t[ty + 4 * q][tx] = (float)((double)v[q] * inv);
+  for (int q = 0; q < 16; ++q) t[ty + 4 * q][tx] = ldexpf(v[q], e) * f;
   __syncthreads();
+  // 16 threads a row of the tile, four columns each, four rows a thread
   const int64_t base = mat * mp * np;
-#pragma unroll 4
-  for (int q = 0; q < 16; ++q) {
-    const int a = ty + 4 * q;
-    const float x = tall ? t[tx][a] : t[a][tx];            // X[i0 + a][j0 + tx]
-    const float y = tall ? t[a][tx] : t[tx][a];            // X[i0 + tx][j0 + a]
-    X[base + (int64_t)(i0 + a) * np + j0 + tx] = x;
-    Xh[base + (int64_t)(i0 + a) * np + j0 + tx] = (_Float16)(x * kSX);
-    Yh[base + (int64_t)(j0 + a) * mp + i0 + tx] = (_Float16)(y * kSX);
+  const int c = (threadIdx.x & 15) * 4;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int a = (threadIdx.x >> 4) + 16 * q;
+    float x[4], y[4];                            // X[i0 + a][j0 + c ..], X[i0 + c ..][j0 + a]
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      x[u] = tall ? t[c + u][a] : t[a][c + u];
+      y[u] = tall ? t[a][c + u] : t[c + u][a];
+    }
+    const int64_t at = base + (int64_t)(i0 + a) * np + j0 + c;
+    *reinterpret_cast<float4*>(X + at) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint2*>(Xh + at) =
+        make_uint2(pack_half(x[0] * kSX, x[1] * kSX), pack_half(x[2] * kSX, x[3] * kSX));
+    *reinterpret_cast<uint2*>(Yh + base + (int64_t)(j0 + a) * mp + i0 + c) =
+        make_uint2(pack_half(y[0] * kSX, y[1] * kSX), pack_half(y[2] * kSX, y[3] * kSX));
   }
 }
 
-#ifndef UPD256
-#define UPD256 0
-#endif
-#ifndef UPD128
-#define UPD128 0
-#endif
 enum { NS_GRAM, NS_POLY, NS_UPDATE };
 
 struct NsArgs {
@@ -183,10 +188,6 @@ __device__ __forceinline__ void ring_barrier() {
   asm volatile("" ::: "memory");
 }
 
-__device__ __forceinline__ uint32_t pack_half(float a, float b) {
-  return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)a) |
-         ((uint32_t)__builtin_bit_cast(uint16_t, (_Float16)b) << 16);
-}
 
 template <int CTRL>
 __device__ __forceinline__ uint32_t quad_move(uint32_t x) {
@@ -232,19 +233,20 @@ __device__ __forceinline__ void store_cols(uint16_t* dst, int64_t ld, const Tile
   }
 }
 
-// BM x BN tile of P Q^T by WM x WN waves, S stages of 64 in the ring.
-template <int MODE, int BM, int BN, int WM, int WN, int S>
-__global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
+// BM x BN tile of P Q^T by KS groups of WM x WN waves; S stages in the ring, a
+// stage being 64 of K for each group. Two groups halve the chain of stages of
+// a small product, whose time is latency; their sums are joined at the end.
+template <int MODE, int BM, int BN, int WM, int WN, int S, int KS>
+__global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
   constexpr int NW = WM * WN;
   constexpr int TM = BM / WM, TN = BN / WN;          // a wave's part
   constexpr int FM = TM / 32, FN = TN / 32;
   constexpr int PL = BM / 8 / NW, QL = BN / 8 / NW;  // loads of 8 rows a wave and stage
   constexpr int L = PL + QL;
-  constexpr int R = BM / BN;                         // tiles of a diagonal block
   constexpr int kStage = (BM + BN) * 128;
   static_assert(PL >= 1 && QL >= 1 && TM % 32 == 0 && TN % 32 == 0 && (S - 1) * L < 64, "tile");
-  static_assert(MODE == NS_UPDATE || BM == BN || BM == 2 * BN, "mirrored tiles");
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[S * kStage];
+  static_assert(MODE == NS_UPDATE || (BM == BN && TM * TN <= 4096), "mirrored tiles");
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[S * KS * kStage];
 
   // consecutive tiles run on one of the 8 XCDs and share operands in its L2
   const int64_t total = gridDim.x, per = total / 8;
@@ -256,12 +258,11 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
   if constexpr (MODE == NS_UPDATE) {
     bi = t / g.cols_t;
     bj = t - bi * g.cols_t;
-  } else {                                           // row bi has R (bi + 1) tiles
-    const int h = t / R;
-    bi = (int)((sqrtf(8.f * (float)h + 1.f) - 1.f) * 0.5f);
-    while (bi * (bi + 1) / 2 > h) --bi;
-    while ((bi + 1) * (bi + 2) / 2 <= h) ++bi;
-    bj = t - R * (bi * (bi + 1) / 2);
+  } else {                                           // t = bi (bi + 1) / 2 + bj, bj <= bi
+    bi = (int)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
+    while (bi * (bi + 1) / 2 > t) --bi;
+    while ((bi + 1) * (bi + 2) / 2 <= t) ++bi;
+    bj = t - bi * (bi + 1) / 2;
   }
   const int i0 = bi * BM, j0 = bj * BN;
   const int64_t mm = mat * g.mp * g.mp, mn = mat * g.mp * g.np;
@@ -269,7 +270,8 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
   const auto* P = reinterpret_cast<const uint8_t*>(g.P + (MODE == NS_GRAM ? mn : mm) + i0 * K);
   const auto* Q = reinterpret_cast<const uint8_t*>(g.Q + (MODE == NS_POLY ? mm : mn) + j0 * K);
 
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int ks = all / NW, wave = all % NW;
   const int wm = wave / WN, wn = wave % WN;
   const int fr = lane & 31;
 
@@ -280,23 +282,24 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
   const uint32_t chunk = (uint32_t)(((lane & 7) ^ (dr >> 1)) * 16);
   const uint32_t ring0 = (uint32_t)(uintptr_t)(const lds_void_t*)ring;
   auto issue = [&](int kt) {
-    const uint32_t at = ring0 + (kt % S) * kStage;
+    const uint32_t at = ring0 + ((kt % S) * KS + ks) * kStage;
+    const int64_t k0 = (int64_t)(kt * KS + ks) * 64;
 #pragma unroll
     for (int q = 0; q < PL; ++q) {
       const int grp = wave * PL + q;
-      load_to_lds(P + (grp * 8 * K + kt * 64) * 2,
+      load_to_lds(P + (grp * 8 * K + k0) * 2,
                   (uint32_t)(dr * K * 2) + (chunk ^ (uint32_t)((grp & 1) * 64)), at + grp * 1024);
     }
 #pragma unroll
     for (int q = 0; q < QL; ++q) {
       const int grp = wave * QL + q;
-      load_to_lds(Q + (grp * 8 * K + kt * 64) * 2,
+      load_to_lds(Q + (grp * 8 * K + k0) * 2,
                   (uint32_t)(dr * K * 2) + (chunk ^ (uint32_t)((grp & 1) * 64)),
                   at + BM * 128 + grp * 1024);
     }
   };
   auto frags = [&](int kt, int st, f16x8_t (&pf)[FM], f16x8_t (&qf)[FN]) {
-    const uint8_t* sp = ring + (kt % S) * kStage;
+    const uint8_t* sp = ring + ((kt % S) * KS + ks) * kStage;
     const uint8_t* sq = sp + BM * 128;
     const int c = ((st * 2 + (lane >> 5)) ^ ((fr >> 1) & 7)) * 16;
 #pragma unroll
@@ -307,15 +310,17 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
       qf[b] = *reinterpret_cast<const f16x8_t*>(sq + (wn * TN + b * 32 + fr) * 128 + c);
   };
 
-  // What the epilogue reads is fetched before the first stage: a load behind
-  // the epilogue's stores would wait for them, tile after tile (20 us a call).
+  // What the epilogue reads is fetched before the first stage, where the
+  // registers hold it (PRE): a load behind the epilogue's stores waits for
+  // them, tile after tile.
+  constexpr bool PRE = FM * FN <= 4;
   const int half = lane >> 5;
   uint2 oin[MODE == NS_POLY ? FM : 1][MODE == NS_POLY ? FN : 1][4];
   float4 xin[MODE == NS_UPDATE ? FM : 1][MODE == NS_UPDATE ? FN : 1][4];
   float4 djin[MODE == NS_POLY ? FN : 1][4];
   float din[FM];
 #pragma unroll
-  for (int a = 0; a < FM; ++a) {
+  for (int a = 0; a < FM && ks == 0; ++a) {
     const int i = i0 + wm * TM + a * 32 + fr;
     if constexpr (MODE == NS_POLY) din[a] = g.D[mat * g.mp + i];
     if constexpr (MODE == NS_UPDATE) din[a] = g.a + g.E[mat * g.mp + i];
@@ -328,13 +333,16 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
           oin[a][b][q] = *reinterpret_cast<const uint2*>(g.O + mm + (int64_t)i * g.mp + jq);
           if (a == 0) djin[b][q] = *reinterpret_cast<const float4*>(g.D + mat * g.mp + jq);
         }
-        if constexpr (MODE == NS_UPDATE)
+        if constexpr (MODE == NS_UPDATE && PRE)
           xin[a][b][q] = *reinterpret_cast<const float4*>(g.X + mn + (int64_t)i * g.np + jq);
       }
   }
 
-  f32x16_t acc[FM][FN] = {};
-  const int KT = (int)(K / 64);
+  // one tile a wave: two accumulators in turn, so products need not wait
+  constexpr int AC = FM * FN == 1 ? 2 : 1;
+  f32x16_t sums[AC][FM][FN] = {};
+  auto& acc = sums[0];
+  const int KT = (int)(K / (64 * KS));
   constexpr int PD = S - 1;                          // stages in flight
 #pragma unroll
   for (int st = 0; st < PD; ++st)
@@ -358,8 +366,8 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
       for (int a = 0; a < FM; ++a)
 #pragma unroll
         for (int b = 0; b < FN; ++b)
-          acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(qf[st & 1][b], pf[st & 1][a],
-                                                             acc[a][b], 0, 0, 0);
+          sums[st % AC][a][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+              qf[st & 1][b], pf[st & 1][a], sums[st % AC][a][b], 0, 0, 0);
       if (st == 0) __builtin_amdgcn_sched_group_barrier(0x100, RD, 0);
       if (st < 3) {
         constexpr int FULL = RD / RPM, REM = RD - FULL * RPM;
@@ -378,6 +386,22 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
         __builtin_amdgcn_sched_group_barrier(0x008, MF, 0);
       }
     }
+  }
+
+  if constexpr (AC == 2)
+#pragma unroll
+    for (int q = 0; q < 16; ++q) acc[0][0][q] += sums[1][0][0][q];
+  if constexpr (KS == 2) {                           // the second group's sums, by way of LDS
+    static_assert(FM * FN == 1 && NW * 4096 <= S * KS * kStage, "join");
+    float* j = reinterpret_cast<float*>(ring) + wave * 1024 + lane;
+    __syncthreads();
+    if (ks == 1)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) j[64 * q] = acc[0][0][q];
+    __syncthreads();
+    if (ks == 1) return;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) acc[0][0][q] += j[64 * q];
   }
 
   // Epilogue, one 32 x 32 tile after the other: stores only.
@@ -433,7 +457,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int jq = jb + 8 * q + 4 * half;
-          const float4 x = xin[a][b][q];
+          const float4 x = PRE ? xin[a][b][q] : *reinterpret_cast<const float4*>(X + jq);
           const float y[4] = {di * x.x + acc[a][b][4 * q] * (1.f / (kSF * kSX)),
                               di * x.y + acc[a][b][4 * q + 1] * (1.f / (kSF * kSX)),
                               di * x.z + acc[a][b][4 * q + 2] * (1.f / (kSF * kSX)),
@@ -482,7 +506,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ns_tile_kernel(NsArgs g) {
       } else {
         _Float16* m = (MODE == NS_GRAM ? g.O : g.F) + mm;
         store_rows(reinterpret_cast<uint16_t*>(m + (int64_t)ib * g.mp + jb), g.mp, w, lane);
-        if (bj < R * bi)                             // the mirrored tile
+        if (bj < bi)                                 // the mirrored tile
           store_cols(reinterpret_cast<uint16_t*>(m + (int64_t)jb * g.mp + ib), g.mp, w, lane);
       }
     }
@@ -547,11 +571,12 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(
   ss = 0.0;
 #pragma unroll
   for (int w = 0; w < kSmallThreads / 64; ++w) ss += red[w];
-  const double inv = ss == 0.0 ? 0.0 : 1.0 / (sqrt(ss) + (double)oa.eps);
+  int e = 0;                                         // 1 / (norm + eps) = f 2^e
+  const float f = (float)frexp(ss == 0.0 ? 0.0 : 1.0 / (sqrt(ss) + (double)oa.eps), &e);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) x[t][q] = (float)((double)x[t][q] * inv);
+    for (int q = 0; q < 4; ++q) x[t][q] = ldexpf(x[t][q], e) * f;
 
   // four values of one column of a tile into row `r` of a symmetric or
   // transposed matrix
@@ -710,31 +735,34 @@ hipError_t launch_orthogonalize(const OrthoPlan& p, const void* G, int32_t dtype
   };
   if (dtype == PG_F32) load(static_cast<const float*>(G));
   else load(static_cast<const uint16_t*>(G));
-  // Tile of a product: TODO
+  // The tile of a product: the largest that leaves a chip of 256 compute units
+  // about a block each. Larger tiles read operands less often, smaller ones
+  // start more work at once. Measured, us of a whole call: 256 x 256 updates
+  // against 128 x 128 at 256 blocks (4096 x 4096) 1954 to 2035, at 100 (two
+  // 2560 x 1280) 508 to 389; 128 x 128 against 64 x 64 at 200 blocks (one
+  // 2560 x 1280) 246 to 272, at 100 (one 1280 x 1280) 210 to 173. Up to 256
+  // blocks of 64 x 64 two groups of waves share a tile's K (768 x 1024: 124
+  // to 131); beyond, two blocks share a compute unit instead (32 of 256 x
+  // 256: 117 to 147).
   auto launch = [&](auto MODE, const NsArgs& args) {
+    constexpr bool UPDATE = MODE() == NS_UPDATE;
     NsArgs g = args;
-    auto go = [&](auto BM, auto BN, auto WM, auto WN, auto S) {
-      const int ti = p.mp / BM(), r = BM() / BN();
-      g.cols_t = p.np / BN();
-      g.tiles = MODE() == NS_UPDATE ? ti * g.cols_t : r * (ti * (ti + 1) / 2);
-      hipLaunchKernelGGL((ns_tile_kernel<MODE(), BM(), BN(), WM(), WN(), S()>),
-                         dim3((unsigned)(n_mat * g.tiles)), dim3(64 * WM() * WN()), 0, s, g);
+    auto blocks = [&](int B) {
+      const int64_t ti = p.mp / B;
+      return n_mat * (UPDATE ? ti * (p.np / B) : ti * (ti + 1) / 2);
     };
-    auto count = [&](int BM, int BN) {
-      const int64_t ti = p.mp / BM;
-      return n_mat * (MODE() == NS_UPDATE ? ti * (p.np / BN) : BM / BN * (ti * (ti + 1) / 2));
+    auto go = [&](auto B, auto WM, auto WN, auto S, auto KS) {
+      g.cols_t = p.np / B();
+      g.tiles = (int)(blocks(B()) / n_mat);
+      hipLaunchKernelGGL((ns_tile_kernel<MODE(), B(), B(), WM(), WN(), S(), KS()>),
+                         dim3((unsigned)blocks(B())), dim3(64 * WM() * WN() * KS()), 0, s, g);
     };
-    if (p.mp % 256 == 0 && count(256, 128) >= 128) {
-      if (MODE() == NS_UPDATE && p.np % 256 == 0 && UPD256)
-        go(IC<256>{}, IC<256>{}, IC<2>{}, IC<4>{}, IC<2>{});
-      else if (MODE() == NS_UPDATE && UPD128)
-        go(IC<128>{}, IC<128>{}, IC<2>{}, IC<2>{}, IC<2>{});
-      else go(IC<256>{}, IC<128>{}, IC<WMX>{}, IC<2>{}, IC<3>{});
-    }
-    else if (count(128, 128) >= 192)
-      go(IC<128>{}, IC<128>{}, IC<2>{}, IC<2>{}, IC<2>{});
-    else
-      go(IC<64>{}, IC<64>{}, IC<2>{}, IC<2>{}, IC<S64>{});
+    if constexpr (UPDATE)
+      if (p.mp % 256 == 0 && p.np % 256 == 0 && blocks(256) >= 200)
+        return go(IC<256>{}, IC<2>{}, IC<4>{}, IC<2>{}, IC<1>{});
+    if (blocks(128) >= 192) return go(IC<128>{}, IC<2>{}, IC<2>{}, IC<2>{}, IC<1>{});
+    if (blocks(64) > 256) return go(IC<64>{}, IC<2>{}, IC<2>{}, IC<4>{}, IC<1>{});
+    go(IC<64>{}, IC<2>{}, IC<2>{}, IC<3>{}, IC<2>{});
   };
   for (int k = 0; k < oa.steps; ++k) {
     NsArgs g{};
