@@ -33,42 +33,53 @@ constexpr int kItems = 8;
 constexpr int kTile = kThreads * kItems;     // items per block of a sort pass
 constexpr int kSortThreads = 1024;
 constexpr int kSmall = 4096;                 // most tokens the one-block sort takes
+constexpr int kEmbedBlocks = 4;              // forward blocks a compute unit
+// LDS a reduction block asks for without using it: three blocks, twelve waves
+// a compute unit, whose eight rows in flight are enough; 268 us at 32 waves,
+// 260 at 12 (131,072 rows of 2,560 bf16).
+constexpr unsigned kReduceLds = 53 * 1024;
 constexpr int64_t kOneLaunch = 65536;        // most tokens a one-launch pass takes
 
 // ---------------------------------------------------------------------------
 // Forward
 
 // A group of L lanes covers one row, U vectors of 8 columns a lane at a time:
-// the loads of a whole pass are out before the first store (one vector a pass
-// left too little in flight: 208 us against LATER for 131,072 rows of 2,560
-// bf16). The output is written past the caches, which the table's hot rows
-// keep to themselves.
+// the loads of a whole pass are out before the first store. Blocks walk rows
+// with the next token in hand, four blocks a compute unit. The output is
+// written past the caches, which the table's hot rows keep to themselves.
+// 131,072 rows of 2,560 bf16: 208 us with one vector a pass and 32 waves a
+// unit, 192 with streaming stores, 180 with the whole pass in flight, 171 with
+// 16 waves (180, 175 and 187 with 12, 20 and 32).
 template <typename TI, typename TO, int L, int U>
 __global__ __launch_bounds__(kThreads) void embed_kernel(
     const TI* __restrict__ table, int64_t V, int d, float scale,
     const int32_t* __restrict__ tokens, int64_t n, TO* __restrict__ out, int64_t ld,
     int32_t* __restrict__ status) {
   const int ln = threadIdx.x & (L - 1);
-  const int64_t t = (int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L;
-  if (t >= n) return;
-  const int32_t tok = tokens[t];
-  const bool ok = tok >= 0 && (int64_t)tok < V;
-  if (!ok && ln == 0 && status) atomicOr(status, 1);
-  const TI* src = table + (int64_t)(ok ? tok : 0) * d;
-  TO* dst = out + t * ld;
-  for (int c0 = ln * 8; c0 < d; c0 += U * L * 8) {
-    Raw8<TI> r[U];
+  const int64_t stride = (int64_t)gridDim.x * (kThreads / L);
+  int64_t t = (int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L;
+  int32_t tok = t < n ? tokens[t] : 0;
+  for (; t < n; t += stride) {
+    const int32_t next = t + stride < n ? tokens[t + stride] : 0;
+    const bool ok = tok >= 0 && (int64_t)tok < V;
+    if (!ok && ln == 0 && status) atomicOr(status, 1);
+    const TI* src = table + (int64_t)(ok ? tok : 0) * d;
+    TO* dst = out + t * ld;
+    for (int c0 = ln * 8; c0 < d; c0 += U * L * 8) {
+      Raw8<TI> r[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) r[u] = load8(src + c0 + u * L * 8, ok ? d - c0 - u * L * 8 : 0);
+      for (int u = 0; u < U; ++u) r[u] = load8(src + c0 + u * L * 8, ok ? d - c0 - u * L * 8 : 0);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * L * 8;
-      if (c >= d) continue;
-      float y[8];
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * L * 8;
+        if (c >= d) continue;
+        float y[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = ok ? scale * r[u].get(i) : 0.f;
-      store8<true>(dst + c, y, d - c);
+        for (int i = 0; i < 8; ++i) y[i] = ok ? scale * r[u].get(i) : 0.f;
+        store8<true>(dst + c, y, d - c);
+      }
     }
+    tok = next;
   }
 }
 
@@ -730,8 +741,8 @@ hipError_t launch_embed(int32_t table_dtype, const void* table, int64_t V, int d
     using TI = std::remove_const_t<std::remove_pointer_t<decltype(tab)>>;
     using TO = std::remove_pointer_t<decltype(o)>;
     auto launch = [&](auto L, auto U) {
-      const int64_t rows = kThreads / L();
-      hipLaunchKernelGGL((embed_kernel<TI, TO, L(), U()>), dim3((unsigned)((n + rows - 1) / rows)),
+      const int64_t rows = kThreads / L(), need = (n + rows - 1) / rows, cap = 256 * kEmbedBlocks;
+      hipLaunchKernelGGL((embed_kernel<TI, TO, L(), U()>), dim3((unsigned)std::min(need, cap)),
                          dim3(kThreads), 0, s, tab, V, d, scale, tokens, n, o, ld, status);
     };
     if (d <= 64) return launch(IC<8>{}, IC<1>{});
@@ -866,7 +877,7 @@ hipError_t launch_embed_backward(const EmbedPlan& p, const void* dout, int32_t d
       using T = std::remove_const_t<std::remove_pointer_t<decltype(src)>>;
       const int64_t per = kThreads / L(), groups = p.nchunk * slabs;
       hipLaunchKernelGGL((embed_reduce_kernel<T, L(), MODE(), PARTS()>),
-                         dim3((unsigned)((groups + per - 1) / per)), block, 0, s, src, ld, k, v, n,
+                         dim3((unsigned)((groups + per - 1) / per)), block, kReduceLds, s, src, ld, k, v, n,
                          V, d, p.chunk, p.nchunk, slabs, heads, part, dpad, list, out);
     };
     auto by_lanes = [&](auto* src) {
