@@ -135,17 +135,18 @@ __global__ __launch_bounds__(kThreads) void embed_hist_kernel(
 
 // Exclusive scan of the m counts of row blockIdx.x, in place; the row's sum
 // goes to totals[blockIdx.x], and as n_unique to a caller who wants it.
-__global__ __launch_bounds__(kThreads) void embed_scan_kernel(int32_t* __restrict__ a, int64_t m,
+template <int NT>
+__global__ __launch_bounds__(NT) void embed_scan_kernel(int32_t* __restrict__ a, int64_t m,
                                                               int32_t* __restrict__ totals,
                                                               int64_t* __restrict__ n_unique) {
-  __shared__ int32_t sh[kThreads / 64];
+  __shared__ int32_t sh[NT / 64];
   int32_t* row = a + (int64_t)blockIdx.x * m;
   int32_t run = 0;
-  for (int64_t base = 0; base < m; base += kThreads) {
+  for (int64_t base = 0; base < m; base += NT) {
     const int64_t i = base + threadIdx.x;
     const int32_t x = i < m ? row[i] : 0;
     int32_t tot;
-    const int32_t e = block_exclusive_scan<kThreads>(x, sh, &tot);
+    const int32_t e = block_exclusive_scan<NT>(x, sh, &tot);
     if (i < m) row[i] = run + e;
     run += tot;
   }
@@ -647,9 +648,9 @@ __global__ __launch_bounds__(kThreads) void embed_reduce_kernel(
 // Rows cut by chunk borders, from the lists: the parts of the row that starts
 // in chunk c are part[2 c + 1], part[2 (c + 1)], ... up to the chunk where it
 // ends. Blocks below `longs` take the long rows, a block each, split over its
-// eight waves in order (the hottest row of 131,072 Zipf tokens has about 350
+// sixteen waves in order (the hottest row of 131,072 Zipf tokens has about 350
 // parts); the others the short ones, a wave each.
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 1024;
 template <int MODE, bool PARTS>
 __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(
     const uint32_t* __restrict__ keys, int d, int chunk, int64_t nchunk,
@@ -860,7 +861,7 @@ hipError_t launch_embed_backward(const EmbedPlan& p, const void* dout, int32_t d
       const int64_t fb = q == 0 ? fill_blocks : 0;
       hipLaunchKernelGGL(embed_hist_kernel, dim3((unsigned)(p.nblk + fb)), block, 0, s, tk, kin, n,
                          V, shift, digits, p.nblk, counts, list, dtable, fill_count);
-      hipLaunchKernelGGL(embed_scan_kernel, dim3((unsigned)digits), block, 0, s, counts, p.nblk,
+      hipLaunchKernelGGL(embed_scan_kernel<kThreads>, dim3((unsigned)digits), block, 0, s, counts, p.nblk,
                          totals, nullptr);
       hipLaunchKernelGGL(embed_scatter_kernel, dim3((unsigned)p.nblk), block, 0, s, tk, kin, vin,
                          n, V, shift, p.rb, counts, totals, keys[q & 1], vals[q & 1]);
@@ -869,7 +870,8 @@ hipError_t launch_embed_backward(const EmbedPlan& p, const void* dout, int32_t d
     v = vals[(p.passes - 1) & 1];
     hipLaunchKernelGGL(embed_heads_kernel, dim3((unsigned)((p.nchunk + 3) / 4)), block, 0, s, k, n,
                        V, p.chunk, p.nchunk, heads);
-    hipLaunchKernelGGL(embed_scan_kernel, dim3(1), block, 0, s, heads, p.nchunk, total, n_unique);
+    hipLaunchKernelGGL(embed_scan_kernel<kSortThreads>, dim3(1), dim3(kSortThreads), 0, s, heads,
+                       p.nchunk, total, n_unique);
   }
   const RowOut out{urows, ugrad, dtable, scale};
   auto finish = [&](auto MODE, auto PARTS) {
@@ -890,7 +892,7 @@ hipError_t launch_embed_backward(const EmbedPlan& p, const void* dout, int32_t d
     else by_lanes(static_cast<const uint16_t*>(dout));
     if (p.nchunk > 1) {
       const int64_t longs = std::min<int64_t>(p.nchunk / kShortParts + 1, 128);
-      const int64_t shorts = std::min<int64_t>((p.nchunk + 7) / 8, 512);
+      const int64_t shorts = std::min<int64_t>((p.nchunk + 15) / 16, 256);
       hipLaunchKernelGGL((embed_join_kernel<MODE(), PARTS()>),
                          dim3((unsigned)(longs + shorts), (unsigned)slabs), dim3(kJoinThreads), 0,
                          s, k, d, p.chunk, p.nchunk, heads, part, dpad, list, (int)longs, out);
