@@ -45,6 +45,9 @@ int check_ortho(int64_t n_mat, int32_t rows, int32_t cols) {
   if (n_mat < 0 || rows < 1 || cols < 1) return PG_EINVAL;
   if (rows > kMaxOrthoSide || cols > kMaxOrthoSide) return PG_EUNSUPPORTED;
   if (n_mat > 65535) return PG_ERANGE;
+  // the tile kernels' grid: 2^34 padded elements are 2^22 blocks at most
+  const auto pad = [](int64_t x) { return (x + 127) / 128 * 128; };
+  if (n_mat * pad(rows) * pad(cols) > (int64_t)1 << 34) return PG_ERANGE;
   return PG_OK;
 }
 

@@ -29,8 +29,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxDigitBits = 9;
 constexpr int kMaxDigits = 1 << kMaxDigitBits;
-constexpr int kItems = 8;
-constexpr int kTile = kThreads * kItems;     // items per block of a sort pass
+// Items a thread of a three-launch sort pass takes: two fill the chip up to
+// 2^18 items (a pass over 131,072: 16 us against 21), eight keep the count
+// matrix small beyond.
+constexpr int kFewItems = 2, kManyItems = 8;
+constexpr int64_t kFewLimit = 1 << 18;
 constexpr int kSortThreads = 1024;
 constexpr int kSmall = 4096;                 // most tokens the one-block sort takes
 constexpr int kEmbedBlocks = 4;              // forward blocks a compute unit
@@ -107,6 +110,7 @@ __device__ __forceinline__ void fill_zero(float* __restrict__ p, int64_t count, 
 // counts[digit * nblk + b] = keys of block b's tile with that digit. The
 // first pass reads the tokens themselves and clears the join list's counter;
 // blocks behind the nblk tiles clear the dense gradient.
+template <int kItems>
 __global__ __launch_bounds__(kThreads) void embed_hist_kernel(
     const int32_t* __restrict__ tokens, const uint32_t* __restrict__ keys, int64_t n, int64_t V,
     int shift, int digits, int64_t nblk, int32_t* __restrict__ counts, int32_t* __restrict__ list,
@@ -119,7 +123,7 @@ __global__ __launch_bounds__(kThreads) void embed_hist_kernel(
   for (int q = threadIdx.x; q < digits; q += kThreads) c[q] = 0;
   if (tokens && blockIdx.x == 0 && threadIdx.x < 2) list[threadIdx.x] = 0;
   __syncthreads();
-  const int64_t base = (int64_t)blockIdx.x * kTile;
+  const int64_t base = (int64_t)blockIdx.x * (kThreads * kItems);
 #pragma unroll
   for (int q = 0; q < kItems; ++q) {
     const int64_t i = base + q * kThreads + threadIdx.x;
@@ -170,6 +174,7 @@ __device__ __forceinline__ uint64_t same_digit(bool live, int dg, int rb) {
 // 64 consecutive items at a time; lanes of equal digit find each other with
 // one ballot per digit bit, and per-wave digit counters in LDS carry the
 // order from one step to the next.
+template <int kItems>
 __global__ __launch_bounds__(kThreads) void embed_scatter_kernel(
     const int32_t* __restrict__ tokens, const uint32_t* __restrict__ kin,
     const int32_t* __restrict__ vin, int64_t n, int64_t V, int shift, int rb,
@@ -183,8 +188,8 @@ __global__ __launch_bounds__(kThreads) void embed_scatter_kernel(
   for (int q = threadIdx.x; q < kWaves * kMaxDigits; q += kThreads)
     (&wcnt[0][0])[q] = 0;
   __syncthreads();
-  // wave w owns items [base + w * 512, base + (w + 1) * 512) of the tile
-  const int64_t base = (int64_t)blockIdx.x * kTile + (int64_t)wave * (kItems * 64);
+  // wave w owns the tile's items [64 w kItems, 64 (w + 1) kItems)
+  const int64_t base = ((int64_t)blockIdx.x * kThreads + wave * 64) * kItems;
   uint32_t key[kItems];
   int32_t val[kItems];
   int rank[kItems];                 // rank among the wave's earlier equal digits
@@ -781,7 +786,8 @@ EmbedPlan embed_plan(int64_t n, int64_t V, int d) {
   while (((int64_t)1 << p.bits) <= V) ++p.bits;      // keys 0 .. V
   p.passes = (p.bits + kMaxDigitBits - 1) / kMaxDigitBits;
   p.rb = (p.bits + p.passes - 1) / p.passes;
-  p.nblk = (n + kTile - 1) / kTile;
+  const int64_t tile = kThreads * (n <= kFewLimit ? kFewItems : kManyItems);
+  p.nblk = (n + tile - 1) / tile;
   const int64_t slabs = ((int64_t)d + 511) / 512;
   p.chunk = 64;
   const int64_t groups = 64 / embed_lanes(d);        // a wave's
@@ -853,19 +859,23 @@ hipError_t launch_embed_backward(const EmbedPlan& p, const void* dout, int32_t d
     hipLaunchKernelGGL(embed_rank_kernel, dim3((unsigned)nblk), dim3(kSortThreads), 0, s, k,
                        (int)n, V, p.chunk, heads, total, n_unique);
   } else {
-    for (int q = 0; q < p.passes; ++q) {
-      const int shift = q * p.rb;
-      const int32_t* tk = q == 0 ? tokens : nullptr;
-      const uint32_t* kin = keys[(q + 1) & 1];
-      const int32_t* vin = vals[(q + 1) & 1];
-      const int64_t fb = q == 0 ? fill_blocks : 0;
-      hipLaunchKernelGGL(embed_hist_kernel, dim3((unsigned)(p.nblk + fb)), block, 0, s, tk, kin, n,
-                         V, shift, digits, p.nblk, counts, list, dtable, fill_count);
-      hipLaunchKernelGGL(embed_scan_kernel<kThreads>, dim3((unsigned)digits), block, 0, s, counts, p.nblk,
-                         totals, nullptr);
-      hipLaunchKernelGGL(embed_scatter_kernel, dim3((unsigned)p.nblk), block, 0, s, tk, kin, vin,
-                         n, V, shift, p.rb, counts, totals, keys[q & 1], vals[q & 1]);
-    }
+    auto sort = [&](auto ITEMS) {
+      for (int q = 0; q < p.passes; ++q) {
+        const int shift = q * p.rb;
+        const int32_t* tk = q == 0 ? tokens : nullptr;
+        const uint32_t* kin = keys[(q + 1) & 1];
+        const int32_t* vin = vals[(q + 1) & 1];
+        const int64_t fb = q == 0 ? fill_blocks : 0;
+        hipLaunchKernelGGL(embed_hist_kernel<ITEMS()>, dim3((unsigned)(p.nblk + fb)), block, 0, s,
+                           tk, kin, n, V, shift, digits, p.nblk, counts, list, dtable, fill_count);
+        hipLaunchKernelGGL(embed_scan_kernel<kThreads>, dim3((unsigned)digits), block, 0, s,
+                           counts, p.nblk, totals, nullptr);
+        hipLaunchKernelGGL(embed_scatter_kernel<ITEMS()>, dim3((unsigned)p.nblk), block, 0, s, tk,
+                           kin, vin, n, V, shift, p.rb, counts, totals, keys[q & 1], vals[q & 1]);
+      }
+    };
+    if (n <= kFewLimit) sort(IC<kFewItems>{});
+    else sort(IC<kManyItems>{});
     k = keys[(p.passes - 1) & 1];
     v = vals[(p.passes - 1) & 1];
     hipLaunchKernelGGL(embed_heads_kernel, dim3((unsigned)((p.nchunk + 3) / 4)), block, 0, s, k, n,

@@ -212,6 +212,61 @@ def test_embed_backward_non_finite_stays_in_its_row():
     assert torch.equal(torch.nan_to_num(dt, nan=-1.0), torch.nan_to_num(want, nan=-1.0))
 
 
+def test_embed_backward_of_the_largest_vocabulary():
+    V, n, d = 2**31 - 2, 5000, 9
+    rng = np.random.default_rng(4)
+    tok = rng.integers(0, V, n).astype(np.int32)
+    tok[::7] = tok[0]
+    tok[1], tok[2], tok[3] = V - 1, -1, 2**31 - 1
+    dout = to(rng.standard_normal((n, d)), "f32")
+    urows = torch.zeros(n, dtype=torch.int64, device=dev())
+    ugrad = torch.zeros(n, d, device=dev())
+    nu = torch.zeros(1, dtype=torch.int64, device=dev())
+    ws = torch.empty(pg.pg_embed_workspace_size(n, V, d), dtype=torch.uint8, device=dev())
+    pg.pg_embed_backward(dout, torch.from_numpy(tok).to(dev()), V, urows, ugrad, nu, ws)
+    ref_rows, ref, cnt, mag = ot.embed_rows(f64(dout), tok, V, 1.0)
+    k = nu.item()
+    assert np.array_equal(urows[:k].cpu().numpy(), ref_rows)
+    within(ugrad[:k], ref, (cnt[:, None] + 1) * U32 * mag)
+
+
+def test_rows_beyond_32_bit_offsets():
+    """Row strides of 2^30 elements, and a table of 2.4 G elements."""
+    g = torch.Generator(device=dev()).manual_seed(3)
+    n, d, ld = 3, 520, 1 << 30
+    buf = torch.empty(n * ld, dtype=torch.bfloat16, device=dev())
+    wide = buf.view(n, ld)[:, :d]
+    near = torch.randn(n, d, device=dev(), generator=g).bfloat16()
+    wide.copy_(near)
+    gamma = torch.ones(d, device=dev())
+    y, mean, rstd = torch.empty_like(near), torch.empty(n, device=dev()), torch.empty(n, device=dev())
+    pg.pg_layer_norm(near, gamma, None, y, mean=mean, rstd=rstd)
+    pg.pg_layer_norm(wide, gamma, None, wide)
+    assert torch.equal(wide, y)
+    ws = torch.empty(pg.pg_layer_norm_workspace_size(n, d), dtype=torch.uint8, device=dev())
+    dx, dg = torch.empty_like(near), torch.empty(d, device=dev())
+    pg.pg_layer_norm_backward(near, near, gamma, mean, rstd, dx, dg, None, ws)
+    wide.copy_(near)
+    pg.pg_layer_norm_backward(wide, near, gamma, mean, rstd, wide, dg, None, ws)
+    assert torch.equal(wide, dx)
+    V, d = 1_200_000, 2048
+    del buf, wide
+    table = torch.zeros(V, d, dtype=torch.bfloat16, device=dev())
+    tok = torch.tensor([V - 1, 0, V - 2, V - 1], dtype=torch.int32, device=dev())
+    rows = torch.randn(4, d, device=dev(), generator=g).bfloat16()
+    table[tok.long()] = rows
+    out = torch.empty(4, d, dtype=torch.bfloat16, device=dev())
+    pg.pg_embed(pg.make_table(pg.PG_BF16, table, V), tok, out)
+    assert torch.equal(out, table[tok.long()])
+    del table
+    dt = torch.full((V, d), 3.0, device=dev())
+    ws = torch.empty(pg.pg_embed_workspace_size(4, V, d), dtype=torch.uint8, device=dev())
+    pg.pg_embed_backward_dense(rows, tok, dt, ws)
+    assert torch.equal(dt[V - 1], rows[0].float() + rows[3].float())
+    assert torch.equal(dt[0], rows[1].float()) and torch.equal(dt[V - 2], rows[2].float())
+    assert int(torch.count_nonzero(dt)) <= 3 * d
+
+
 # ---------------------------------------------------------------------------
 # Layer norm
 

@@ -112,7 +112,8 @@ def test_orthogonalize_refusals():
     # other admissible polynomials, and no matrices at all
     for coef in ((1.5, -0.5, 0.0), (1.875, -1.25, 0.375), (2.0, -1.5, 0.5)):
         check("pg_orthogonalize", {**good, **dict(zip("abc", coef))}, [(dict(n=0), pg.PG_OK)])
-    for bad, status in (((-1, 5, 5), E), ((1, 0, 5), E), ((1, 5, 16385), U), ((65536, 5, 5), R)):
+    for bad, status in (((-1, 5, 5), E), ((1, 0, 5), E), ((1, 5, 16385), U), ((65536, 5, 5), R),
+                        ((65, 16384, 16384), R)):
         with pytest.raises(pg.PagegramError) as err:
             pg.pg_orthogonalize_workspace_size(*bad)
         assert err.value.status == status
