@@ -28,9 +28,10 @@
 // direct global-to-LDS loads, rows swizzled so that fragment reads meet no
 // bank conflicts; v_mfma_f32_32x32x16_f16, with the Q fragment as its A
 // operand, so a lane's accumulators are runs of four consecutive columns of
-// one row. The epilogue works on the accumulators where they are: rows leave
-// as 16-byte stores after one exchange between the half waves, transposed
-// ones as 8-byte stores after a 4 x 4 transpose inside quads of lanes.
+// one row. The epilogue passes each 32 x 32 block through a patch of LDS that
+// is the wave's own, so that rows and, for the mirrored and transposed copies,
+// columns leave in whole runs: stores straight from the accumulators, 16 to
+// 32 bytes a row, took up to 3.4 of a small product's 9 us.
 //
 // Matrices of up to 64 x 256 take one launch instead of 3 steps + 2: a block
 // holds its matrix in LDS through all steps. There the operands are split
@@ -189,50 +190,6 @@ __device__ __forceinline__ void ring_barrier() {
 }
 
 
-template <int CTRL>
-__device__ __forceinline__ uint32_t quad_move(uint32_t x) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
-}
-
-// 4 x 4 transpose of 16-bit values inside quads of lanes: lane q holds its
-// row's columns 0..3 as (lo, hi) pairs and gets column q of rows 0..3.
-__device__ __forceinline__ uint2 quad_transpose(uint32_t lo, uint32_t hi, int lane) {
-  const uint32_t nl = quad_move<0xB1>(lo), nh = quad_move<0xB1>(hi);   // lane ^ 1
-  const bool odd = lane & 1;
-  const uint32_t l = odd ? (nl >> 16) | (lo & 0xFFFF0000u) : (lo & 0xFFFFu) | (nl << 16);
-  const uint32_t h = odd ? (nh >> 16) | (hi & 0xFFFF0000u) : (hi & 0xFFFFu) | (nh << 16);
-  const uint32_t fl = quad_move<0x4E>(l), fh = quad_move<0x4E>(h);     // lane ^ 2
-  return (lane & 2) ? make_uint2(fh, h) : make_uint2(l, fl);
-}
-
-// The 16 accumulators of one lane of a 32 x 32 tile, as 16-bit pairs
-// w[g][0..1]: row lane % 32, columns 8 g + 4 (lane / 32) + 0..3.
-struct Tile16 {
-  uint32_t w[4][2];
-};
-
-// dst[row][col..]: 16-byte stores, two 32-byte runs a row. ld in elements.
-__device__ __forceinline__ void store_rows(uint16_t* dst, int64_t ld, const Tile16& t, int lane) {
-#pragma unroll
-  for (int g = 0; g < 4; g += 2) {
-    // lanes below 32 get columns 8 g .. 8 g + 7, the others the next eight
-    const auto a = __builtin_amdgcn_permlane32_swap(t.w[g][0], t.w[g + 1][0], false, false);
-    const auto b = __builtin_amdgcn_permlane32_swap(t.w[g][1], t.w[g + 1][1], false, false);
-    *reinterpret_cast<uint4*>(dst + (lane & 31) * ld + 8 * g + 8 * (lane >> 5)) =
-        make_uint4(a[0], b[0], a[1], b[1]);
-  }
-}
-
-// dst[col][row..]: 8-byte stores, 64-byte runs a column.
-__device__ __forceinline__ void store_cols(uint16_t* dst, int64_t ld, const Tile16& t, int lane) {
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const uint2 v = quad_transpose(t.w[g][0], t.w[g][1], lane);
-    const int c = 8 * g + 4 * (lane >> 5) + (lane & 3);
-    *reinterpret_cast<uint2*>(dst + c * ld + (lane & 28)) = v;
-  }
-}
-
 // BM x BN tile of P Q^T by KS groups of WM x WN waves; S stages in the ring, a
 // stage being 64 of K for each group. Two groups halve the chain of stages of
 // a small product, whose time is latency; their sums are joined at the end.
@@ -310,32 +267,44 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
       qf[b] = *reinterpret_cast<const f16x8_t*>(sq + (wn * TN + b * 32 + fr) * 128 + c);
   };
 
-  // What the epilogue reads is fetched before the first stage, where the
-  // registers hold it (PRE): a load behind the epilogue's stores waits for
-  // them, tile after tile.
+  // In the epilogue a lane has, of each 32 x 32 block, rows er + 8 p and
+  // columns ec .. ec + 3: eight lanes a row. What it reads there is fetched
+  // before the first stage, where the registers hold it (PRE), otherwise one
+  // block ahead: a load behind stores waits for them.
+  const int er = lane >> 3, ec = (lane & 7) * 4;
   constexpr bool PRE = FM * FN <= 4;
-  const int half = lane >> 5;
   uint2 oin[MODE == NS_POLY ? FM : 1][MODE == NS_POLY ? FN : 1][4];
-  float4 xin[MODE == NS_UPDATE ? FM : 1][MODE == NS_UPDATE ? FN : 1][4];
-  float4 djin[MODE == NS_POLY ? FN : 1][4];
-  float din[FM];
+  float4 xin[MODE == NS_UPDATE ? (PRE ? FM * FN : 2) : 1][4];
+  float4 djin[FN];
+  float din[FM][4];
+  auto fetch_x = [&](int t) {
+    if constexpr (MODE == NS_UPDATE) {
+      const int i = i0 + wm * TM + t / FN * 32 + er, j = j0 + wn * TN + t % FN * 32 + ec;
 #pragma unroll
-  for (int a = 0; a < FM && ks == 0; ++a) {
-    const int i = i0 + wm * TM + a * 32 + fr;
-    if constexpr (MODE == NS_POLY) din[a] = g.D[mat * g.mp + i];
-    if constexpr (MODE == NS_UPDATE) din[a] = g.a + g.E[mat * g.mp + i];
+      for (int p = 0; p < 4; ++p)
+        xin[PRE ? t : t & 1][p] =
+            *reinterpret_cast<const float4*>(g.X + mn + (int64_t)(i + 8 * p) * g.np + j);
+    }
+  };
+  if (ks == 0) {
 #pragma unroll
-    for (int b = 0; b < FN; ++b)
+    for (int a = 0; a < FM; ++a)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int jq = j0 + wn * TN + b * 32 + 8 * q + 4 * half;
-        if constexpr (MODE == NS_POLY) {
-          oin[a][b][q] = *reinterpret_cast<const uint2*>(g.O + mm + (int64_t)i * g.mp + jq);
-          if (a == 0) djin[b][q] = *reinterpret_cast<const float4*>(g.D + mat * g.mp + jq);
-        }
-        if constexpr (MODE == NS_UPDATE && PRE)
-          xin[a][b][q] = *reinterpret_cast<const float4*>(g.X + mn + (int64_t)i * g.np + jq);
+      for (int p = 0; p < 4; ++p) {
+        const int i = i0 + wm * TM + a * 32 + er + 8 * p;
+        if constexpr (MODE == NS_POLY) din[a][p] = g.D[mat * g.mp + i];
+        if constexpr (MODE == NS_UPDATE) din[a][p] = g.a + g.E[mat * g.mp + i];
+        if constexpr (MODE == NS_POLY)
+#pragma unroll
+          for (int b = 0; b < FN; ++b) {
+            const int j = j0 + wn * TN + b * 32 + ec;
+            oin[a][b][p] = *reinterpret_cast<const uint2*>(g.O + mm + (int64_t)i * g.mp + j);
+            if (a == 0 && p == 0)
+              djin[b] = *reinterpret_cast<const float4*>(g.D + mat * g.mp + j);
+          }
       }
+#pragma unroll
+    for (int t = 0; t < (PRE ? FM * FN : 1); ++t) fetch_x(t);
   }
 
   // one tile a wave: two accumulators in turn, so products need not wait
@@ -391,10 +360,12 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
   if constexpr (AC == 2)
 #pragma unroll
     for (int q = 0; q < 16; ++q) acc[0][0][q] += sums[1][0][0][q];
+  __syncthreads();                                   // the ring is read; now it is scratch
+  constexpr int kLd = 36;                            // floats of a patch row: no bank conflicts
+  float* patch = reinterpret_cast<float*>(ring) + wave * 32 * kLd;
   if constexpr (KS == 2) {                           // the second group's sums, by way of LDS
-    static_assert(FM * FN == 1 && NW * 4096 <= S * KS * kStage, "join");
-    float* j = reinterpret_cast<float*>(ring) + wave * 1024 + lane;
-    __syncthreads();
+    static_assert(FM * FN == 1 && NW * (32 * kLd + 1024) * 4 <= S * KS * kStage, "join");
+    float* j = reinterpret_cast<float*>(ring) + NW * 32 * kLd + wave * 1024 + lane;
     if (ks == 1)
 #pragma unroll
       for (int q = 0; q < 16; ++q) j[64 * q] = acc[0][0][q];
@@ -404,113 +375,112 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
     for (int q = 0; q < 16; ++q) acc[0][0][q] += j[64 * q];
   }
 
-  // Epilogue, one 32 x 32 tile after the other: stores only.
+  // Epilogue, one 32 x 32 block after the other.
+  const int half = lane >> 5;
+  const bool tall = g.rows > g.cols;
+  auto halves = [](const float (&f)[4]) {
+    return make_uint2(pack_half(f[0], f[1]), pack_half(f[2], f[3]));
+  };
+  // four of the result's values from column c of row r on, inside its edges
+  auto put_out = [&](int r, int c, const float (&f)[4]) {
+    if (r >= g.rows) return;
+    const uint2 v = make_uint2(pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]));
+    uint16_t* dst = g.out + mat * g.rows * g.cols + (int64_t)r * g.cols + c;
+    if (c + 4 <= g.cols) {
+      __builtin_memcpy(dst, &v, 8);
+    } else {
 #pragma unroll
-  for (int a = 0; a < FM; ++a) {
-    const int ib = i0 + wm * TM + a * 32, i = ib + fr;
-    const float di = MODE == NS_GRAM ? 0.f : din[a];
+      for (int u = 0; u < 4; ++u)
+        if (c + u < g.cols) dst[u] = (uint16_t)(((u & 2) ? v.y : v.x) >> (16 * (u & 1)));
+    }
+  };
+#pragma unroll
+  for (int a = 0; a < FM; ++a)
 #pragma unroll
     for (int b = 0; b < FN; ++b) {
-      const int jb = j0 + wn * TN + b * 32;
-      Tile16 w;
-      if constexpr (MODE == NS_GRAM) {
-        if (ib == jb) {                              // the tile of the diagonal
+      const int t = a * FN + b;
+      const int ib = i0 + wm * TM + a * 32, jb = j0 + wn * TN + b * 32;
+      if (!PRE && t + 1 < FM * FN) fetch_x(t + 1);
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            const int j = jb + 8 * (q >> 2) + 4 * half + (q & 3);
-            if (i == j) {
-              g.D[mat * g.mp + i] = acc[a][b][q] * (1.f / (kSX * kSX));
-              acc[a][b][q] = 0.f;
-            }
-          }
-        }
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float4*>(patch + fr * kLd + 8 * q + 4 * half) =
+            make_float4(acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2],
+                        acc[a][b][4 * q + 3]);
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            w.w[q][u] = pack_half(acc[a][b][4 * q + 2 * u] * (kSO / (kSX * kSX)),
-                                  acc[a][b][4 * q + 2 * u + 1] * (kSO / (kSX * kSX)));
-      } else if constexpr (MODE == NS_POLY) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int jq = jb + 8 * q + 4 * half;
-          const uint2 ow = oin[a][b][q];
-          const float4 dj = djin[b][q];
-          const float djs[4] = {dj.x, dj.y, dj.z, dj.w};
-          float f[4];
+      for (int p = 0; p < 4; ++p) {
+        const int i = ib + er + 8 * p, j = jb + ec;
+        float4* slot = reinterpret_cast<float4*>(patch + (er + 8 * p) * kLd + ec);
+        const float4 s4 = *slot;
+        const float v[4] = {s4.x, s4.y, s4.z, s4.w};
+        float f[4];
+        if constexpr (MODE == NS_GRAM) {
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const uint32_t bits = ((u & 2) ? ow.y : ow.x) >> (16 * (u & 1));
+            f[u] = v[u] * (kSO / (kSX * kSX));
+            if (ib == jb && i == j + u) {            // the diagonal
+              g.D[mat * g.mp + i] = v[u] * (1.f / (kSX * kSX));
+              f[u] = 0.f;
+            }
+          }
+          *reinterpret_cast<uint2*>(g.O + mm + (int64_t)i * g.mp + j) = halves(f);
+        } else if constexpr (MODE == NS_POLY) {
+          const float di = din[a][p];
+          const float dj[4] = {djin[b].x, djin[b].y, djin[b].z, djin[b].w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t bits = ((u & 2) ? oin[a][b][p].y : oin[a][b][p].x) >> (16 * (u & 1));
             const float o = (float)__builtin_bit_cast(_Float16, (uint16_t)bits) * (1.f / kSO);
-            const float aa = acc[a][b][4 * q + u] * (1.f / (kSO * kSO));
-            f[u] = ((g.b + g.c * (di + djs[u])) * o + g.c * aa) * kSF;
-            if (ib == jb && i == jq + u) {
+            const float aa = v[u] * (1.f / (kSO * kSO));
+            f[u] = ((g.b + g.c * (di + dj[u])) * o + g.c * aa) * kSF;
+            if (ib == jb && i == j + u) {
               g.E[mat * g.mp + i] = g.b * di + g.c * (aa + di * di);
               f[u] = 0.f;
             }
           }
-          w.w[q][0] = pack_half(f[0], f[1]);
-          w.w[q][1] = pack_half(f[2], f[3]);
-        }
-      } else {
-        float* X = g.X + mn + (int64_t)i * g.np;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int jq = jb + 8 * q + 4 * half;
-          const float4 x = PRE ? xin[a][b][q] : *reinterpret_cast<const float4*>(X + jq);
-          const float y[4] = {di * x.x + acc[a][b][4 * q] * (1.f / (kSF * kSX)),
-                              di * x.y + acc[a][b][4 * q + 1] * (1.f / (kSF * kSX)),
-                              di * x.z + acc[a][b][4 * q + 2] * (1.f / (kSF * kSX)),
-                              di * x.w + acc[a][b][4 * q + 3] * (1.f / (kSF * kSX))};
-          if (g.out) {                               // bf16 result, no more copies
-            w.w[q][0] = pack2_bf16(g.scale * y[0], g.scale * y[1]);
-            w.w[q][1] = pack2_bf16(g.scale * y[2], g.scale * y[3]);
-          } else {
-            *reinterpret_cast<float4*>(X + jq) = make_float4(y[0], y[1], y[2], y[3]);
-            w.w[q][0] = pack_half(y[0] * kSX, y[1] * kSX);
-            w.w[q][1] = pack_half(y[2] * kSX, y[3] * kSX);
-          }
-        }
-      }
-      if constexpr (MODE == NS_UPDATE) {
-        if (g.out) {
-          // rows x cols without padding: X or, for a tall matrix, its transpose
-          const bool tall = g.rows > g.cols;
-          uint16_t* o = g.out + mat * g.rows * g.cols;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint2 v = make_uint2(w.w[q][0], w.w[q][1]);
-            int r = i, c = jb + 8 * q + 4 * half;
-            if (tall) {
-              v = quad_transpose(v.x, v.y, lane);
-              r = c + (lane & 3);
-              c = ib + (lane & 28);
-            }
-            if (r >= g.rows) continue;
-            uint16_t* dst = o + (int64_t)r * g.cols + c;
-            if (c + 4 <= g.cols) {
-              __builtin_memcpy(dst, &v, 8);
-            } else {
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                if (c + u < g.cols)
-                  dst[u] = (uint16_t)(((u & 2) ? v.y : v.x) >> (16 * (u & 1)));
-            }
-          }
+          *reinterpret_cast<uint2*>(g.F + mm + (int64_t)i * g.mp + j) = halves(f);
         } else {
-          store_rows(reinterpret_cast<uint16_t*>(g.Xh + mn + (int64_t)ib * g.np + jb), g.np, w,
-                     lane);
-          store_cols(reinterpret_cast<uint16_t*>(g.Yh + mn + (int64_t)jb * g.mp + ib), g.mp, w,
-                     lane);
+          const float4 x = xin[PRE ? t : t & 1][p];
+          const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) f[u] = din[a][p] * xs[u] + v[u] * (1.f / (kSF * kSX));
+          if (g.out) {                               // the result, no more copies
+#pragma unroll
+            for (int u = 0; u < 4; ++u) f[u] *= g.scale;
+            if (!tall) put_out(i, j, f);
+          } else {
+            *reinterpret_cast<float4*>(g.X + mn + (int64_t)i * g.np + j) =
+                make_float4(f[0], f[1], f[2], f[3]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) f[u] *= kSX;
+            *reinterpret_cast<uint2*>(g.Xh + mn + (int64_t)i * g.np + j) = halves(f);
+          }
         }
-      } else {
-        _Float16* m = (MODE == NS_GRAM ? g.O : g.F) + mm;
-        store_rows(reinterpret_cast<uint16_t*>(m + (int64_t)ib * g.mp + jb), g.mp, w, lane);
-        if (bj < bi)                                 // the mirrored tile
-          store_cols(reinterpret_cast<uint16_t*>(m + (int64_t)jb * g.mp + ib), g.mp, w, lane);
+        *slot = make_float4(f[0], f[1], f[2], f[3]);
       }
+      __builtin_amdgcn_wave_barrier();
+      // columns: the mirrored block, the transpose, or a tall matrix's result
+      const bool cols = MODE == NS_UPDATE ? !g.out || tall : bi != bj;
+      if (cols) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const int j = jb + er + 8 * p, i = ib + ec;
+          float f[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) f[u] = patch[(ec + u) * kLd + er + 8 * p];
+          if constexpr (MODE == NS_UPDATE) {
+            if (g.out)
+              put_out(j, i, f);
+            else
+              *reinterpret_cast<uint2*>(g.Yh + mn + (int64_t)j * g.mp + i) = halves(f);
+          } else {
+            _Float16* m = (MODE == NS_GRAM ? g.O : g.F) + mm;
+            *reinterpret_cast<uint2*>(m + (int64_t)j * g.mp + i) = halves(f);
+          }
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
     }
-  }
 }
 
 // ---------------------------------------------------------------------------
