@@ -189,7 +189,6 @@ __device__ __forceinline__ void ring_barrier() {
   asm volatile("" ::: "memory");
 }
 
-
 // BM x BN tile of P Q^T by KS groups of WM x WN waves; S stages in the ring, a
 // stage being 64 of K for each group. Two groups halve the chain of stages of
 // a small product, whose time is latency; their sums are joined at the end.
