@@ -108,7 +108,7 @@ __device__ __forceinline__ void fill_zero(float* __restrict__ p, int64_t count, 
 }
 
 // counts[digit * nblk + b] = keys of block b's tile with that digit. The
-// first pass reads the tokens themselves and clears the join list's counter;
+// first pass reads the tokens themselves and clears the join lists' counters;
 // blocks behind the nblk tiles clear the dense gradient.
 template <int kItems>
 __global__ __launch_bounds__(kThreads) void embed_hist_kernel(
@@ -141,8 +141,8 @@ __global__ __launch_bounds__(kThreads) void embed_hist_kernel(
 // goes to totals[blockIdx.x], and as n_unique to a caller who wants it.
 template <int NT>
 __global__ __launch_bounds__(NT) void embed_scan_kernel(int32_t* __restrict__ a, int64_t m,
-                                                              int32_t* __restrict__ totals,
-                                                              int64_t* __restrict__ n_unique) {
+                                                        int32_t* __restrict__ totals,
+                                                        int64_t* __restrict__ n_unique) {
   __shared__ int32_t sh[NT / 64];
   int32_t* row = a + (int64_t)blockIdx.x * m;
   int32_t run = 0;

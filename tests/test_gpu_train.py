@@ -631,6 +631,22 @@ def test_training_step_together():
     assert np.max(np.abs(f64(theta) - want)) < 1e-5
 
 
+def test_explicit_stream():
+    """stream= overrides the current stream (a torch stream or its handle)."""
+    x = torch.randn(7, 40, device=dev())
+    gamma = torch.rand(40, device=dev())
+    want = torch.empty_like(x)
+    pg.pg_layer_norm(x, gamma, None, want)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for how in (s, s.cuda_stream):
+        y = torch.zeros_like(x)
+        torch.cuda.synchronize()
+        pg.pg_layer_norm(x, gamma, None, y, stream=how)
+        s.synchronize()
+        assert torch.equal(y, want)
+
+
 def test_training_step_captured_and_on_another_stream():
     """The captured step replays to the eager result, with eager work on the
     same buffers in between; a second step runs on its own stream meanwhile."""
