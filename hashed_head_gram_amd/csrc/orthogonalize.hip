@@ -705,14 +705,13 @@ hipError_t launch_orthogonalize(const OrthoPlan& p, const void* G, int32_t dtype
   if (dtype == PG_F32) load(static_cast<const float*>(G));
   else load(static_cast<const uint16_t*>(G));
   // The tile of a product: the largest that leaves a chip of 256 compute units
-  // about a block each. Larger tiles read operands less often, smaller ones
-  // start more work at once. Measured, us of a whole call: 256 x 256 updates
-  // against 128 x 128 at 256 blocks (4096 x 4096) 1954 to 2035, at 100 (two
-  // 2560 x 1280) 508 to 389; 128 x 128 against 64 x 64 at 200 blocks (one
-  // 2560 x 1280) 246 to 272, at 100 (one 1280 x 1280) 210 to 173. Up to 256
-  // blocks of 64 x 64 two groups of waves share a tile's K (768 x 1024: 124
-  // to 131); beyond, two blocks share a compute unit instead (32 of 256 x
-  // 256: 117 to 147).
+  // work for most of them. Larger tiles read operands less often, smaller ones
+  // start more work at once. Measured, us of a whole call with and without:
+  // 256 x 256 updates at 256 blocks (4096 x 4096) 1853 and 1988, at 100 (two
+  // 2560 x 1280) 405 and 340; 128 x 128 at 136 blocks (2048 x 2048) 408 and
+  // 429, at 128 (32 of 256 x 256) 125 and 111. Up to 256 blocks of 64 x 64 two
+  // groups of waves share a tile's K (768 x 1024: 121 and 131); beyond, two
+  // blocks share a compute unit instead (32 of 256 x 256: 111 and 138).
   auto launch = [&](auto MODE, const NsArgs& args) {
     constexpr bool UPDATE = MODE() == NS_UPDATE;
     NsArgs g = args;
@@ -729,7 +728,7 @@ hipError_t launch_orthogonalize(const OrthoPlan& p, const void* G, int32_t dtype
     if constexpr (UPDATE)
       if (p.mp % 256 == 0 && p.np % 256 == 0 && blocks(256) >= 200)
         return go(IC<256>{}, IC<2>{}, IC<4>{}, IC<2>{}, IC<1>{});
-    if (blocks(128) >= 192) return go(IC<128>{}, IC<2>{}, IC<2>{}, IC<2>{}, IC<1>{});
+    if (blocks(128) > 128) return go(IC<128>{}, IC<2>{}, IC<2>{}, IC<2>{}, IC<1>{});
     if (blocks(64) > 256) return go(IC<64>{}, IC<2>{}, IC<2>{}, IC<4>{}, IC<1>{});
     go(IC<64>{}, IC<2>{}, IC<2>{}, IC<3>{}, IC<2>{});
   };
