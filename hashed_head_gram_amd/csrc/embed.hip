@@ -209,9 +209,9 @@ __global__ __launch_bounds__(kThreads) void embed_scatter_kernel(
     int before = 0;
     if (live) before = wcnt[wave][dg];
     rank[q] = before + __popcll(below);
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     if (live && below == 0) wcnt[wave][dg] = before + __popcll(same);
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
   }
   __syncthreads();
   // first output position of (digit, wave): digit base + block offset + the
@@ -308,9 +308,9 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(
       int before = 0;
       if (live) before = wcnt[wave][dg];
       rank[q] = before + __popcll(below);
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
       if (live && below == 0) wcnt[wave][dg] = (uint16_t)(before + __popcll(same));
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
     }
     __syncthreads();
     int sum = 0;
@@ -566,8 +566,8 @@ constexpr int kShortParts = 8;
 // of the row that starts in c and goes on; such a chunk joins a list of the
 // second kernel: rows that reach chunk c + kShortParts (list[0] of them, from
 // list[2] on) or shorter ones (list[1], from the list's end back), each in any
-// order, for every entry is a row summed by itself. keys and vals are readable to a multiple of
-// 8 entries.
+// order, for every entry is a row summed by itself. keys and vals are readable
+// to a multiple of 8 entries.
 template <typename T, int L, int MODE, bool PARTS>
 __global__ __launch_bounds__(kThreads) void embed_reduce_kernel(
     const T* __restrict__ dout, int64_t ld, const uint32_t* __restrict__ keys,

@@ -405,7 +405,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
         *reinterpret_cast<float4*>(patch + fr * kLd + 8 * q + 4 * half) =
             make_float4(acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2],
                         acc[a][b][4 * q + 3]);
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         const int i = ib + er + 8 * p, j = jb + ec;
@@ -457,7 +457,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
         }
         *slot = make_float4(f[0], f[1], f[2], f[3]);
       }
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
       // columns: the mirrored block, the transpose, or a tall matrix's result
       const bool cols = MODE == NS_UPDATE ? !g.out || tall : bi != bj;
       if (cols) {
@@ -478,7 +478,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
           }
         }
       }
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
     }
 }
 

@@ -37,8 +37,13 @@ struct Raw8<uint16_t> {
   }
 };
 
-__device__ __forceinline__ float elt_f32(float x) { return x; }
-__device__ __forceinline__ float elt_f32(uint16_t x) { return bf16_to_f32(x); }
+// Between a wave's LDS writes and reads of them by its other lanes: orders the
+// accesses for the compiler (a wave's LDS operations take effect in order).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // Part vectors move single elements, whole ones 16 bytes at a time. STREAM
 // marks data that this call touches once and that is larger than the caches
