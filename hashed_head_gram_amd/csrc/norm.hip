@@ -355,20 +355,22 @@ void with_geometry(int d, F f) {
 }
 
 // Blocks that walk n rows: enough to fill the chip's 256 compute units
-// `waves` waves deep, no more than there are rows. 131,072 rows of 2,560 bf16:
+// `waves` waves deep, no more than there are rows, and past one block a unit
+// `per` rows a group or more. 131,072 rows of 2,560 bf16:
 // forward 296, 264 and 316 us at 15, 20 and 30 waves, backward 511, 490, 512
 // and 542 us at 10, 15, 20 and 30.
 template <int L, int W>
 int64_t norm_blocks(int64_t n, int waves, int per) {
   constexpr int NT = kNormThreads<W>;
   constexpr int64_t ROWS = NT / (L * W);
-  const int64_t need = (n + ROWS * per - 1) / (ROWS * per), cap = 256 * (int64_t)(waves * 64 / NT);
-  return need < cap ? need : cap;
+  const int64_t one = (n + ROWS - 1) / ROWS, few = (one + per - 1) / per;
+  const int64_t need = std::min<int64_t>(one, std::max<int64_t>(few, 256));
+  return std::min<int64_t>(need, 256 * (int64_t)(waves * 64 / NT));
 }
 constexpr int kForwardWaves = 20, kBackwardWaves = 15;
-// Rows a backward group takes before another block starts: each block's
-// partial row costs as much as two thirds of a bf16 row of all four tensors
-// (4,095 rows of 1,001 fp32: 22, 20, 23 and 31 us at 2, 4, 8 and 16).
+// Rows a backward group takes before a block beyond the 256th starts: each
+// block's partial row costs as much as two thirds of a bf16 row of all four
+// tensors (4,095 rows of 1,001 fp32: 22, 20, 23 and 31 us at 2, 4, 8 and 16).
 constexpr int kBackwardRows = 4;
 
 }  // namespace
