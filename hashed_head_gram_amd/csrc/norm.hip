@@ -185,8 +185,12 @@ __global__ __launch_bounds__(kNormThreads<W>) void norm_backward_kernel(
   const float fd = (float)d;
   const int64_t stride = (int64_t)gridDim.x * G::ROWS;
   int64_t r = (int64_t)blockIdx.x * G::ROWS + grp;
+  // four vectors a lane of fp32 leave no registers for a third prefetched
+  // tensor (123 spilled): add is then read where it is added. 4,000 rows of
+  // 12,288: 165 us (4.8 TB/s), 261 prefetched; bf16 holds it and takes 98
+  constexpr bool LATE = ADD && CH == 4 && sizeof(T) == 4;
   struct Row {
-    Raw8<T> x[CH], y[CH], a[ADD ? CH : 1];
+    Raw8<T> x[CH], y[CH], a[ADD && !LATE ? CH : 1];
     float mu, rs;
   };
   auto fetch = [&](int64_t row, Row& v) {
@@ -199,7 +203,7 @@ __global__ __launch_bounds__(kNormThreads<W>) void norm_backward_kernel(
       const int c = c0 + G::STEP * k, left = live ? d - c : 0;
       v.x[k] = load8<true>(x + rc * ldx + c, left);
       v.y[k] = load8<true>(dy + rc * lddy + c, left);
-      if constexpr (ADD) v.a[k] = load8<true>(add + rc * ldadd + c, left);
+      if constexpr (ADD && !LATE) v.a[k] = load8<true>(add + rc * ldadd + c, left);
     }
   };
   Row v;
@@ -257,12 +261,15 @@ __global__ __launch_bounds__(kNormThreads<W>) void norm_backward_kernel(
         const int c = c0 + G::STEP * k;
         if (c >= d) continue;
         const Raw8<float> gm = staged(sg, c >> 3);
+        Raw8<T> a{};
+        if constexpr (LATE) a = load8<true>(add + r * ldadd + c, d - c);
+        else if constexpr (ADD) a = v.a[k];
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float xh = (v.x[k].get(i) - v.mu) * v.rs;
           o[i] = v.rs * (v.y[k].get(i) * gm.v[i] - m1 - xh * m2);
-          if constexpr (ADD) o[i] += v.a[k].get(i);
+          if constexpr (ADD) o[i] += a.get(i);
         }
         store8<true>(dx + r * lddx + c, o, d - c);
       }

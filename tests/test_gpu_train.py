@@ -279,7 +279,8 @@ NORM = [(1, 1, "f32", 0, 0), (5, 2, "bf16", 0, 0), (3, 7, "bf16", 1, 1), (100, 6
         (33, 2048, "bf16", 0, 0), (50, 2560, "bf16", 0, 0), (50, 2560, "f32", 0, 0),
         (11, 2561, "bf16", 0, 1), (6, 4096, "f32", 0, 0), (5, 4100, "bf16", 0, 0),
         (4, 8192, "bf16", 0, 0), (3, 8199, "f32", 0, 1), (3, 16384, "bf16", 0, 0),
-        (5000, 72, "bf16", 0, 0), (5003, 384, "f32", 0, 0)]
+        (5000, 72, "bf16", 0, 0), (5003, 384, "f32", 0, 0), (600, 5001, "f32", 0, 1),
+        (600, 12001, "f32", 0, 0), (520, 12001, "bf16", 1, 0)]
 DEPTH = 66     # deepest row sum: 40 terms a lane, 6 lane steps, 16 waves, the division
 
 
