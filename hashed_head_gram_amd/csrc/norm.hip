@@ -401,7 +401,9 @@ hipError_t launch_layer_norm(const void* x, int32_t dtype, int64_t n, int d, int
 
 int64_t layer_norm_partials(int64_t n, int d) {
   int64_t blocks = 0;
-  with_geometry(d, [&](auto L, auto W, auto) { blocks = norm_blocks<L(), W()>(n, kBackwardWaves, kBackwardRows); });
+  with_geometry(d, [&](auto L, auto W, auto) {
+    blocks = norm_blocks<L(), W()>(n, kBackwardWaves, kBackwardRows);
+  });
   return blocks;
 }
 

@@ -711,10 +711,11 @@ PG_API int64_t pg_orthogonalize_workspace_size(int64_t n_mat, int32_t rows,
  *   G    [n_mat][rows][cols] of dtype; out bf16 of the same shape
  *   1 <= rows, cols <= 16384 (PG_EUNSUPPORTED beyond); n_mat <= 65535 and at
  *   most 2^34 elements with rows and cols rounded up to multiples of 128
- *   (PG_ERANGE); 1 <= steps <= 64. The products run in fp16 with fp32 accumulation, the
- *   iterate and the diagonals in fp32 (matrices small enough for one compute
- *   unit's memory: all of it in fp32). Coefficients under which a singular
- *   value in [0, 1] could pass 3 before a step, or b s^2 + c s^4 pass 100 in
+ *   (PG_ERANGE); 1 <= steps <= 64. The products run in fp16 with fp32
+ *   accumulation, the iterate and the diagonals in fp32; matrices small
+ *   enough for one compute unit's memory take each operand as two fp16
+ *   halves, about 22 bits. Coefficients under which a singular value in
+ *   [0, 1] could pass 3 before a step, or b s^2 + c s^4 pass 100 in
  *   magnitude, are refused (PG_EUNSUPPORTED).
  *   workspace of pg_orthogonalize_workspace_size bytes, 256-byte aligned
  */
