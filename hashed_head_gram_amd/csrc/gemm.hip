@@ -110,9 +110,11 @@ __device__ __forceinline__ void wait_vmcnt() {
 // sides by compiler-only memory barriers; volatile asm keeps its order.
 // The address is a wave-uniform base (SGPR pair) plus a per-lane 32-bit
 // byte offset, so a stage's loads hold one VGPR per lane instead of a 64-bit
-// pointer per instruction.
+// pointer per instruction. s_nop: a load that reads M0 needs a wait state
+// behind the write of M0 (five behind a v_readlane that restores the base),
+// which the compiler, seeing no load in the asm, does not add.
 __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds));
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds));
 }
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {

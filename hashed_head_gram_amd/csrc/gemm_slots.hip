@@ -78,12 +78,13 @@ __device__ __forceinline__ void wait_vm() {
 // Direct global->LDS load (see gemm.hip): 16 bytes per lane from base + off,
 // the wave's 1 KiB to LDS address lds (M0). Not tracked by the compiler's
 // wait counting; the ring orders it with explicit vmcnt waits and barriers.
+// s_nop: the wait state behind the write of M0.
 __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds));
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds));
 }
 // The same with 4 bytes per lane (the wave's 256 bytes to LDS address lds).
 __device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("global_load_lds_dword %0, %1" : : "v"(off), "s"(base), "{m0}"(lds));
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(base), "{m0}"(lds));
 }
 
 __device__ __forceinline__ uint32_t lds_u32(const void* p) {

@@ -178,9 +178,11 @@ __device__ __forceinline__ void wait_loads() {
 
 // Direct global-to-LDS load: each lane moves 16 bytes from base + off; the
 // wave writes 1 KiB at LDS address lds + 16 lane. No memory clobber: the ring
-// orders it with counted waits and barriers.
+// orders it with counted waits and barriers. s_nop: a load that reads M0 needs
+// a wait state behind the write of M0, which the compiler, seeing no load in
+// the asm, does not add.
 __device__ __forceinline__ void load_to_lds(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds));
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds));
 }
 
 __device__ __forceinline__ void ring_barrier() {
