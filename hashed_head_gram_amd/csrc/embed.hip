@@ -786,21 +786,27 @@ EmbedPlan embed_plan(int64_t n, int64_t V, int d) {
   while (((int64_t)1 << p.bits) <= V) ++p.bits;      // keys 0 .. V
   p.passes = (p.bits + kMaxDigitBits - 1) / kMaxDigitBits;
   p.rb = (p.bits + p.passes - 1) / p.passes;
-  const int64_t tile = kThreads * (n <= kFewLimit ? kFewItems : kManyItems);
+  const int64_t few = kThreads * kFewItems, tile = n <= kFewLimit ? few : kThreads * kManyItems;
   p.nblk = (n + tile - 1) / tile;
   const int64_t slabs = ((int64_t)d + 511) / 512;
   p.chunk = 64;
   const int64_t groups = 64 / embed_lanes(d);        // a wave's
   while (p.chunk > 8 && n / p.chunk * slabs < 2048 * groups) p.chunk /= 2;
   p.nchunk = (n + p.chunk - 1) / p.chunk;
+  // Room for what any smaller batch needs, whose tiles and chunks may be
+  // shorter and more: one workspace serves every batch up to the largest. A
+  // chunk of c < 64 is taken up to n / 2c = q - 1, so there are at most 2 q.
+  const int64_t q = (2048 * groups + slabs - 1) / slabs;
+  const int64_t chunks = std::max(p.nchunk, std::min((n + 7) / 8, 2 * q));
+  const int64_t tiles = std::max(p.nblk, (std::min(n, kFewLimit) + few - 1) / few);
   int64_t off = 0;
   for (int i = 0; i < 2; ++i) { p.off_keys[i] = off; off += al((n + 8) * 4); }
   for (int i = 0; i < 2; ++i) { p.off_vals[i] = off; off += al((n + 8) * 4); }
-  p.off_counts = off; off += al(((int64_t)1 << p.rb) * p.nblk * 4);
+  p.off_counts = off; off += al(((int64_t)1 << p.rb) * tiles * 4);
   p.off_totals = off; off += al((kMaxDigits + 1) * 4);
-  p.off_heads = off; off += al((p.nchunk + 1) * 4);
-  p.off_list = off; off += al((p.nchunk + 2) * 4);
-  p.off_part = off; off += al(2 * p.nchunk * embed_dpad(d) * 4);
+  p.off_heads = off; off += al((chunks + 1) * 4);
+  p.off_list = off; off += al((chunks + 2) * 4);
+  p.off_part = off; off += al(2 * chunks * embed_dpad(d) * 4);
   p.bytes = off;
   return p;
 }

@@ -625,7 +625,8 @@ PG_API int pg_embed(const pg_table* table, int32_t d, float scale,
 /*
  * pg_embed_workspace_size -- device workspace bytes of either gradient call
  * (negative pg_status for unsupported sizes: those of pg_embed, and V < 2^31
- * - 1).
+ * - 1). It does not fall as n_tok grows: a workspace sized for the largest
+ * batch serves every smaller one of the same V and d.
  */
 PG_API int64_t pg_embed_workspace_size(int64_t n_tok, int64_t V, int32_t d);
 
