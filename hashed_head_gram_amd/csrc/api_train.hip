@@ -71,20 +71,61 @@ double quintic_max(double a, double b, double c, double m) {
   return best;
 }
 
+// Largest |b t + c t^2| over t = s^2, 0 <= s <= m.
+double factor_max(double b, double c, double m) {
+  const double t = m * m;
+  const double best = fabs(b * t + c * t * t);
+  return c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < t ? fmax(best, fabs(b * b / (4 * c))) : best;
+}
+
 // Whether every iterate stays where the fp16 copies hold it: singular values
 // at most 3 before each step, |b t + c t^2| at most 100 for t = s^2.
 bool ortho_in_range(double a, double b, double c, int steps) {
   double m = 1.0;
   for (int k = 0; k < steps; ++k) {
     if (!(m <= 3.0)) return false;
-    const double t = m * m;
-    double best = fabs(b * t + c * t * t);
-    if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < t)
-      best = fmax(best, fabs(b * b / (4 * c)));
-    if (!(best <= 100.0)) return false;
+    if (!(factor_max(b, c, m) <= 100.0)) return false;
     m = quintic_max(a, b, c, m);
   }
   return m <= 100.0;
+}
+
+// Leading steps whose operands have to be split in halves. The rounding of the
+// fp16 operands of step k enters in proportion to B's size there and is moved
+// by the steps behind it as s is: their composed slope, largest on 33 points
+// of [0, m] (at 0 it is |a| a step). On spectra that suffer most (half the
+// directions 1e-2 to 1e-4 of the others), simulated in float64 with fp16
+// operands, the sum of size times slope over the steps moves the result by
+// 6.5e-6 of it in the 2-norm: 600 are half a step of the result's bf16, 2^-8.
+// Five steps of the usual coefficients come to 550. Where all steps together
+// pass 600, only the last ones stay unsplit, up to 120: by then the singular
+// values are large, and with them what is rounded.
+constexpr double kSumAll = 600, kSumLast = 120;
+int ortho_split(double a, double b, double c, int steps) {
+  double m[kMaxOrthoSteps + 1];
+  m[0] = 1.0;
+  for (int k = 0; k < steps; ++k) m[k + 1] = quintic_max(a, b, c, m[k]);
+  double sum = 0;
+  int last = 0;
+  for (int k = steps - 1; k >= 0; --k) {
+    const double size = factor_max(b, c, m[k]);
+    if (size > 0) {
+      double slope = 0;
+      for (int i = 0; i <= 32; ++i) {
+        double s = m[k + 1] * i / 32, g = 1;
+        for (int j = k + 1; j < steps; ++j) {
+          const double t = s * s;
+          g *= a + t * (3 * b + 5 * c * t);
+          s *= a + t * (b + c * t);
+        }
+        slope = fmax(slope, fabs(g));
+      }
+      sum += size * slope;
+    }
+    if (sum <= kSumLast) last = steps - k;
+    if (sum > kSumAll) return steps - last;
+  }
+  return 0;
 }
 
 }  // namespace
@@ -226,7 +267,7 @@ PG_API int pg_orthogonalize(const void* G, int32_t dtype, int64_t n_mat, int32_t
   if (!G || !out || !aligned(G, elt(dtype)) || !aligned(out, 2)) return PG_EINVAL;
   const pg::OrthoPlan p = pg::ortho_plan(n_mat, rows, cols);
   if (!workspace || workspace_bytes < p.bytes || !aligned(workspace, 256)) return PG_EINVAL;
-  const pg::OrthoArgs oa{steps, a, b, c, eps, scale};
+  const pg::OrthoArgs oa{steps, p.small ? 0 : ortho_split(a, b, c, steps), a, b, c, eps, scale};
   return hip_status(pg::launch_orthogonalize(p, G, dtype, n_mat, rows, cols, oa,
                                              static_cast<uint16_t*>(out), workspace, stream));
 }

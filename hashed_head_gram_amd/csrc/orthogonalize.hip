@@ -19,6 +19,17 @@
 //     at most 3, |b s^2 + c s^4| at most 100) and with subnormals below 2^-33.
 // bf16 operands, the usual choice, would be eight times coarser.
 //
+// Rounding that falls on directions G nearly lacks grows with them, up to |a|
+// times a step. Where a call's polynomial and steps let it grow past the
+// result's own rounding (ortho_split), the leading steps take every operand as
+// two fp16 halves, about 22 bits, and three products for one: hi hi, hi lo and
+// lo hi, as one K three times as long. Relative 2-norm before the result's
+// rounding, half the directions 1e-3 of the others, 256 x 1024: 5 steps 2.9e-3
+// in plain fp16; 8 steps 3.3e-2, with leading halves 1e-3. Such a step takes
+// about three times as long (ten of five 2560 x 1280: 2910 us, 1320 in plain
+// fp16). The halves need no memory of their own: they lie where nothing else
+// lives at the time.
+//
 // A and B are symmetric: only tiles on and below the diagonal are computed,
 // the others are their mirror images. The products run as tiles of P Q^T with
 // both operands K-contiguous: A = Xh Xh^T, O O^T, and F Yh^T with Yh the
@@ -61,6 +72,11 @@ __device__ __forceinline__ float g_at(const uint16_t* G, int64_t i) { return bf1
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)a) |
          ((uint32_t)__builtin_bit_cast(uint16_t, (_Float16)b) << 16);
+}
+__device__ __forceinline__ float low_part(float x) { return x - (float)(_Float16)x; }
+__device__ __forceinline__ float half_at(uint2 v, int u) {   // u-th of four packed halves
+  const uint32_t bits = ((u & 2) ? v.y : v.x) >> (16 * (u & 1));
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
 }
 
 // Sum over the block in a fixed order, in every thread.
@@ -147,6 +163,47 @@ __global__ __launch_bounds__(kThreads) void ns_load_kernel(
   }
 }
 
+// The scaled fp16 copies of X as two halves (lo nullable), TRANSPOSED: of its
+// transpose; 64 x 64 tiles.
+template <bool TRANSPOSED>
+__global__ __launch_bounds__(kThreads) void ns_copy_kernel(const float* __restrict__ X, int mp,
+                                                           int np, _Float16* __restrict__ hi,
+                                                           _Float16* __restrict__ lo) {
+  __shared__ float t[64][65];
+  const int64_t base = (int64_t)blockIdx.z * mp * np;
+  const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
+  const int c = (threadIdx.x & 15) * 4, a0 = threadIdx.x >> 4;
+  auto put = [&](int64_t at, const float (&f)[4]) {
+    *reinterpret_cast<uint2*>(hi + at) = make_uint2(pack_half(f[0], f[1]), pack_half(f[2], f[3]));
+    if (lo)
+      *reinterpret_cast<uint2*>(lo + at) =
+          make_uint2(pack_half(low_part(f[0]), low_part(f[1])),
+                     pack_half(low_part(f[2]), low_part(f[3])));
+  };
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int a = a0 + 16 * q;
+    const int64_t at = base + (int64_t)(i0 + a) * np + j0 + c;
+    const float4 x = *reinterpret_cast<const float4*>(X + at);
+    const float f[4] = {x.x * kSX, x.y * kSX, x.z * kSX, x.w * kSX};
+    if constexpr (TRANSPOSED) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) t[a][c + u] = f[u];
+    } else {
+      put(at, f);
+    }
+  }
+  if constexpr (TRANSPOSED) {
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int a = a0 + 16 * q;
+      const float f[4] = {t[c][a], t[c + 1][a], t[c + 2][a], t[c + 3][a]};
+      put(base + (int64_t)(j0 + a) * mp + i0 + c, f);
+    }
+  }
+}
+
 enum { NS_GRAM, NS_POLY, NS_UPDATE };
 
 struct NsArgs {
@@ -164,6 +221,8 @@ struct NsArgs {
   float* E;
   uint16_t* out;          // last update: the result, rows x cols
   int rows, cols;
+  int64_t plo, qlo;       // split: bytes from the operands to their low halves
+  _Float16 *Ol, *Fl;      // split: low halves of O and F
 };
 
 typedef __attribute__((address_space(3))) void lds_void_t;
@@ -194,7 +253,9 @@ __device__ __forceinline__ void ring_barrier() {
 // BM x BN tile of P Q^T by KS groups of WM x WN waves; S stages in the ring, a
 // stage being 64 of K for each group. Two groups halve the chain of stages of
 // a small product, whose time is latency; their sums are joined at the end.
-template <int MODE, int BM, int BN, int WM, int WN, int S, int KS>
+// SPLIT: operands of two halves, K walked three times; the update then writes
+// X alone, whose copies ns_copy_kernel makes.
+template <int MODE, int BM, int BN, int WM, int WN, int S, int KS, bool SPLIT>
 __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
   constexpr int NW = WM * WN;
   constexpr int TM = BM / WM, TN = BN / WN;          // a wave's part
@@ -239,19 +300,31 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
   const int dr = lane >> 3;
   const uint32_t chunk = (uint32_t)(((lane & 7) ^ (dr >> 1)) * 16);
   const uint32_t ring0 = (uint32_t)(uintptr_t)(const lds_void_t*)ring;
+  const int K1 = (int)(K / (64 * KS));               // stages of one walk of K
   auto issue = [&](int kt) {
     const uint32_t at = ring0 + ((kt % S) * KS + ks) * kStage;
-    const int64_t k0 = (int64_t)(kt * KS + ks) * 64;
+    const uint8_t *pb = P, *qb = Q;
+    int kw = kt;
+    if constexpr (SPLIT) {
+      if (kt >= 2 * K1) {
+        kw -= 2 * K1;
+        pb += g.plo;
+      } else if (kt >= K1) {
+        kw -= K1;
+        qb += g.qlo;
+      }
+    }
+    const int64_t k0 = (int64_t)(kw * KS + ks) * 64;
 #pragma unroll
     for (int q = 0; q < PL; ++q) {
       const int grp = wave * PL + q;
-      load_to_lds(P + (grp * 8 * K + k0) * 2,
+      load_to_lds(pb + (grp * 8 * K + k0) * 2,
                   (uint32_t)(dr * K * 2) + (chunk ^ (uint32_t)((grp & 1) * 64)), at + grp * 1024);
     }
 #pragma unroll
     for (int q = 0; q < QL; ++q) {
       const int grp = wave * QL + q;
-      load_to_lds(Q + (grp * 8 * K + k0) * 2,
+      load_to_lds(qb + (grp * 8 * K + k0) * 2,
                   (uint32_t)(dr * K * 2) + (chunk ^ (uint32_t)((grp & 1) * 64)),
                   at + BM * 128 + grp * 1024);
     }
@@ -275,6 +348,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
   const int er = lane >> 3, ec = (lane & 7) * 4;
   constexpr bool PRE = FM * FN <= 4;
   uint2 oin[MODE == NS_POLY ? FM : 1][MODE == NS_POLY ? FN : 1][4];
+  uint2 olin[MODE == NS_POLY && SPLIT ? FM : 1][MODE == NS_POLY && SPLIT ? FN : 1][4];
   float4 xin[MODE == NS_UPDATE ? (PRE ? FM * FN : 2) : 1][4];
   float4 djin[FN];
   float din[FM][4];
@@ -300,6 +374,8 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
           for (int b = 0; b < FN; ++b) {
             const int j = j0 + wn * TN + b * 32 + ec;
             oin[a][b][p] = *reinterpret_cast<const uint2*>(g.O + mm + (int64_t)i * g.mp + j);
+            if constexpr (SPLIT)
+              olin[a][b][p] = *reinterpret_cast<const uint2*>(g.Ol + mm + (int64_t)i * g.mp + j);
             if (a == 0 && p == 0)
               djin[b] = *reinterpret_cast<const float4*>(g.D + mat * g.mp + j);
           }
@@ -312,7 +388,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
   constexpr int AC = FM * FN == 1 ? 2 : 1;
   f32x16_t sums[AC][FM][FN] = {};
   auto& acc = sums[0];
-  const int KT = (int)(K / (64 * KS));
+  const int KT = SPLIT ? 3 * K1 : K1;
   constexpr int PD = S - 1;                          // stages in flight
 #pragma unroll
   for (int st = 0; st < PD; ++st)
@@ -382,6 +458,10 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
   auto halves = [](const float (&f)[4]) {
     return make_uint2(pack_half(f[0], f[1]), pack_half(f[2], f[3]));
   };
+  auto lows = [](const float (&f)[4]) {
+    return make_uint2(pack_half(low_part(f[0]), low_part(f[1])),
+                      pack_half(low_part(f[2]), low_part(f[3])));
+  };
   // four of the result's values from column c of row r on, inside its edges
   auto put_out = [&](int r, int c, const float (&f)[4]) {
     if (r >= g.rows) return;
@@ -425,13 +505,16 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
             }
           }
           *reinterpret_cast<uint2*>(g.O + mm + (int64_t)i * g.mp + j) = halves(f);
+          if constexpr (SPLIT)
+            *reinterpret_cast<uint2*>(g.Ol + mm + (int64_t)i * g.mp + j) = lows(f);
         } else if constexpr (MODE == NS_POLY) {
           const float di = din[a][p];
           const float dj[4] = {djin[b].x, djin[b].y, djin[b].z, djin[b].w};
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const uint32_t bits = ((u & 2) ? oin[a][b][p].y : oin[a][b][p].x) >> (16 * (u & 1));
-            const float o = (float)__builtin_bit_cast(_Float16, (uint16_t)bits) * (1.f / kSO);
+            float o = half_at(oin[a][b][p], u);
+            if constexpr (SPLIT) o += half_at(olin[a][b][p], u);
+            o *= 1.f / kSO;
             const float aa = v[u] * (1.f / (kSO * kSO));
             f[u] = ((g.b + g.c * (di + dj[u])) * o + g.c * aa) * kSF;
             if (ib == jb && i == j + u) {
@@ -440,6 +523,8 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
             }
           }
           *reinterpret_cast<uint2*>(g.F + mm + (int64_t)i * g.mp + j) = halves(f);
+          if constexpr (SPLIT)
+            *reinterpret_cast<uint2*>(g.Fl + mm + (int64_t)i * g.mp + j) = lows(f);
         } else {
           const float4 x = xin[PRE ? t : t & 1][p];
           const float xs[4] = {x.x, x.y, x.z, x.w};
@@ -452,16 +537,18 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
           } else {
             *reinterpret_cast<float4*>(g.X + mn + (int64_t)i * g.np + j) =
                 make_float4(f[0], f[1], f[2], f[3]);
+            if constexpr (!SPLIT) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) f[u] *= kSX;
-            *reinterpret_cast<uint2*>(g.Xh + mn + (int64_t)i * g.np + j) = halves(f);
+              for (int u = 0; u < 4; ++u) f[u] *= kSX;
+              *reinterpret_cast<uint2*>(g.Xh + mn + (int64_t)i * g.np + j) = halves(f);
+            }
           }
         }
         *slot = make_float4(f[0], f[1], f[2], f[3]);
       }
       wave_sync();
       // columns: the mirrored block, the transpose, or a tall matrix's result
-      const bool cols = MODE == NS_UPDATE ? !g.out || tall : bi != bj;
+      const bool cols = MODE == NS_UPDATE ? (g.out ? tall : !SPLIT) : bi != bj;
       if (cols) {
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
@@ -477,6 +564,10 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
           } else {
             _Float16* m = (MODE == NS_GRAM ? g.O : g.F) + mm;
             *reinterpret_cast<uint2*>(m + (int64_t)j * g.mp + i) = halves(f);
+            if constexpr (SPLIT) {
+              _Float16* l = (MODE == NS_GRAM ? g.Ol : g.Fl) + mm;
+              *reinterpret_cast<uint2*>(l + (int64_t)j * g.mp + i) = lows(f);
+            }
           }
         }
       }
@@ -714,7 +805,8 @@ hipError_t launch_orthogonalize(const OrthoPlan& p, const void* G, int32_t dtype
   // 429, at 128 (32 of 256 x 256) 125 and 111. Up to 256 blocks of 64 x 64 two
   // groups of waves share a tile's K (768 x 1024: 121 and 131); beyond, two
   // blocks share a compute unit instead (32 of 256 x 256: 111 and 138).
-  auto launch = [&](auto MODE, const NsArgs& args) {
+  // Products of halves, three times as long, take 128 x 128 or 64 x 64.
+  auto launch = [&](auto MODE, auto SPLIT, const NsArgs& args) {
     constexpr bool UPDATE = MODE() == NS_UPDATE;
     NsArgs g = args;
     auto blocks = [&](int B) {
@@ -724,15 +816,22 @@ hipError_t launch_orthogonalize(const OrthoPlan& p, const void* G, int32_t dtype
     auto go = [&](auto B, auto WM, auto WN, auto S, auto KS) {
       g.cols_t = p.np / B();
       g.tiles = (int)(blocks(B()) / n_mat);
-      hipLaunchKernelGGL((ns_tile_kernel<MODE(), B(), B(), WM(), WN(), S(), KS()>),
+      hipLaunchKernelGGL((ns_tile_kernel<MODE(), B(), B(), WM(), WN(), S(), KS(), SPLIT()>),
                          dim3((unsigned)blocks(B())), dim3(64 * WM() * WN() * KS()), 0, s, g);
     };
-    if constexpr (UPDATE)
+    if constexpr (UPDATE && !SPLIT())
       if (p.mp % 256 == 0 && p.np % 256 == 0 && blocks(256) >= 200)
         return go(IC<256>{}, IC<2>{}, IC<4>{}, IC<2>{}, IC<1>{});
     if (blocks(128) > 128) return go(IC<128>{}, IC<2>{}, IC<2>{}, IC<2>{}, IC<1>{});
-    if (blocks(64) > 256) return go(IC<64>{}, IC<2>{}, IC<2>{}, IC<4>{}, IC<1>{});
+    if constexpr (!SPLIT())
+      if (blocks(64) > 256) return go(IC<64>{}, IC<2>{}, IC<2>{}, IC<4>{}, IC<1>{});
     go(IC<64>{}, IC<2>{}, IC<2>{}, IC<3>{}, IC<2>{});
+  };
+  auto copies = [&](auto TRANSPOSED, _Float16* hi, _Float16* lo) {
+    hipLaunchKernelGGL(ns_copy_kernel<TRANSPOSED()>, lgrid, block, 0, s, X, p.mp, p.np, hi, lo);
+  };
+  const auto bytes = [](const _Float16* to, const _Float16* from) {
+    return (int64_t)(reinterpret_cast<const uint8_t*>(to) - reinterpret_cast<const uint8_t*>(from));
   };
   for (int k = 0; k < oa.steps; ++k) {
     NsArgs g{};
@@ -740,13 +839,32 @@ hipError_t launch_orthogonalize(const OrthoPlan& p, const void* G, int32_t dtype
     g.a = oa.a; g.b = oa.b; g.c = oa.c; g.scale = oa.scale;
     g.X = X; g.Xh = Xh; g.O = O; g.D = D; g.F = F; g.E = E;
     g.rows = rows; g.cols = cols;
-    g.P = Xh; g.Q = Xh; g.K = p.np;
-    launch(IC<NS_GRAM>{}, g);
-    g.P = O; g.Q = O; g.K = p.mp;
-    launch(IC<NS_POLY>{}, g);
-    g.P = F; g.Q = Yh[k & 1]; g.Yh = Yh[(k + 1) & 1];
     g.out = k + 1 == oa.steps ? out : nullptr;
-    launch(IC<NS_UPDATE>{}, g);
+    if (k < oa.split) {
+      // The low halves lie, of X in the first transpose (free until the
+      // update), of O in the second (as long), of F in X's copy (read by the
+      // Gram product alone), of the transpose in the second again.
+      g.Ol = Yh[1]; g.Fl = Xh;
+      copies(IC<0>{}, Xh, Yh[0]);
+      g.P = Xh; g.Q = Xh; g.K = p.np; g.plo = g.qlo = bytes(Yh[0], Xh);
+      launch(IC<NS_GRAM>{}, std::true_type{}, g);
+      g.P = O; g.Q = O; g.K = p.mp; g.plo = g.qlo = bytes(g.Ol, O);
+      launch(IC<NS_POLY>{}, std::true_type{}, g);
+      copies(IC<1>{}, Yh[0], Yh[1]);
+      g.P = F; g.Q = Yh[0]; g.plo = bytes(g.Fl, F); g.qlo = bytes(Yh[1], Yh[0]);
+      launch(IC<NS_UPDATE>{}, std::true_type{}, g);
+      if (k + 1 == oa.split && k + 1 < oa.steps) {   // what the plain steps start from
+        copies(IC<0>{}, Xh, nullptr);
+        copies(IC<1>{}, Yh[(k + 1) & 1], nullptr);
+      }
+      continue;
+    }
+    g.P = Xh; g.Q = Xh; g.K = p.np;
+    launch(IC<NS_GRAM>{}, std::false_type{}, g);
+    g.P = O; g.Q = O; g.K = p.mp;
+    launch(IC<NS_POLY>{}, std::false_type{}, g);
+    g.P = F; g.Q = Yh[k & 1]; g.Yh = Yh[(k + 1) & 1];
+    launch(IC<NS_UPDATE>{}, std::false_type{}, g);
   }
   return hipGetLastError();
 }

@@ -171,7 +171,7 @@ struct OrthoPlan {
 };
 OrthoPlan ortho_plan(int64_t n_mat, int64_t rows, int64_t cols);
 struct OrthoArgs {
-  int steps;
+  int steps, split;           // split: leading steps on operands of two halves
   float a, b, c, eps, scale;
 };
 hipError_t launch_orthogonalize(const OrthoPlan& p, const void* G, int32_t dtype, int64_t n_mat,

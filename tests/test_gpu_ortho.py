@@ -1,0 +1,63 @@
+"""GPU parity of the orthogonalised update where its rounding or its tile rule
+could go wrong: spectra and step counts under which fp16 operands alone would
+leave the result's own rounding behind.
+
+Bound, relative in the 2-norm: 2^-8 for the result's rounding to bf16 (half a
+step of every value) and 2^-8 for the products' operands, the most the entry
+point lets their rounding come to."""
+import numpy as np
+import pytest
+import torch
+
+import hashed_head_gram_amd as pg
+from oracle import train as ot
+
+pytestmark = pytest.mark.gpu
+
+USUAL = (3.4445, -4.7750, 2.0315)
+LIMIT = 2.0 ** -8 + 2.0 ** -8
+
+
+def dev():
+    return torch.device("cuda:0")
+
+
+def ortho(G, **kw):
+    n, r, c = G.shape
+    ws = torch.full((pg.pg_orthogonalize_workspace_size(n, r, c),), 0xFF, dtype=torch.uint8,
+                    device=dev())
+    out = torch.full(G.shape, 9.0, dtype=torch.bfloat16, device=dev())
+    pg.pg_orthogonalize(G, out, ws, **kw)
+    return out
+
+
+def weak(rng, r, c, floor):
+    """A matrix half of whose directions are `floor` of the others."""
+    k = min(r, c)
+    u = np.linalg.qr(rng.standard_normal((r, k)))[0]
+    v = np.linalg.qr(rng.standard_normal((c, k)))[0]
+    return (u * np.where(np.arange(k) < k // 2, 1.0, floor)) @ v.T
+
+
+# matrices, rows, columns: 64 x 64 tiles and (40 of 384 x 384) 128 x 128 ones,
+# whole and ragged, wide and tall
+@pytest.mark.parametrize("n,r,c", [(1, 130, 300), (2, 300, 130), (2, 256, 1024), (40, 384, 384)])
+@pytest.mark.parametrize("steps,coef", [(5, USUAL), (6, USUAL), (8, USUAL), (10, USUAL),
+                                        (64, USUAL), (16, (1.875, -1.25, 0.375)),
+                                        (24, (1.5, -0.5, 0.0))])
+@pytest.mark.parametrize("floor", [1e-2, 1e-3])
+def test_weak_directions(n, r, c, steps, coef, floor):
+    print(f"[weak directions] {n} {r} {c} {steps} {coef} {floor}", flush=True)
+    rng = np.random.default_rng(r + 7 * c)
+    some = min(n, 2)
+    G = np.stack([weak(rng, r, c, floor) for _ in range(some)])
+    G = torch.from_numpy(np.resize(G, (n, r, c)).astype(np.float32)).to(dev())
+    out = ortho(G, steps=steps, coef=coef)
+    for g, o in zip(G[:some].double().cpu().numpy(), out[:some].double().cpu().numpy()):
+        ref = ot.newton_schulz(g, steps, coef, 1e-7)
+        far = np.linalg.norm(o - ref) / np.linalg.norm(ref)
+        print(f"  {far:.2e}", flush=True)
+        assert far <= LIMIT
+    assert torch.equal(ortho(G, steps=steps, coef=coef), out)
+    if n > 2:                                        # the other matrices are these again
+        assert torch.equal(out, out[:2].repeat(n // 2, 1, 1))
