@@ -78,8 +78,8 @@ double factor_max(double b, double c, double m) {
   return c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < t ? fmax(best, fabs(b * b / (4 * c))) : best;
 }
 
-// Whether every iterate stays where the fp16 copies hold it: singular values
-// at most 3 before each step, |b t + c t^2| at most 100 for t = s^2.
+// Whether every iterate a step reads stays where the fp16 copies hold it:
+// singular values at most 3 before each step, |b t + c t^2| at most 100 for t = s^2.
 bool ortho_in_range(double a, double b, double c, int steps) {
   double m = 1.0;
   for (int k = 0; k < steps; ++k) {
@@ -87,7 +87,7 @@ bool ortho_in_range(double a, double b, double c, int steps) {
     if (!(factor_max(b, c, m) <= 100.0)) return false;
     m = quintic_max(a, b, c, m);
   }
-  return m <= 100.0;
+  return isfinite(m);                                // the result itself stays in fp32
 }
 
 // Leading steps whose operands have to be split in halves. The rounding of the

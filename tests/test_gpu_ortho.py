@@ -61,3 +61,16 @@ def test_weak_directions(n, r, c, steps, coef, floor):
     assert torch.equal(ortho(G, steps=steps, coef=coef), out)
     if n > 2:                                        # the other matrices are these again
         assert torch.equal(out, out[:2].repeat(n // 2, 1, 1))
+
+
+@pytest.mark.parametrize("r,c", [(40, 70), (130, 300)])
+def test_large_result_of_one_step(r, c):
+    rng = np.random.default_rng(3)
+    G = torch.from_numpy(rng.standard_normal((2, r, c)).astype(np.float32)).to(dev())
+    for coef, scale in (((150.0, 0.0, 0.0), 1.0), ((60.0, 50.0, 49.0), 1e3)):
+        out = ortho(G, steps=1, coef=coef, scale=scale).double().cpu().numpy()
+        for g, o in zip(G.double().cpu().numpy(), out):
+            ref = ot.newton_schulz(g, 1, coef, 1e-7, scale)
+            # b = c = 0 has no products: half a bf16 step and a few fp32 operations
+            limit = LIMIT if coef[1] else 2.0 ** -8 + 8 * 2.0 ** -24
+            assert np.linalg.norm(o - ref) <= limit * np.linalg.norm(ref)

@@ -25,3 +25,23 @@ def test_layer_norm_workspace_of_the_largest_batch_serves_every_smaller_one(d):
     need = [pg.pg_layer_norm_workspace_size(n, d) for n in
             sorted({*range(0, 6000, 13), *(1 << k for k in range(32))})]
     assert need == sorted(need)
+
+
+def test_orthogonalize_last_iterate_is_free():
+    """Refusals are the two the header names: a singular value beyond 3 before a step, and
+    |b s^2 + c s^4| beyond 100. The result itself may be large."""
+    f = pg.lib().pg_orthogonalize
+
+    def call(steps, a, b, c):
+        return f(None, pg.PG_F32, 0, 100, 300, steps, a, b, c, 1e-7, 1.0, None, None, 0, None)
+
+    assert call(1, 150.0, 0.0, 0.0) == pg.PG_OK
+    assert call(2, 2.9, 0.0, 0.0) == pg.PG_OK
+    assert call(1, 3e38, 0.0, 0.0) == pg.PG_OK
+    assert call(1, 60.0, 50.0, 49.0) == pg.PG_OK
+    assert call(1, 60.0, 51.0, 50.0) == pg.PG_EUNSUPPORTED
+    assert call(2, 3.1, 0.0, 0.0) == pg.PG_EUNSUPPORTED
+    nan, inf = float("nan"), float("inf")
+    for bad in (nan, inf, -inf):
+        for coef in ((bad, 0.0, 0.0), (0.0, bad, 0.0), (0.0, 0.0, bad)):
+            assert call(1, *coef) == pg.PG_EUNSUPPORTED, coef
