@@ -74,3 +74,49 @@ def test_large_result_of_one_step(r, c):
             # b = c = 0 has no products: half a bf16 step and a few fp32 operations
             limit = LIMIT if coef[1] else 2.0 ** -8 + 8 * 2.0 ** -24
             assert np.linalg.norm(o - ref) <= limit * np.linalg.norm(ref)
+
+
+# Tiles that the products of one shape run on (Gram and polynomial, update):
+# 64a: 64 x 64, K shared by two wave groups; 64b: 64 x 64, four stages.
+TILES = [(5, 768, 768, "f32"),          # 64b, 128
+         (2, 768, 1000, "f32"),         # 64a, 64b; ragged
+         (2, 1000, 768, "bf16"),        # 64a, 64b; ragged, tall
+         (30, 250, 200, "f32"),         # 64b, 64b; ragged, tall
+         (30, 200, 250, "bf16"),        # 64b, 64b; ragged
+         (1, 1280, 1280, "f32"),        # 64a, 64b
+         (1, 2560, 1280, "bf16"),       # 64a, 128; tall
+         (4, 900, 700, "f32"),          # 64b, 128; ragged, tall
+         (100, 500, 250, "f32"),        # 128, 256; ragged, tall
+         (50, 480, 500, "bf16"),        # 128, 256; ragged
+         (60, 500, 256, "f32"),         # 128, 128; ragged, tall
+         (1, 16384, 130, "f32"),        # 64a, 128; the longest side, tall
+         (1, 130, 16384, "bf16")]       # 64a, 128; the longest side
+
+
+@pytest.mark.parametrize("n,r,c,dt", TILES)
+def test_every_tile(n, r, c, dt):
+    """Against the oracle, with what the documented fp16 storage moves it by (twice, in the
+    2-norm) beside half a bf16 step."""
+    print(f"[tiles] {n} {r} {c} {dt}", flush=True)
+    rng = np.random.default_rng(r + 3 * c)
+    some = sorted({0, n - 1})
+    k = min(r, c)
+    G = np.stack([(rng.standard_normal((r, k)) * np.arange(1, k + 1) ** -0.7)
+                  @ rng.standard_normal((k, c)) for _ in some])
+    G = torch.from_numpy(G.astype(np.float32)).to(dev())
+    G = G.to({"f32": torch.float32, "bf16": torch.bfloat16}[dt])
+    if n > 2:                                        # the others: the first one, scaled by powers of 2
+        G = torch.cat([G[:1] * 2.0 ** (i % 7) for i in range(n - 1)] + [G[1:]])
+    out = ortho(G)
+    for i in some:
+        g, o = G[i].double().cpu().numpy(), out[i].double().cpu().numpy()
+        ref = ot.newton_schulz(g, 5, USUAL, 1e-7)
+        noise = np.linalg.norm(ot.newton_schulz_half(g, 5, USUAL, 1e-7) - ref)
+        far = np.linalg.norm(o - ref)
+        print(f"  {far / np.linalg.norm(ref):.2e}, storage {noise / np.linalg.norm(ref):.1e}",
+              flush=True)
+        assert far <= 2.0 ** -8 * np.linalg.norm(ref) + 2 * noise
+    assert torch.equal(ortho(G), out)
+    if n > 2:                                        # powers of two change nothing but eps' share
+        a, b = out[:n - 1].float(), out[:1].float()
+        assert bool(((a - b).norm(dim=(1, 2)) <= 2.0 ** -8 * b.norm()).all())
