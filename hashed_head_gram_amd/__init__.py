@@ -513,8 +513,19 @@ def _call(fn, dev, stream, *args):
         raise PagegramError(fn, status)
 
 
+def _in32(v):
+    """v, or the end of int32 that it lies beyond: ctypes would pass its low bits. The library
+    refuses the ends like any size past its limits."""
+    return v if -2**31 <= v < 2**31 else 2**31 - 1 if v > 0 else -2**31
+
+
+def _in64(v):
+    return v if -2**63 <= v < 2**63 else 2**63 - 1 if v > 0 else -2**63
+
+
 def _size(fn, *args):
-    v = getattr(lib(), fn)(*(int(a) for a in args))
+    f = getattr(lib(), fn)
+    v = f(*((_in32 if t is _i32 else _in64)(int(a)) for a, t in zip(args, f.argtypes)))
     if v < 0:
         raise PagegramError(fn, v)
     return v
@@ -534,7 +545,7 @@ def pg_embed(table, tokens, out, scale=1.0, dev_status=None, stream=None):
     if hasattr(data, "numel") and table.dtype != PG_NF4:
         want = torch.float32 if table.dtype == PG_F32 else torch.bfloat16
         _flat("pg_embed", "table data", data, want, table.n_rows * d, dev)
-    _call("pg_embed", dev, stream, ctypes.byref(table), d, float(scale), _ptr(tokens), n,
+    _call("pg_embed", dev, stream, ctypes.byref(table), _in32(d), float(scale), _ptr(tokens), n,
           _dtype("pg_embed", "out", out), _ptr(out), ld, _ptr(dev_status))
 
 
@@ -562,8 +573,8 @@ def pg_embed_backward(dout, tokens, V, urows, ugrad, n_unique, workspace, scale=
     _flat(fn, "urows", urows, torch.int64, cap, dev, at_least=True)
     _flat(fn, "ugrad", ugrad, torch.float32, cap * d, dev, at_least=True)
     _flat(fn, "n_unique", n_unique, torch.int64, 1, dev, at_least=True)
-    _call(fn, dev, stream, _ptr(dout), dt, ld, _ptr(tokens), n, int(V), d, float(scale),
-          _ptr(urows), _ptr(ugrad), _ptr(n_unique), _ptr(workspace), _ws_bytes(workspace))
+    _call(fn, dev, stream, _ptr(dout), dt, ld, _ptr(tokens), n, _in64(int(V)), _in32(d),
+          float(scale), _ptr(urows), _ptr(ugrad), _ptr(n_unique), _ptr(workspace), _ws_bytes(workspace))
 
 
 def pg_embed_backward_dense(dout, tokens, dtable, workspace, scale=1.0, accumulate=0,
@@ -574,8 +585,8 @@ def pg_embed_backward_dense(dout, tokens, dtable, workspace, scale=1.0, accumula
     dev, n, ld, d, dt = _embed_dout(fn, dout, tokens, workspace)
     V = dtable.shape[0]
     _flat(fn, "dtable", dtable, torch.float32, V * d, dev)
-    _call(fn, dev, stream, _ptr(dout), dt, ld, _ptr(tokens), n, V, d, float(scale),
-          _ptr(dtable), int(accumulate), _ptr(workspace), _ws_bytes(workspace))
+    _call(fn, dev, stream, _ptr(dout), dt, ld, _ptr(tokens), n, V, _in32(d), float(scale),
+          _ptr(dtable), _in32(int(accumulate)), _ptr(workspace), _ws_bytes(workspace))
 
 
 def pg_layer_norm(x, gamma, beta, y, eps=1e-5, mean=None, rstd=None, stream=None):
@@ -595,7 +606,7 @@ def pg_layer_norm(x, gamma, beta, y, eps=1e-5, mean=None, rstd=None, stream=None
         _flat(fn, "mean", mean, torch.float32, n, dev)
     if rstd is not None:
         _flat(fn, "rstd", rstd, torch.float32, n, dev)
-    _call(fn, dev, stream, _ptr(x), _dtype(fn, "x", x), n, d, ldx, _ptr(gamma), _ptr(beta),
+    _call(fn, dev, stream, _ptr(x), _dtype(fn, "x", x), n, _in32(d), ldx, _ptr(gamma), _ptr(beta),
           float(eps), _ptr(y), ldy, _ptr(mean), _ptr(rstd))
 
 
@@ -626,7 +637,7 @@ def pg_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspac
         _flat(fn, "dbeta", dbeta, torch.float32, d, dev)
     _flat(fn, "workspace", workspace, torch.uint8, 0, dev, at_least=True)
     _call(fn, dev, stream, _ptr(dy), _rows(fn, "dy", dy)[1], _ptr(x), ldx, _dtype(fn, "x", x), n,
-          d, _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(add), ldadd, _ptr(dx),
+          _in32(d), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(add), ldadd, _ptr(dx),
           _rows(fn, "dx", dx)[1], _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
           _ws_bytes(workspace))
 
@@ -651,8 +662,9 @@ def pg_orthogonalize(G, out, workspace, steps=5, coef=(3.4445, -4.7750, 2.0315),
     _flat(fn, "out", out, torch.bfloat16, G.numel(), dev)
     _flat(fn, "workspace", workspace, torch.uint8, 0, dev, at_least=True)
     a, b, c = (float(v) for v in coef)
-    _call(fn, dev, stream, _ptr(G), _dtype(fn, "G", G), n_mat, rows, cols, int(steps), a, b, c,
-          float(eps), float(scale), _ptr(out), _ptr(workspace), _ws_bytes(workspace))
+    _call(fn, dev, stream, _ptr(G), _dtype(fn, "G", G), n_mat, _in32(rows), _in32(cols),
+          _in32(int(steps)), a, b, c, float(eps), float(scale), _ptr(out), _ptr(workspace),
+          _ws_bytes(workspace))
 
 
 # ----------------------------------------------------------------------------

@@ -1,0 +1,39 @@
+"""Calls of the training-step entry points at the edges of their arguments."""
+import pytest
+import torch
+
+import hashed_head_gram_amd as pg
+
+pytestmark = pytest.mark.gpu
+
+
+def dev():
+    return torch.device("cuda:0")
+
+
+def refused(call, status):
+    with pytest.raises(pg.PagegramError) as err:
+        call()
+    assert err.value.status == status
+
+
+def test_numbers_beyond_the_c_types_are_refused():
+    """Each of these would be a call of ordinary size if the number were cut to its low bits."""
+    G = torch.randn(2, 30, 50, device=dev())
+    out = torch.empty(2, 30, 50, dtype=torch.bfloat16, device=dev())
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=dev())
+    refused(lambda: pg.pg_orthogonalize(G, out, ws, steps=2**32 + 5), pg.PG_EINVAL)
+    x = torch.randn(4, 64, device=dev())
+    tok = torch.zeros(4, dtype=torch.int32, device=dev())
+    table = torch.zeros(10, 64, device=dev())
+    refused(lambda: pg.pg_embed_backward_dense(x, tok, table, ws, accumulate=2**32), pg.PG_EINVAL)
+    refused(lambda: pg.pg_embed_backward(x, tok, 2**64 + 10, tok.long(), x.clone(), tok.long(), ws),
+            pg.PG_ERANGE)
+    # one row of 2^32 + 64 columns, 17 GB (its first half as bf16 is another)
+    gamma = torch.empty(2**32 + 64, device=dev())
+    row = gamma.view(torch.bfloat16)[:2**32 + 64].view(1, -1)
+    refused(lambda: pg.pg_embed(pg.make_table(pg.PG_F32, table.data_ptr(), 10), tok[:1], row),
+            pg.PG_EUNSUPPORTED)
+    refused(lambda: pg.pg_layer_norm(row, gamma, None, row), pg.PG_EUNSUPPORTED)
+    refused(lambda: pg.pg_embed_backward_dense(row, tok[:1], gamma.view(1, -1), ws),
+            pg.PG_EUNSUPPORTED)

@@ -45,3 +45,18 @@ def test_orthogonalize_last_iterate_is_free():
     for bad in (nan, inf, -inf):
         for coef in ((bad, 0.0, 0.0), (0.0, bad, 0.0), (0.0, 0.0, bad)):
             assert call(1, *coef) == pg.PG_EUNSUPPORTED, coef
+
+
+@pytest.mark.parametrize("fn,args,status", [
+    ("pg_embed_workspace_size", (5, 100, 2**32 + 64), pg.PG_EUNSUPPORTED),
+    ("pg_embed_workspace_size", (2**64 + 5, 100, 64), pg.PG_ERANGE),
+    ("pg_embed_workspace_size", (5, 2**64 + 100, 64), pg.PG_ERANGE),
+    ("pg_embed_workspace_size", (5, 100, -2**32 + 64), pg.PG_EINVAL),
+    ("pg_layer_norm_workspace_size", (5, 2**32 + 64), pg.PG_EUNSUPPORTED),
+    ("pg_orthogonalize_workspace_size", (1, 2**32 + 5, 5), pg.PG_EUNSUPPORTED),
+    ("pg_orthogonalize_workspace_size", (1, 5, 2**32 + 5), pg.PG_EUNSUPPORTED),
+    ("pg_orthogonalize_workspace_size", (2**64 + 1, 5, 5), pg.PG_ERANGE)])
+def test_sizes_beyond_the_c_types_are_not_wrapped(fn, args, status):
+    with pytest.raises(pg.PagegramError) as err:
+        getattr(pg, fn)(*args)
+    assert err.value.status == status
