@@ -503,7 +503,12 @@ def _call(fn, dev, stream, *args):
     import torch
     f = getattr(_lib or lib(), fn)
     index = dev.index
-    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        raw = _stream(stream)
+        if getattr(stream, "device", dev) != dev:
+            raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {dev}")
     if index == torch._C._cuda_getDevice():
         status = f(*args, raw)
     else:

@@ -60,3 +60,14 @@ def test_sizes_beyond_the_c_types_are_not_wrapped(fn, args, status):
     with pytest.raises(pg.PagegramError) as err:
         getattr(pg, fn)(*args)
     assert err.value.status == status
+
+
+class _Stream:
+    def __init__(self, device):
+        self.device, self.cuda_stream = device, 0
+
+
+def test_a_stream_of_another_device_is_refused():
+    import torch
+    with pytest.raises(ValueError, match="stream"):
+        pg._call("pg_embed", torch.device("cuda", 0), _Stream(torch.device("cuda", 1)))
