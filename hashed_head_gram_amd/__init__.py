@@ -478,22 +478,29 @@ def _rows(fn, name, t):
 
 def _flat(fn, name, t, dtype, size, dev, at_least=False):
     """t is contiguous, of dtype, with size elements, on dev."""
-    n = t.numel()
-    if (n != size and not (at_least and n > size)) or t.dtype != dtype or t.device != dev or \
-            not t.is_contiguous():
+    n = None if t is None else t.numel()
+    if n is None or (n != size and not (at_least and n > size)) or t.dtype != dtype or \
+            t.device != dev or not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of {size} elements "
                          f"on {dev}")
 
 
+def _work(fn, t, dev):
+    """A workspace: uint8 on dev, or None, which the library takes where it needs none."""
+    import torch
+    if t is not None:
+        _flat(fn, "workspace", t, torch.uint8, 0, dev, at_least=True)
+
+
 def _like(fn, name, t, ref):
-    if t.shape != ref.shape or t.dtype != ref.dtype or t.device != ref.device:
+    if t is None or t.shape != ref.shape or t.dtype != ref.dtype or t.device != ref.device:
         raise ValueError(f"{fn}: {name} must be a {ref.dtype} tensor of shape "
                          f"{tuple(ref.shape)} on {ref.device}")
 
 
 def _gpu(fn, name, t):
-    if not t.is_cuda:
-        raise ValueError(f"{fn}: {name} is on {t.device}, not on a GPU")
+    if t is None or not t.is_cuda:
+        raise ValueError(f"{fn}: {name} is {'None' if t is None else t.device}, not on a GPU")
     return t.device
 
 
@@ -563,7 +570,7 @@ def _embed_dout(fn, dout, tokens, workspace):
     dev = _gpu(fn, "dout", dout)
     n, ld = _rows(fn, "dout", dout)
     _flat(fn, "tokens", tokens, torch.int32, n, dev)
-    _flat(fn, "workspace", workspace, torch.uint8, 0, dev, at_least=True)
+    _work(fn, workspace, dev)
     return dev, n, ld, dout.shape[-1], _dtype(fn, "dout", dout)
 
 
@@ -640,7 +647,7 @@ def pg_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspac
     _flat(fn, "dgamma", dgamma, torch.float32, d, dev)
     if dbeta is not None:
         _flat(fn, "dbeta", dbeta, torch.float32, d, dev)
-    _flat(fn, "workspace", workspace, torch.uint8, 0, dev, at_least=True)
+    _work(fn, workspace, dev)
     _call(fn, dev, stream, _ptr(dy), _rows(fn, "dy", dy)[1], _ptr(x), ldx, _dtype(fn, "x", x), n,
           _in32(d), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(add), ldadd, _ptr(dx),
           _rows(fn, "dx", dx)[1], _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
@@ -658,14 +665,14 @@ def pg_orthogonalize(G, out, workspace, steps=5, coef=(3.4445, -4.7750, 2.0315),
     import torch
     fn = "pg_orthogonalize"
     dev = _gpu(fn, "G", G)
-    if G.dim() < 2 or not G.is_contiguous() or out.shape != G.shape:
+    if G.dim() < 2 or not G.is_contiguous() or out is None or out.shape != G.shape:
         raise ValueError(f"{fn}: G must be contiguous [..., rows, cols], out of its shape")
     rows, cols = G.shape[-2:]
     n_mat = 1
     for s in G.shape[:-2]:
         n_mat *= s
     _flat(fn, "out", out, torch.bfloat16, G.numel(), dev)
-    _flat(fn, "workspace", workspace, torch.uint8, 0, dev, at_least=True)
+    _work(fn, workspace, dev)
     a, b, c = (float(v) for v in coef)
     _call(fn, dev, stream, _ptr(G), _dtype(fn, "G", G), n_mat, _in32(rows), _in32(cols),
           _in32(int(steps)), a, b, c, float(eps), float(scale), _ptr(out), _ptr(workspace),

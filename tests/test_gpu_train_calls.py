@@ -37,3 +37,29 @@ def test_numbers_beyond_the_c_types_are_refused():
     refused(lambda: pg.pg_layer_norm(row, gamma, None, row), pg.PG_EUNSUPPORTED)
     refused(lambda: pg.pg_embed_backward_dense(row, tok[:1], gamma.view(1, -1), ws),
             pg.PG_EUNSUPPORTED)
+
+
+def test_no_workspace_where_none_is_needed():
+    """A workspace of None is a null pointer: taken for no tokens and no rows, refused otherwise;
+    other tensors that are missing are a ValueError."""
+    x, tok = torch.randn(4, 8, device=dev()), torch.zeros(4, dtype=torch.int32, device=dev())
+    s, one = torch.ones(4, device=dev()), torch.ones(8, device=dev())
+    count = torch.full((1,), 7, device=dev())
+    table = torch.ones(5, 8, device=dev())
+    pg.pg_embed_backward(x[:0], tok[:0], 5, tok.long(), table, count, None)
+    pg.pg_embed_backward_dense(x[:0], tok[:0], table, None)
+    assert count.item() == 0 and bool((table == 0).all())
+    dg, db = one.clone(), one.clone()
+    pg.pg_layer_norm_backward(x[:0], x[:0], one, s[:0], s[:0], x[:0], dg, db, None)
+    assert bool((dg == 0).all()) and bool((db == 0).all())
+    refused(lambda: pg.pg_embed_backward(x, tok, 5, tok.long(), table, count, None), pg.PG_EINVAL)
+    refused(lambda: pg.pg_embed_backward_dense(x, tok, table, None), pg.PG_EINVAL)
+    refused(lambda: pg.pg_layer_norm_backward(x, x.clone(), one, s, s, x, dg, db, None), pg.PG_EINVAL)
+    refused(lambda: pg.pg_orthogonalize(x, x.bfloat16(), None), pg.PG_EINVAL)
+    for call in (lambda: pg.pg_layer_norm(x, None, None, x),
+                 lambda: pg.pg_layer_norm(x, one, None, None),
+                 lambda: pg.pg_layer_norm_backward(x, x.clone(), one, None, s, x, dg, db, None),
+                 lambda: pg.pg_embed_backward(x, tok, 5, None, table, count, None),
+                 lambda: pg.pg_orthogonalize(x, None, None)):
+        with pytest.raises(ValueError):
+            call()

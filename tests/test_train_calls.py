@@ -71,3 +71,9 @@ def test_a_stream_of_another_device_is_refused():
     import torch
     with pytest.raises(ValueError, match="stream"):
         pg._call("pg_embed", torch.device("cuda", 0), _Stream(torch.device("cuda", 1)))
+
+
+def test_a_missing_tensor_is_a_value_error():
+    import torch
+    with pytest.raises(ValueError, match="gamma"):
+        pg._flat("pg_layer_norm", "gamma", None, torch.float32, 8, torch.device("cuda", 0))
