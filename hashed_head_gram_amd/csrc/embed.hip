@@ -530,8 +530,10 @@ struct RowOut {
 // The 8 columns a lane covers start at `col`. A lane whose columns would pass
 // the row's end covers its last 8 instead: it computes and writes what its
 // neighbour does, and no code for part vectors is needed. Only where that
-// cannot be (PARTS: rows of fewer than 8 columns, and the adding form, which
-// must read and write an element once) the last lane moves single elements.
+// cannot be (PARTS: rows of fewer than 8 columns, and the adding form at every
+// width, which must read and write an element once) the last lane moves single
+// elements (131,072 x 2,560 bf16 of 128,000, added: 276 us, touched rows alone
+// 218, with one set of inputs).
 template <bool PARTS>
 __device__ __forceinline__ int lane_col(int col, int d) {
   return !PARTS && col > d - 8 ? d - 8 : col;

@@ -365,7 +365,10 @@ void with_geometry(int d, F f) {
 // `waves` waves deep, no more than there are rows, and past one block a unit
 // `per` rows a group or more. 131,072 rows of 2,560 bf16:
 // forward 296, 264 and 316 us at 15, 20 and 30 waves, backward 511, 490, 512
-// and 542 us at 10, 15, 20 and 30.
+// and 542 us at 10, 15, 20 and 30. Whole blocks only: a backward block of
+// eight waves, rows beyond 3,584 columns, has a unit to itself, eight waves
+// deep (65,536 bf16 rows, with add: 4,096 columns 421 us, 5.1 TB/s, 3,584
+// columns 314 us, 6.0; 32,768 of 8,192, two vectors a lane, 351 us, 6.1).
 template <int L, int W>
 int64_t norm_blocks(int64_t n, int waves, int per) {
   constexpr int NT = kNormThreads<W>;

@@ -7,7 +7,7 @@
 // the singular vectors; out = scale X.
 //
 // The products run on the matrix cores in fp16 with fp32 accumulation. What
-// keeps the rounding to fp16 far below the result's bf16:
+// keeps that rounding below the result's own, bf16's, on common spectra:
 //   * X itself stays in fp32 and enters as (a + B_ii) X_ij in the epilogue;
 //     only the products read an fp16 copy;
 //   * the diagonals of A and B, where most of their weight is, stay in fp32
@@ -16,7 +16,8 @@
 //       E_i  = b D_i + c ((O O)_ii + D_i^2);
 //   * fixed powers of two place the fp16 copies: X 2^10, O 2^12, F 2^9, far
 //     from overflow for every iterate the entry point admits (singular values
-//     at most 3, |b s^2 + c s^4| at most 100) and with subnormals below 2^-33.
+//     at most 3, |b s^2 + c s^4| at most 100); values below 2^-24, 2^-26 and
+//     2^-23 become subnormals, in steps of 2^-34, 2^-36 and 2^-33.
 // bf16 operands, the usual choice, would be eight times coarser.
 //
 // Rounding that falls on directions G nearly lacks grows with them, up to |a|

@@ -595,8 +595,10 @@ PG_API int pg_row_rms_flush(const pg_layout* layout, float* table, float* vhat,
 /* ------------------------------------------------------------------------
  * The training step around the memory: the token embedding whose output is
  * the residual stream the memory is added to, the layer norm that reads that
- * stream, and the orthogonalised update of the projection weights (the rows
- * of W_V and of the W_K^(m); their gradient is pg_backward_scalar's dW).
+ * stream, and the orthogonalised update of projection weights: W_V, whose
+ * gradient is pg_backward_scalar's dW for the scalar gate, and, from gradients
+ * of the caller's own (the context gate has no backward pass here), the
+ * W_K^(m). The update is the caller's to apply: W stays as it is.
  * Besides the conventions above: `dtype` is PG_F32 or PG_BF16; ld_* is a row
  * stride in elements, at least d (rows may be slices of wider ones, and
  * pointers need no more than their element's alignment unless stated);
@@ -633,7 +635,8 @@ PG_API int64_t pg_embed_workspace_size(int64_t n_tok, int64_t V, int32_t d);
 /*
  * pg_embed_backward -- the table gradient of pg_embed restricted to the rows
  * the tokens touch, in pg_backward_scalar's form: urows int64 [*n_unique]
- * ascending, ugrad fp32 [*n_unique][d] with
+ * ascending, ugrad fp32 [*n_unique][d] (pg_row_rms_step takes them up to its
+ * row limit, d <= 256; wider ones are for an optimiser of the caller's) with
  *   ugrad[u] = scale * sum over t with tokens[t] = urows[u] of dout[t],
  * summed in fp32 over runs of tokens in token order, the runs then in order.
  * Tokens outside [0, V) add nothing.
@@ -663,7 +666,10 @@ PG_API int pg_embed_backward_dense(const void* dout, int32_t dtype, int64_t ld,
 /*
  * pg_layer_norm -- for each of n rows of d elements:
  *   mu = mean(x), rstd = 1 / sqrt(mean((x - mu)^2) + eps),
- *   y = (x - mu) rstd gamma + beta.
+ *   y = (x - mu) rstd gamma + beta,
+ * in fp32: a row whose sum of squares leaves its range (deviations beyond
+ * about 1e19 / sqrt(d)) has rstd 0, and a row of equal values needs eps > 0
+ * (0 inf is NaN). A NaN or an infinity makes its row NaN and no other.
  *   gamma fp32 [d]; beta fp32 [d], nullable (zero); mean, rstd fp32 [n],
  *   nullable, what the backward pass takes; 1 <= d <= 16384
  *   (PG_EUNSUPPORTED beyond); n <= 2^31; x and y of dtype. y may be x itself

@@ -63,3 +63,21 @@ def test_no_workspace_where_none_is_needed():
                  lambda: pg.pg_orthogonalize(x, None, None)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_layer_norm_at_the_ends_of_fp32():
+    """A row whose squares overflow has rstd 0, equal values without eps give NaN, and no row
+    reaches another."""
+    x = torch.randn(5, 300, device=dev())
+    x[1] *= 1e25
+    x[2] = 3.0
+    x[3, 4] = float("inf")
+    gamma, beta = torch.rand(300, device=dev()) + 0.5, torch.randn(300, device=dev())
+    y, mean, rstd = torch.empty_like(x), torch.empty(5, device=dev()), torch.empty(5, device=dev())
+    pg.pg_layer_norm(x, gamma, beta, y, eps=0.0, mean=mean, rstd=rstd)
+    assert rstd[1] == 0 and torch.equal(y[1], beta)
+    assert bool(torch.isnan(y[2:4]).all()) and bool(torch.isfinite(y[[0, 4]]).all())
+    alone = torch.empty_like(x[:1])
+    for i in (0, 4):
+        pg.pg_layer_norm(x[i:i + 1], gamma, beta, alone, eps=0.0)
+        assert torch.equal(alone[0], y[i])
