@@ -27,8 +27,8 @@
 // lo hi, as one K three times as long. Relative 2-norm before the result's
 // rounding, half the directions 1e-3 of the others, 256 x 1024: 5 steps 2.9e-3
 // in plain fp16; 8 steps 3.3e-2, with leading halves 1e-3. Such a step takes
-// about three times as long (ten of five 2560 x 1280: 2910 us, 1320 in plain
-// fp16). The halves need no memory of their own: they lie where nothing else
+// about 2.6 times as long (ten of five 2560 x 1280: 2800 to 2820 us, 1320 in
+// plain fp16). The halves need no memory of their own: they lie where nothing else
 // lives at the time.
 //
 // A and B are symmetric: only tiles on and below the diagonal are computed,
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(kThreads) void ns_load_kernel(
 }
 
 // The scaled fp16 copies of X as two halves (lo nullable), TRANSPOSED: of its
-// transpose; 64 x 64 tiles.
+// transpose; 64 x 64 tiles. Bound by memory: five 2560 x 1280 20 us (6.4 TB/s).
 template <bool TRANSPOSED>
 __global__ __launch_bounds__(kThreads) void ns_copy_kernel(const float* __restrict__ X, int mp,
                                                            int np, _Float16* __restrict__ hi,
@@ -255,7 +255,8 @@ __device__ __forceinline__ void ring_barrier() {
 // stage being 64 of K for each group. Two groups halve the chain of stages of
 // a small product, whose time is latency; their sums are joined at the end.
 // SPLIT: operands of two halves, K walked three times; the update then writes
-// X alone, whose copies ns_copy_kernel makes.
+// X alone, whose copies ns_copy_kernel makes. Five 2560 x 1280: Gram 107
+// us, polynomial 63, update 123; unsplit 38, 26 and 67.
 template <int MODE, int BM, int BN, int WM, int WN, int S, int KS, bool SPLIT>
 __global__ __launch_bounds__(64 * WM * WN * KS) void ns_tile_kernel(NsArgs g) {
   constexpr int NW = WM * WN;
@@ -806,7 +807,9 @@ hipError_t launch_orthogonalize(const OrthoPlan& p, const void* G, int32_t dtype
   // 429, at 128 (32 of 256 x 256) 125 and 111. Up to 256 blocks of 64 x 64 two
   // groups of waves share a tile's K (768 x 1024: 121 and 131); beyond, two
   // blocks share a compute unit instead (32 of 256 x 256: 111 and 138).
-  // Products of halves, three times as long, take 128 x 128 or 64 x 64.
+  // Products of halves follow the same rule (ten steps of five 2560 x 1280 2824
+  // us, 2990 without 256 x 256; of 32 of 256 x 256 399 us, 441 without four
+  // stages).
   auto launch = [&](auto MODE, auto SPLIT, const NsArgs& args) {
     constexpr bool UPDATE = MODE() == NS_UPDATE;
     NsArgs g = args;
@@ -820,12 +823,11 @@ hipError_t launch_orthogonalize(const OrthoPlan& p, const void* G, int32_t dtype
       hipLaunchKernelGGL((ns_tile_kernel<MODE(), B(), B(), WM(), WN(), S(), KS(), SPLIT()>),
                          dim3((unsigned)blocks(B())), dim3(64 * WM() * WN() * KS()), 0, s, g);
     };
-    if constexpr (UPDATE && !SPLIT())
+    if constexpr (UPDATE)
       if (p.mp % 256 == 0 && p.np % 256 == 0 && blocks(256) >= 200)
         return go(IC<256>{}, IC<2>{}, IC<4>{}, IC<2>{}, IC<1>{});
     if (blocks(128) > 128) return go(IC<128>{}, IC<2>{}, IC<2>{}, IC<2>{}, IC<1>{});
-    if constexpr (!SPLIT())
-      if (blocks(64) > 256) return go(IC<64>{}, IC<2>{}, IC<2>{}, IC<4>{}, IC<1>{});
+    if (blocks(64) > 256) return go(IC<64>{}, IC<2>{}, IC<2>{}, IC<4>{}, IC<1>{});
     go(IC<64>{}, IC<2>{}, IC<2>{}, IC<3>{}, IC<2>{});
   };
   auto copies = [&](auto TRANSPOSED, _Float16* hi, _Float16* lo) {

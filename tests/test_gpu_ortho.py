@@ -120,3 +120,71 @@ def test_every_tile(n, r, c, dt):
     if n > 2:                                        # powers of two change nothing but eps' share
         a, b = out[:n - 1].float(), out[:1].float()
         assert bool(((a - b).norm(dim=(1, 2)) <= 2.0 ** -8 * b.norm()).all())
+
+
+@pytest.mark.parametrize("n,r,c", [(2, 64, 256), (3, 256, 60), (1, 7, 9)])
+@pytest.mark.parametrize("steps", [8, 64])
+def test_weak_directions_of_small_matrices(n, r, c, steps):
+    rng = np.random.default_rng(r)
+    G = torch.from_numpy(np.stack([weak(rng, r, c, 1e-3) for _ in range(n)]).astype(np.float32))
+    out = ortho(G.to(dev()), steps=steps).double().cpu().numpy()
+    for g, o in zip(G.double().numpy(), out):
+        ref = ot.newton_schulz(g, steps, USUAL, 1e-7)
+        assert np.linalg.norm(o - ref) <= LIMIT * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("shape", [(130, 300), (300, 130)])
+def test_split_steps_zero_and_non_finite_matrices(shape):
+    rng = np.random.default_rng(5)
+    G = torch.from_numpy(rng.standard_normal((4, *shape)).astype(np.float32)).to(dev())
+    alone = ortho(G[2:3], steps=10)
+    G[0] = 0
+    G[1, 5, 6] = float("nan")
+    G[3, 2, 3] = float("inf")
+    out = ortho(G, steps=10)
+    assert bool((out[0] == 0).all()) and torch.equal(out[2:3], alone)
+    assert bool(torch.isnan(out[1]).all()) and bool(torch.isnan(out[3]).all())
+
+
+def test_split_steps_captured_and_on_another_stream():
+    """A captured call of ten steps replays to the eager result, with eager calls on the same
+    buffers between the replays and a call on another stream meanwhile."""
+    rng = np.random.default_rng(6)
+    G = torch.from_numpy(rng.standard_normal((2, 200, 333)).astype(np.float32)).to(dev())
+    H = G[:, :150, :].contiguous().bfloat16()
+    size = pg.pg_orthogonalize_workspace_size(2, 200, 333)
+    ws, ws2 = (torch.empty(size, dtype=torch.uint8, device=dev()) for _ in range(2))
+    out, out2 = torch.empty_like(G, dtype=torch.bfloat16), torch.empty_like(H)
+    want, want2 = ortho(G, steps=10), ortho(H, steps=7, scale=0.5)
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        pg.pg_orthogonalize(G, out, ws, steps=10)
+    for _ in range(3):
+        out.zero_()
+        ws.fill_(255)
+        torch.cuda.synchronize()
+        graph.replay()
+        pg.pg_orthogonalize(H, out2, ws2, steps=7, scale=0.5, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(out2, want2)
+        out2.zero_()
+        pg.pg_orthogonalize(G, out, ws)              # five steps, unsplit, on the same buffers
+        torch.cuda.synchronize()
+        assert not torch.equal(out, want)
+
+
+@pytest.mark.parametrize("n,r,c", [(200, 256, 256),    # Gram and polynomial 128, update 256
+                                   (100, 500, 250),    # the same, ragged and tall
+                                   (30, 250, 200)])    # 64 x 64 in four stages
+@pytest.mark.parametrize("steps", [6, 10])
+def test_split_steps_on_the_other_tiles(n, r, c, steps):
+    rng = np.random.default_rng(n)
+    two = np.stack([weak(rng, r, c, 1e-3) for _ in range(2)]).astype(np.float32)
+    G = torch.from_numpy(two).to(dev()).repeat(n // 2, 1, 1)
+    out = ortho(G, steps=steps)
+    assert torch.equal(out, out[:2].repeat(n // 2, 1, 1)) and torch.equal(ortho(G, steps=steps), out)
+    for g, o in zip(two.astype(np.float64), out[:2].double().cpu().numpy()):
+        ref = ot.newton_schulz(g, steps, USUAL, 1e-7)
+        assert np.linalg.norm(o - ref) <= LIMIT * np.linalg.norm(ref)

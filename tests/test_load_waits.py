@@ -55,7 +55,7 @@ def parse(text):
 def written(op, ops):
     """(scalar registers written, by a vector instruction?)"""
     if op.startswith("v_"):
-        n = 2 if "_co_" in op or "div_scale" in op else 1
+        n = 2 if re.search(r"_co_|div_scale|mad_[ui]64", op) else 1    # a carry or flag too
         return set().union(*(scalars(x) for x in ops[:n])), True
     if op.startswith("s_") and not re.match(r"s_(cmp|bitcmp|waitcnt|nop|c?branch|barrier)", op):
         return scalars(ops[0]), False
