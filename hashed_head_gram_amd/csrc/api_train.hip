@@ -93,14 +93,15 @@ bool ortho_in_range(double a, double b, double c, int steps) {
 // Leading steps whose operands have to be split in halves. The rounding of the
 // fp16 operands of step k enters in proportion to B's size there and is moved
 // by the steps behind it as s is: their composed slope, largest on 33 points
-// of [0, m] (at 0 it is |a| a step). On spectra that suffer most (half the
-// directions 1e-2 to 1e-4 of the others), simulated in float64 with fp16
-// operands, the sum of size times slope over the steps moves the result by
-// 6.5e-6 of it in the 2-norm: 600 are half a step of the result's bf16, 2^-8.
-// Five steps of the usual coefficients come to 550. Where all steps together
-// pass 600, only the last ones stay unsplit, up to 120: by then the singular
-// values are large, and with them what is rounded.
-constexpr double kSumAll = 600, kSumLast = 120;
+// of [0, m] (at 0 it is |a| a step). On spectra that suffer most (an eighth to
+// half of the directions strong, the others 1e-2 to 1e-4 of them), simulated in
+// float64 with fp16 operands, a sum of size times slope of 1 moves the result
+// by up to 7e-6 of it in the 2-norm: 600 are about half a step of the result's
+// bf16, 2^-8. Five steps of the usual coefficients come to 548 and 4.0e-3.
+// Where all steps together pass 600, only the last ones stay unsplit, up to 80:
+// by then the singular values are large, and with them what is rounded. Seven
+// polynomials at 5 to 20 steps: none moved the result by more than 4.0e-3.
+constexpr double kSumAll = 600, kSumLast = 80;
 int ortho_split(double a, double b, double c, int steps) {
   double m[kMaxOrthoSteps + 1];
   m[0] = 1.0;

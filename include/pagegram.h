@@ -721,13 +721,13 @@ PG_API int64_t pg_orthogonalize_workspace_size(int64_t n_mat, int32_t rows,
  *   (PG_ERANGE); 1 <= steps <= 64. The products run in fp16 with fp32
  *   accumulation, the iterate and the diagonals in fp32. That rounding moves
  *   the result by 4e-4 to 7e-4 of it (2-norm) on common spectra, and by up to
- *   2^-8, half a step of bf16, where G has many weak directions, in which it
- *   grows from step to step. The leading steps of calls in which it could
- *   grow further (more than 5 steps of the usual coefficients), and matrices
- *   small enough for one compute unit's memory, take each operand as two fp16
- *   halves, about 22 bits. Coefficients under which a singular value in
- *   [0, 1] could pass 3 before a step, or b s^2 + c s^4 pass 100 in
- *   magnitude, are refused (PG_EUNSUPPORTED).
+ *   about 2^-8, half a step of bf16, where G has many weak directions, in
+ *   which it grows from step to step. The leading steps of calls in which it
+ *   could grow further (more than 5 steps of the usual coefficients), and
+ *   matrices small enough for one compute unit's memory, take each operand as
+ *   two fp16 halves, about 22 bits. Coefficients that are not finite, or under
+ *   which a singular value in [0, 1] could pass 3 before a step, or
+ *   b s^2 + c s^4 pass 100 in magnitude, are refused (PG_EUNSUPPORTED).
  *   workspace of pg_orthogonalize_workspace_size bytes, 256-byte aligned
  */
 PG_API int pg_orthogonalize(const void* G, int32_t dtype, int64_t n_mat,
