@@ -105,6 +105,19 @@ _SIGS = {
     "pg_orthogonalize_workspace_size": (_i64, [_i64, _i32, _i32]),
     "pg_orthogonalize": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _f32, _f32, _f32, _f32, _f32,
                                 _vp, _vp, _i64, _vp]),
+    "pg_head_loss_workspace_size": (_i64, [_i64, _i32, _i64, _i32]),
+    "pg_head_loss_backward_workspace_size": (_i64, [_i64, _i32, _i64, _i32]),
+    "pg_head_distill_workspace_size": (_i64, [_i64, _i32, _i64, _i32, _i32]),
+    "pg_head_distill_backward_workspace_size": (_i64, [_i64, _i32, _i64, _i32, _i32]),
+    "pg_head_loss": (_i32, [_vp, _i32, _i64, _i32, _i64, _P(PgTable), _f32, _vp, _vp, _vp, _vp,
+                            _i64, _vp]),
+    "pg_head_loss_backward": (_i32, [_vp, _i32, _i64, _i32, _i64, _P(PgTable), _f32, _vp, _vp, _vp,
+                                     _vp, _vp, _i64, _vp, _i32, _i32, _vp, _i64, _vp]),
+    "pg_head_distill": (_i32, [_vp, _i32, _i64, _i32, _i64, _P(PgTable), _f32, _vp, _vp, _i32,
+                               _f32, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "pg_head_distill_backward": (_i32, [_vp, _i32, _i64, _i32, _i64, _P(PgTable), _f32, _vp, _vp,
+                                        _i32, _f32, _vp, _vp, _vp, _vp, _i64, _vp, _i32, _i32, _vp,
+                                        _i64, _vp]),
     "pg_flash_blocks": (_i32, [_P(PgLayout), _i32, _vp, _i64, _vp]),
     "pg_lru_cache_sim": (_i32, [_vp, _i64, _i32, _i64, _P(PgCacheStats)]),
 }
@@ -677,6 +690,126 @@ def pg_orthogonalize(G, out, workspace, steps=5, coef=(3.4445, -4.7750, 2.0315),
     _call(fn, dev, stream, _ptr(G), _dtype(fn, "G", G), n_mat, _in32(rows), _in32(cols),
           _in32(int(steps)), a, b, c, float(eps), float(scale), _ptr(out), _ptr(workspace),
           _ws_bytes(workspace))
+
+
+# ----------------------------------------------------------------------------
+# Losses of the head over the token table (make_table), and their gradients.
+
+
+def pg_head_loss_workspace_size(n, d, V, dtype):
+    return _size("pg_head_loss_workspace_size", n, d, V, dtype)
+
+
+def pg_head_loss_backward_workspace_size(n, d, V, dtype):
+    return _size("pg_head_loss_backward_workspace_size", n, d, V, dtype)
+
+
+def pg_head_distill_workspace_size(n, d, V, k, dtype):
+    return _size("pg_head_distill_workspace_size", n, d, V, k, dtype)
+
+
+def pg_head_distill_backward_workspace_size(n, d, V, k, dtype):
+    return _size("pg_head_distill_backward_workspace_size", n, d, V, k, dtype)
+
+
+def _head(fn, h, table, workspace):
+    """(device, leading C arguments) of a head call: h and the table it is multiplied with."""
+    import torch
+    dev = _gpu(fn, "h", h)
+    n, ld = _rows(fn, "h", h)
+    d = h.shape[-1]
+    data = table._keep[0] if hasattr(table, "_keep") else None
+    if hasattr(data, "numel") and table.dtype != PG_NF4:
+        want = torch.float32 if table.dtype == PG_F32 else torch.bfloat16
+        _flat(fn, "table data", data, want, table.n_rows * d, dev)
+    _work(fn, workspace, dev)
+    return dev, n, (_ptr(h), _dtype(fn, "h", h), n, _in32(d), ld, ctypes.byref(table))
+
+
+def _head_grads(fn, h, table, dh, dw, accumulate):
+    """C arguments dh .. accumulate."""
+    ld, code = 0, PG_F32
+    if dh is not None:
+        _like(fn, "dh", dh, h)
+        ld = _rows(fn, "dh", dh)[1]
+    if dw is not None:
+        code = _dtype(fn, "dw", dw)
+        _flat(fn, "dw", dw, dw.dtype, table.n_rows * h.shape[-1], h.device)
+    return _ptr(dh), ld, _ptr(dw), code, _in32(int(accumulate))
+
+
+def _entries(fn, ids, teacher, n, dev):
+    """k of ids int32 and teacher float32 [n, k]."""
+    import torch
+    if ids is None or ids.dim() < 1:
+        raise ValueError(f"{fn}: ids must be an int32 tensor [..., k]")
+    k = ids.shape[-1]
+    _flat(fn, "ids", ids, torch.int32, n * k, dev)
+    _flat(fn, "teacher", teacher, torch.float32, n * k, dev)
+    return k
+
+
+def pg_head_loss(h, table, targets, loss, lse, workspace, scale=1.0, stream=None):
+    """loss, lse (float32, one a row of h): cross entropy of scale * h table^T against targets
+    (int32; outside the table: loss 0) and the log of the sum of exponentials."""
+    import torch
+    fn = "pg_head_loss"
+    dev, n, lead = _head(fn, h, table, workspace)
+    _flat(fn, "targets", targets, torch.int32, n, dev)
+    _flat(fn, "loss", loss, torch.float32, n, dev)
+    _flat(fn, "lse", lse, torch.float32, n, dev)
+    _call(fn, dev, stream, *lead, float(scale), _ptr(targets), _ptr(loss), _ptr(lse),
+          _ptr(workspace), _ws_bytes(workspace))
+
+
+def pg_head_loss_backward(h, table, targets, lse, dloss, dh, dw, workspace, dlse=None, scale=1.0,
+                          accumulate=0, stream=None):
+    """dh (as h, or None) and dw (the table's gradient [V, d], float32 or bfloat16, or None) from
+    pg_head_loss's lse and the gradients dloss and dlse (or None) of its outputs; accumulate=1
+    adds to a float32 dw."""
+    import torch
+    fn = "pg_head_loss_backward"
+    dev, n, lead = _head(fn, h, table, workspace)
+    _flat(fn, "targets", targets, torch.int32, n, dev)
+    _flat(fn, "lse", lse, torch.float32, n, dev)
+    _flat(fn, "dloss", dloss, torch.float32, n, dev)
+    if dlse is not None:
+        _flat(fn, "dlse", dlse, torch.float32, n, dev)
+    _call(fn, dev, stream, *lead, float(scale), _ptr(targets), _ptr(lse), _ptr(dloss), _ptr(dlse),
+          *_head_grads(fn, h, table, dh, dw, accumulate), _ptr(workspace), _ws_bytes(workspace))
+
+
+def pg_head_distill(h, table, ids, teacher, loss, lse, logits, workspace, temperature=1.0,
+                    scale=1.0, stream=None):
+    """loss, lse (float32, one a row of h): divergence of the softmax of scale * h table^T at
+    `temperature` from a teacher's, given by its logits (float32 [..., k]) of the tokens ids (int32;
+    outside the table: none); logits (float32 [..., k]): the student's at the ids."""
+    import torch
+    fn = "pg_head_distill"
+    dev, n, lead = _head(fn, h, table, workspace)
+    k = _entries(fn, ids, teacher, n, dev)
+    _flat(fn, "loss", loss, torch.float32, n, dev)
+    _flat(fn, "lse", lse, torch.float32, n, dev)
+    _flat(fn, "logits", logits, torch.float32, n * k, dev)
+    _call(fn, dev, stream, *lead, float(scale), _ptr(ids), _ptr(teacher), _in32(k),
+          float(temperature), _ptr(loss), _ptr(lse), _ptr(logits), _ptr(workspace),
+          _ws_bytes(workspace))
+
+
+def pg_head_distill_backward(h, table, ids, teacher, lse, logits, dloss, dh, dw, workspace,
+                             temperature=1.0, scale=1.0, accumulate=0, stream=None):
+    """dh and dw (as pg_head_loss_backward's) from pg_head_distill's lse and logits and the gradient
+    dloss of its loss."""
+    import torch
+    fn = "pg_head_distill_backward"
+    dev, n, lead = _head(fn, h, table, workspace)
+    k = _entries(fn, ids, teacher, n, dev)
+    _flat(fn, "lse", lse, torch.float32, n, dev)
+    _flat(fn, "logits", logits, torch.float32, n * k, dev)
+    _flat(fn, "dloss", dloss, torch.float32, n, dev)
+    _call(fn, dev, stream, *lead, float(scale), _ptr(ids), _ptr(teacher), _in32(k),
+          float(temperature), _ptr(lse), _ptr(logits), _ptr(dloss),
+          *_head_grads(fn, h, table, dh, dw, accumulate), _ptr(workspace), _ws_bytes(workspace))
 
 
 # ----------------------------------------------------------------------------

@@ -10,6 +10,7 @@ namespace {
 constexpr int64_t kMaxEmbedTokens = ((int64_t)1 << 26) - 1;
 constexpr int kMaxEmbedD = 16384;
 constexpr int64_t kMaxNormRows = (int64_t)1 << 31;
+constexpr int64_t kMaxHeadTokens = ((int64_t)1 << 26) - 1;
 constexpr int kMaxOrthoSide = 16384;
 constexpr int kMaxOrthoSteps = 64;
 
@@ -49,6 +50,83 @@ int check_ortho(int64_t n_mat, int32_t rows, int32_t cols) {
   const auto pad = [](int64_t x) { return (x + 127) / 128 * 128; };
   if (n_mat * pad(rows) * pad(cols) > (int64_t)1 << 34) return PG_ERANGE;
   return PG_OK;
+}
+
+int check_head(int64_t n, int32_t d, int64_t V, int32_t dtype, int32_t k) {
+  if (n < 0 || d < 1 || V < 1 || k < 1 || !float_dtype(dtype)) return PG_EINVAL;
+  if (d > pg::kHeadMaxD || k > pg::kHeadMaxK) return PG_EUNSUPPORTED;
+  if (n > kMaxHeadTokens || V > INT_MAX - 1) return PG_ERANGE;
+  // tiles are numbered in 32 bits
+  if ((n / 128 + 1) * (V / 128 + 1) > INT_MAX) return PG_ERANGE;
+  return PG_OK;
+}
+
+// The checks of all four head calls. n, the sizes and the flags are looked at
+// before n = 0 returns; g.logits: distillation.
+int check_head_call(const pg::HeadArgs& g, const pg_table* table, int32_t d, float temperature,
+                    bool distill) {
+  if (!table || !table->data || !aligned(table->data, 16)) return PG_EINVAL;
+  if (table->dtype == PG_NF4) return PG_EUNSUPPORTED;
+  const int st = check_head(g.n, d, table->n_rows, table->dtype, g.k);
+  if (st != PG_OK) return st;
+  if (!float_dtype(g.dtype)) return PG_EINVAL;
+  if (g.dtype != table->dtype) return PG_EUNSUPPORTED;
+  if (!isfinite(g.scale) || !(temperature > 0.f) || !isfinite(temperature) ||
+      !isfinite(1.f / temperature))
+    return PG_EINVAL;
+  if (g.ld_h < d) return PG_EINVAL;
+  if (g.n == 0) return PG_OK;
+  if (!g.h || !aligned(g.h, elt(g.dtype)) || !g.ids || !aligned(g.ids, 4)) return PG_EINVAL;
+  if (!g.lse || !aligned(g.lse, 4)) return PG_EINVAL;
+  if (distill && (!g.teacher || !aligned(g.teacher, 4) || !g.logits || !aligned(g.logits, 4)))
+    return PG_EINVAL;
+  return PG_OK;
+}
+
+int head_forward(pg::HeadArgs& g, const pg_table* table, int32_t d, float temperature,
+                 bool distill, void* ws, int64_t ws_bytes, hipStream_t stream) {
+  const int st = check_head_call(g, table, d, temperature, distill);
+  if (st != PG_OK || g.n == 0) return st;
+  if (!g.loss || !aligned(g.loss, 4)) return PG_EINVAL;
+  g.d = d;
+  g.table = table->data;
+  g.V = table->n_rows;
+  g.inv_tau = 1.f / temperature;
+  const pg::HeadPlan p = pg::head_plan(g.n, d, g.V, g.dtype, g.k, false);
+  if (!ws || ws_bytes < p.bytes || !aligned(ws, 256)) return PG_EINVAL;
+  return hip_status(pg::launch_head_forward(p, g, ws, stream));
+}
+
+int head_backward(pg::HeadArgs& g, const pg_table* table, int32_t d, float temperature,
+                  bool distill, void* ws, int64_t ws_bytes, hipStream_t stream) {
+  if (g.accumulate != 0 && g.accumulate != 1) return PG_EINVAL;
+  if (!g.dh && !g.dw) return PG_EINVAL;
+  if (g.dw && (!float_dtype(g.dw_dtype) || !aligned(g.dw, elt(g.dw_dtype)))) return PG_EINVAL;
+  if (g.dw && g.accumulate && g.dw_dtype != PG_F32) return PG_EUNSUPPORTED;
+  const int st = check_head_call(g, table, d, temperature, distill);
+  if (st != PG_OK) return st;
+  if (g.dh && (g.ld_dh < d || !aligned(g.dh, elt(g.dtype)))) return PG_EINVAL;
+  g.d = d;
+  g.table = table->data;
+  g.V = table->n_rows;
+  g.inv_tau = 1.f / temperature;
+  if (g.n > 0 && (!g.dloss || !aligned(g.dloss, 4) || !aligned(g.dlse, 4))) return PG_EINVAL;
+  const pg::HeadPlan p = pg::head_plan(g.n, d, g.V, g.dtype, g.k, true);
+  if (g.n > 0 && (!ws || ws_bytes < p.bytes || !aligned(ws, 256))) return PG_EINVAL;
+  return hip_status(pg::launch_head_backward(p, g, ws, stream));
+}
+
+// Largest workspace of any batch up to n: pieces get narrower as batches grow.
+int64_t head_workspace(int64_t n, int32_t d, int64_t V, int32_t dtype, int32_t k, bool backward) {
+  const int st = check_head(n, d, V, dtype, k);
+  if (st != PG_OK) return st;
+  int64_t most = pg::head_plan(n, d, V, dtype, k, backward).bytes;
+  if (backward)
+    for (int64_t m = 128; m < n && m <= 32768; m += 128) {
+      const int64_t b = pg::head_plan(m, d, V, dtype, k, true).bytes;
+      if (b > most) most = b;
+    }
+  return most;
 }
 
 // Largest |a s + b s^3 + c s^5| over 0 <= s <= m: the ends and the interior
@@ -271,6 +349,117 @@ PG_API int pg_orthogonalize(const void* G, int32_t dtype, int64_t n_mat, int32_t
   const pg::OrthoArgs oa{steps, p.small ? 0 : ortho_split(a, b, c, steps), a, b, c, eps, scale};
   return hip_status(pg::launch_orthogonalize(p, G, dtype, n_mat, rows, cols, oa,
                                              static_cast<uint16_t*>(out), workspace, stream));
+}
+
+// ---------------------------------------------------------------------------
+// Losses of the head
+
+PG_API int64_t pg_head_loss_workspace_size(int64_t n, int32_t d, int64_t V, int32_t dtype) {
+  return head_workspace(n, d, V, dtype, 1, false);
+}
+
+PG_API int64_t pg_head_loss_backward_workspace_size(int64_t n, int32_t d, int64_t V,
+                                                    int32_t dtype) {
+  return head_workspace(n, d, V, dtype, 1, true);
+}
+
+PG_API int64_t pg_head_distill_workspace_size(int64_t n, int32_t d, int64_t V, int32_t k,
+                                              int32_t dtype) {
+  return head_workspace(n, d, V, dtype, k, false);
+}
+
+PG_API int64_t pg_head_distill_backward_workspace_size(int64_t n, int32_t d, int64_t V, int32_t k,
+                                                       int32_t dtype) {
+  return head_workspace(n, d, V, dtype, k, true);
+}
+
+PG_API int pg_head_loss(const void* h, int32_t dtype, int64_t n, int32_t d, int64_t ld_h,
+                        const pg_table* table, float scale, const int32_t* targets, float* loss,
+                        float* lse, void* workspace, int64_t workspace_bytes,
+                        hipStream_t stream) {
+  pg::HeadArgs g{};
+  g.h = h;
+  g.dtype = dtype;
+  g.n = n;
+  g.ld_h = ld_h;
+  g.scale = scale;
+  g.ids = targets;
+  g.k = 1;
+  g.loss = loss;
+  g.lse = lse;
+  return head_forward(g, table, d, 1.f, false, workspace, workspace_bytes, stream);
+}
+
+PG_API int pg_head_loss_backward(const void* h, int32_t dtype, int64_t n, int32_t d, int64_t ld_h,
+                                 const pg_table* table, float scale, const int32_t* targets,
+                                 const float* lse, const float* dloss, const float* dlse,
+                                 void* dh, int64_t ld_dh, void* dw, int32_t dw_dtype,
+                                 int32_t accumulate, void* workspace, int64_t workspace_bytes,
+                                 hipStream_t stream) {
+  pg::HeadArgs g{};
+  g.h = h;
+  g.dtype = dtype;
+  g.n = n;
+  g.ld_h = ld_h;
+  g.scale = scale;
+  g.ids = targets;
+  g.k = 1;
+  g.lse = const_cast<float*>(lse);
+  g.dloss = dloss;
+  g.dlse = dlse;
+  g.dh = dh;
+  g.ld_dh = ld_dh;
+  g.dw = dw;
+  g.dw_dtype = dw_dtype;
+  g.accumulate = accumulate;
+  return head_backward(g, table, d, 1.f, false, workspace, workspace_bytes, stream);
+}
+
+PG_API int pg_head_distill(const void* h, int32_t dtype, int64_t n, int32_t d, int64_t ld_h,
+                           const pg_table* table, float scale, const int32_t* ids,
+                           const float* teacher, int32_t k, float temperature, float* loss,
+                           float* lse, float* logits, void* workspace, int64_t workspace_bytes,
+                           hipStream_t stream) {
+  pg::HeadArgs g{};
+  g.h = h;
+  g.dtype = dtype;
+  g.n = n;
+  g.ld_h = ld_h;
+  g.scale = scale;
+  g.ids = ids;
+  g.teacher = teacher;
+  g.k = k;
+  g.loss = loss;
+  g.lse = lse;
+  g.logits = logits;
+  return head_forward(g, table, d, temperature, true, workspace, workspace_bytes, stream);
+}
+
+PG_API int pg_head_distill_backward(const void* h, int32_t dtype, int64_t n, int32_t d,
+                                    int64_t ld_h, const pg_table* table, float scale,
+                                    const int32_t* ids, const float* teacher, int32_t k,
+                                    float temperature, const float* lse, const float* logits,
+                                    const float* dloss, void* dh, int64_t ld_dh, void* dw,
+                                    int32_t dw_dtype, int32_t accumulate, void* workspace,
+                                    int64_t workspace_bytes, hipStream_t stream) {
+  pg::HeadArgs g{};
+  g.h = h;
+  g.dtype = dtype;
+  g.n = n;
+  g.ld_h = ld_h;
+  g.scale = scale;
+  g.ids = ids;
+  g.teacher = teacher;
+  g.k = k;
+  g.lse = const_cast<float*>(lse);
+  g.logits = const_cast<float*>(logits);
+  g.dloss = dloss;
+  g.dh = dh;
+  g.ld_dh = ld_dh;
+  g.dw = dw;
+  g.dw_dtype = dw_dtype;
+  g.accumulate = accumulate;
+  return head_backward(g, table, d, temperature, true, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

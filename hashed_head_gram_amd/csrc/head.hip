@@ -1,0 +1,1549 @@
+// Losses of the head over a large vocabulary (gfx950): cross entropy and
+// distillation from a teacher's largest logits, forward and backward.
+//
+//   z_nv = scale h_n . T_v            (T: the token table, tied)
+//   lse_n = log sum_v exp(z_nv / tau)
+//   dz_nv = a_n exp(z_nv / tau - lse_n) - (sparse part)
+//   dh = dz T,  dT = dz^T h
+//
+// The logits are never kept. Forward: tiles of 256 tokens x 256 rows of the
+// table on the matrix cores; a tile leaves one running maximum and sum a
+// token, a second kernel joins them along the vocabulary and takes the few
+// logits that the targets name as dot products of their own. Backward, piece
+// by piece of the vocabulary: the tiles again, now with the softmax's
+// statistics known, leave dz of the piece; the sparse positions are written
+// over it with values rounded once; then one launch forms both products of the
+// piece, dh adding up in fp32 from piece to piece.
+//
+// Number formats. bf16 operands enter the logits as they are. dz is held in
+// fp16, not bf16: it is the sum's dominant rounding (bf16 took dh from 1.7e-3
+// to 2.6e-3 off in the 2-norm, of which 1.65e-3 is the result's own rounding;
+// fp16 leaves it there). Powers of two keep it in range: each row of dz is
+// placed by its own bound, which dh's rows undo; h for dT carries the inverse of
+// its row's placement, T is placed by its largest element. So a product's
+// second operands are fp16 copies of h and T, exact for bf16 values down to
+// 2^-31 of the largest. fp32 operands, and dz with them, are two fp16 halves
+// (22 bits), multiplied as hi lo, lo hi and hi hi, one K three times as long;
+// h for the logits is placed row by row.
+#include <type_traits>
+
+#include "train.h"
+
+namespace pg {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16v2_t __attribute__((ext_vector_type(2)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8_t __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void lds_void_t;
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kCUs = 256;
+constexpr int kRing = 4;                  // slots in the LDS ring
+// halves of the two operands by segment of K, small products first
+constexpr int kSegs = 3;
+__device__ __forceinline__ int seg_a(int s) { return s == 1; }
+__device__ __forceinline__ int seg_b(int s) { return s == 0; }
+constexpr int kTop = 14;                  // exponent that placements bring the largest value to
+constexpr int kNone = -4096;              // exponent of nothing
+
+// Two floats to packed fp16, nearest even.
+__device__ __forceinline__ uint32_t pack2_f16(float a, float b) {
+  const f32v2_t v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16v2_t));
+}
+__device__ __forceinline__ float lo_f16(uint32_t w) {
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)w);
+}
+__device__ __forceinline__ float hi_f16(uint32_t w) {
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16));
+}
+// x with 2^e: floor(log2 |x|); nothing for zeros, infinities and NaN.
+__device__ __forceinline__ int exponent_of(float x) {
+  const float a = fabsf(x);
+  return a > 0.f && a < INFINITY ? ilogbf(a) : kNone;
+}
+
+// s_waitcnt with only a vmcnt limit (vmcnt[3:0], expcnt[6:4], lgkmcnt[11:8],
+// vmcnt[5:4] in bits [15:14]).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+__device__ __forceinline__ void wait_lds() {
+  __builtin_amdgcn_s_waitcnt(0xF | (7 << 4) | (0 << 8) | (3 << 14));
+}
+__device__ __forceinline__ void barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Direct global-to-LDS loads: each lane moves 16 (4) bytes from base + off, the
+// wave 1 KiB (256 bytes) to LDS address lds + 16 (4) lane. No memory clobber:
+// the ring orders them with counted waits and barriers. s_nop: the wait state
+// between the write of M0 and a load that reads it.
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds));
+}
+__device__ __forceinline__ void load_to_lds4(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(base), "{m0}"(lds));
+}
+
+// One operand of a product. Plain: `outer` rows of K contiguous elements.
+// Transposed: K rows of `outer` contiguous elements.
+struct Side {
+  const uint8_t* p;
+  int64_t ld;          // bytes between rows
+  int64_t plane;       // bytes between planes
+  int64_t outer;       // valid rows (plain) or columns, a multiple of 8 (transposed)
+};
+
+struct TileArgs {
+  Side A, B;           // A: the index that lies over lanes, B: over accumulators
+  int nseg;            // 1, or 3 products of halves
+  int slots;           // slots of 32 of K in all
+  int splits;          // K is shared by this many tiles, each with a result of its own
+  int nbm, nbn;        // tiles
+  float c2;            // scale log2(e) / tau
+  // running maximum and sum
+  float2* part;        // [nbn][M]
+  int64_t M, V;        // valid rows, valid columns
+  const float* rowf;       // fp16 operands: c2 with the placements undone, by row
+  // gradient of the logits
+  const float *a, *lse2;   // [rows padded to whole tiles]
+  uint16_t* dz;
+  int64_t ldz, dz_plane;   // elements
+  int64_t Mpad, Vpad;      // rows and columns of dz that exist
+  // products
+  void* out;
+  int64_t ld_out, split_out;   // elements; between the results of two splits
+  int out_bf16;
+  const float* prev;   // added (nullable); may be out
+  int64_t ld_prev;
+  const int* row_exp;  // results times 2^(row_exp[row] + *all_exp); each nullable
+  const int* all_exp;
+};
+
+enum { EPI_LSE, EPI_DZ, EPI_OUT };
+
+// One side's walk over K: this wave's part of every slot.
+template <int BX, bool TR, int NW>
+struct Walk {
+  static constexpr int DMA = BX / 16 / NW;           // loads of 1 KiB a wave and slot
+  static_assert(DMA >= 1 && BX % (16 * NW) == 0, "whole loads");
+  const uint8_t* base;
+  uint32_t off[DMA];
+  int64_t step;
+
+  // A slot's row is 64 bytes of K (plain; four 16-byte chunks, chunk c of row r
+  // at c ^ (r / 4) % 4) or BX elements (transposed; 64-byte units, unit u of
+  // row k at u ^ k % 4, or u ^ (k / 2) % 2 where a row has only two): a
+  // fragment read then meets every bank of a 256-byte line once.
+  __device__ __forceinline__ void start(const Side& s, int64_t outer0, int slot0, int wave,
+                                        int lane) {
+    if constexpr (!TR) {
+      const int dr = lane >> 2;
+      const uint32_t chunk = (uint32_t)(((lane & 3) ^ ((dr >> 2) & 3)) * 16);
+      const int64_t r0 = outer0 + wave * DMA * 16;
+      const int64_t rb = r0 < s.outer ? r0 : s.outer - 1;
+#pragma unroll
+      for (int q = 0; q < DMA; ++q) {
+        const int64_t r = r0 + q * 16 + dr;
+        const int64_t rc = r < s.outer ? r : s.outer - 1;
+        off[q] = (uint32_t)((rc - rb) * s.ld) + chunk;
+      }
+      step = 64;
+      base = s.p + rb * s.ld + slot0 * 64;
+    } else {
+      constexpr int kChunks = BX / 8, RPI = 64 / kChunks;
+      const int kr = lane / kChunks, cp = lane % kChunks;
+#pragma unroll
+      for (int q = 0; q < DMA; ++q) {
+        const int k = (wave * DMA + q) * RPI + kr;
+        const int f = BX >= 128 ? (k & 3) : ((k >> 1) & 1);
+        int64_t col = outer0 + (cp ^ (f * 4)) * 8;
+        if (col > s.outer - 8) col = s.outer - 8;
+        off[q] = (uint32_t)(k * s.ld + (col - outer0) * 2);
+      }
+      step = 32 * s.ld;
+      base = s.p + outer0 * 2 + slot0 * step;
+    }
+  }
+  __device__ __forceinline__ void issue(uint32_t lds, int wave) const {
+#pragma unroll
+    for (int q = 0; q < DMA; ++q) load_to_lds(base, off[q], lds + (wave * DMA + q) * 1024);
+  }
+  // fragment of 32 of the outer index from w0 on, K elements 16 t + 8 (lane / 32) ..
+  __device__ __forceinline__ static bf16x8_t frag(const uint8_t* slot, int w0, int t, int lane) {
+    if constexpr (!TR) {
+      const int fr = lane & 31, c = t * 2 + (lane >> 5);
+      return __builtin_bit_cast(
+          bf16x8_t, *reinterpret_cast<const uint4*>(slot + (w0 + fr) * 64 +
+                                                    ((c ^ ((fr >> 2) & 3)) * 16)));
+    } else {
+      // a transposing read gives lane i of 16 the i-th of 16 columns, four rows of K
+      const int k = t * 16 + 8 * (lane >> 5) + ((lane & 15) >> 2);
+      const int f = BX >= 128 ? ((lane & 15) >> 2) : ((lane & 15) >> 3);
+      const uint8_t* p = slot + k * BX * 2 + (((w0 >> 5) ^ f) * 64) + ((lane >> 4) & 1) * 32 +
+                         (lane & 3) * 8;
+      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)p);
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + 4 * BX * 2));
+      const s16x8_t v = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      return __builtin_bit_cast(bf16x8_t, v);
+    }
+  }
+};
+
+// Geometry of a tile kernel: BM x BN by WGM x WGN waves of (BM / WGM) x 64.
+template <int BM, int BN, int WGM, int WGN>
+struct Geo {
+  static constexpr int NW = WGM * WGN, NT = 64 * NW;
+  static constexpr int WTM = BM / WGM, WTN = BN / WGN, FM = WTM / 32, FN = WTN / 32;
+  static_assert(WTN == 64 && WTM % 32 == 0, "a wave's part");
+  static constexpr int kA = BM * 64, kB = BN * 64;   // bytes of a slot
+  static constexpr int kRingBytes = kRing * (kA + kB);
+  // row vectors (two tiles' up to three), then the waves' maxima and sums
+  static constexpr int kRows = 2 * 3 * BM * 4;
+  static constexpr int kExtra = kRows + BM * 8 * WGN;
+  static constexpr int kLds = kRingBytes + kExtra;
+  static_assert(kA + kB >= NW * 4096 || kRing * (kA + kB) >= NW * 4096, "patches");
+};
+
+// The tile of a product's numbering: groups of 8 M tiles, N-major inside, so
+// that tiles running together share their panels.
+__device__ __forceinline__ void tile_at(uint32_t id, uint32_t nbm, uint32_t nbn, uint32_t& bm,
+                                        uint32_t& bn) {
+  const uint32_t per_group = 8 * nbn, g = id / per_group, local = id - g * per_group;
+  const uint32_t rows = nbm - g * 8 < 8 ? nbm - g * 8 : 8;
+  bn = local / rows;
+  bm = g * 8 + (local - bn * rows);
+}
+
+// Walks the tiles next(0), next(1), ... of one block (0xFFFFFFFF: none). The
+// ring of four slots runs on from tile to tile: the last slots of a tile
+// request the first ones of the next, all but the fourth, whose place the
+// epilogue uses as scratch.
+template <int EPI, bool F16, int BM, int BN, int WGM, int WGN, bool TA, bool TB, typename Next>
+__device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Next next) {
+  using G = Geo<BM, BN, WGM, WGN>;
+  constexpr int NW = G::NW, FM = G::FM, FN = G::FN;
+  using WA = Walk<BM, TA, NW>;
+  using WB = Walk<BN, TB, NW>;
+  constexpr int LS = WA::DMA + WB::DMA;
+  static_assert(3 * LS < 60, "vmcnt");
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WGN, wn = wave % WGN;
+  const int fr = lane & 31, half = lane >> 5;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(const lds_void_t*)smem;
+  uint8_t* const smemB = smem + kRing * G::kA;
+  uint8_t* const extra = smem + G::kRingBytes;
+
+  struct Tile { uint32_t bm, bn, split; };
+  auto decode = [&](uint32_t id) {
+    Tile t;
+    const uint32_t mn = (uint32_t)g.nbm * g.nbn;
+    t.split = g.splits > 1 ? id / mn : 0;
+    tile_at(id - t.split * mn, g.nbm, g.nbn, t.bm, t.bn);
+    return t;
+  };
+  auto slot_range = [&](uint32_t split, int& s0, int& n) {
+    if (g.splits == 1) {
+      s0 = 0;
+      n = g.slots;
+      return;
+    }
+    s0 = (int)((int64_t)g.slots * split / g.splits);
+    n = (int)((int64_t)g.slots * (split + 1) / g.splits) - s0;
+  };
+
+  // the walk: where the next slot to request lies
+  WA wa;
+  WB wb;
+  const uint8_t *a00 = nullptr, *b00 = nullptr;
+  int seg_slots = 0, seg_at = 0, seg = 0;
+  auto set_seg = [&] {
+    wa.base = a00 + seg_a(seg) * g.A.plane;
+    wb.base = b00 + seg_b(seg) * g.B.plane;
+    seg_at = 0;
+  };
+  auto start_walk = [&](const Tile& t) {
+    int s0;
+    slot_range(t.split, s0, seg_slots);
+    wa.start(g.A, (int64_t)t.bm * BM, s0, wave, lane);
+    wb.start(g.B, (int64_t)t.bn * BN, s0, wave, lane);
+    a00 = wa.base;
+    b00 = wb.base;
+    seg = kSegs - g.nseg;
+    set_seg();
+  };
+  auto issue_a = [&](int ring) { wa.issue(lds0 + ring * G::kA, wave); };
+  auto issue_b = [&](int ring) {
+    wb.issue(lds0 + kRing * G::kA + ring * G::kB, wave);
+    wa.base += wa.step;
+    wb.base += wb.step;
+    if (++seg_at == seg_slots) {
+      ++seg;
+      if (seg < kSegs) set_seg();
+    }
+  };
+  // a tile's row vectors into the half of its parity
+  constexpr int NV = (EPI == EPI_DZ ? 2 : 0) + (EPI != EPI_OUT && F16 ? 1 : 0);
+  auto issue_rows = [&](const Tile& t, int parity) {
+    constexpr int per = BM / 64;                     // loads of 64 rows
+    if constexpr (NV > 0)
+#pragma unroll
+      for (int q = 0; q < (NV * per + NW - 1) / NW; ++q) {
+        const int x = q * NW + wave, v = x / per;
+        if (x < NV * per) {
+          const float* src = NV == 1 || v == 2 ? g.rowf : v == 0 ? g.a : g.lse2;
+          load_to_lds4(src + (int64_t)t.bm * BM + (x % per) * 64, (uint32_t)lane * 4,
+                       lds0 + G::kRingBytes + parity * (NV * BM * 4) + x * 256);
+        }
+      }
+  };
+
+  uint32_t id = next(0);
+  if (id == 0xFFFFFFFFu) return;
+  Tile cur = decode(id);
+  f32x16_t acc[FM][FN];
+  bf16x8_t fa[2][FM], fb[2][FN];
+
+  issue_rows(cur, 0);
+  start_walk(cur);
+#pragma unroll
+  for (int p = 0; p < kRing; ++p) {
+    issue_a(p);
+    if (p < kRing - 1) issue_b(p);
+  }
+  wait_loads<2 * LS + WA::DMA>();
+  barrier();
+  int ring0 = 0;                                     // ring place of the tile's first slot
+
+  for (int jt = 0;; ++jt) {
+    int s0, KS;
+    slot_range(cur.split, s0, KS);
+    KS *= g.nseg;
+    const uint32_t nid = next(jt + 1);
+    const bool more = nid != 0xFFFFFFFFu;
+    Tile nxt = cur;
+    if (more) nxt = decode(nid);
+
+    auto read_step = [&](int s, int t, bf16x8_t (&af)[FM], bf16x8_t (&bf)[FN]) {
+      const int b = (ring0 + s) & (kRing - 1);
+      const uint8_t* sa = smem + b * G::kA;
+      const uint8_t* sb = smemB + b * G::kB;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) af[i] = WA::frag(sa, wm * G::WTM + i * 32, t, lane);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) bf[j] = WB::frag(sb, wn * 64 + j * 32, t, lane);
+    };
+    constexpr int kReads = FM * (TA ? 2 : 1) + FN * (TB ? 2 : 1);
+    constexpr int kMma = FM * FN;
+    // MFMAs of a step, its fragment reads (kReads, when reads) spread between them
+    auto mma = [&](int i, int j, const bf16x8_t (&af)[FM], const bf16x8_t (&bf)[FN]) {
+      if constexpr (F16)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, bf[j]),
+                                                           __builtin_bit_cast(f16x8_t, af[i]),
+                                                           acc[i][j], 0, 0, 0);
+      else
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
+    };
+    auto spread = [&](auto first) {                  // first: MFMAs already issued
+      constexpr int kF = decltype(first)::value, kM = kMma - kF;
+      constexpr int per = (kReads + kM - 1) / kM;
+#pragma unroll
+      for (int x = 0; x < kM; ++x) {
+        if (x * per < kReads)
+          __builtin_amdgcn_sched_group_barrier(0x100, per, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      }
+    };
+
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+    read_step(0, 0, fa[0], fb[0]);
+
+    // Slot s: the second half of the request for slot s + 3 goes out, step 0
+    // reads step 1's fragments; at the barrier slot s + 1 has landed everywhere
+    // and slot s is read; step 1 starts the request of slot s + 4 into slot s's
+    // place and reads slot s + 1's first fragments. From slot KS - 4 on the
+    // requests are the next tile's first slots, or, behind the last tile, the
+    // same tile's again, which nothing reads.
+    auto step0 = [&](int s) {
+      read_step(s, 1, fa[1], fb[1]);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) mma(i, j, fa[0], fb[0]);
+      spread(std::integral_constant<int, 0>{});
+      __builtin_amdgcn_sched_barrier(0);
+      wait_loads<2 * LS>();
+      wait_lds();
+      barrier();
+    };
+    auto rest = [&] {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          if (i + j > 0) mma(i, j, fa[1], fb[1]);
+    };
+    for (int s = 0; s < KS - 1; ++s) {
+      __builtin_amdgcn_sched_barrier(0);
+      issue_b((ring0 + s + 3) & (kRing - 1));
+      if (s == KS - 4) {
+        issue_rows(nxt, (jt + 1) & 1);
+        start_walk(nxt);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      step0(s);
+      mma(0, 0, fa[1], fb[1]);
+      __builtin_amdgcn_sched_barrier(0);
+      issue_a((ring0 + s) & (kRing - 1));
+      __builtin_amdgcn_sched_barrier(0);
+      read_step(s + 1, 0, fa[0], fb[0]);
+      rest();
+      spread(std::integral_constant<int, 1>{});
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    issue_b((ring0 + KS + 2) & (kRing - 1));
+    __builtin_amdgcn_sched_barrier(0);
+    step0(KS - 1);
+    mma(0, 0, fa[1], fb[1]);
+    rest();
+
+    // ---- epilogue: a lane has, of each 32 x 32 block, row fr of A's index and
+    // 4 of B's from 8 q + 4 half on, q = 0 .. 3
+    const int free_slot = (ring0 + KS - 1) & (kRing - 1);
+    uint8_t* patch;                                  // 4 KiB of the wave's own
+    {
+      constexpr int inA = G::kA / 4096 < NW ? G::kA / 4096 : NW;
+      if constexpr (EPI != EPI_LSE) static_assert(inA + G::kB / 4096 >= NW, "patches");
+      patch = wave < inA ? smem + free_slot * G::kA + wave * 4096
+                         : smemB + free_slot * G::kB + (wave - inA) * 4096;
+    }
+    const int64_t m0 = (int64_t)cur.bm * BM + wm * G::WTM;
+    const int64_t n0 = (int64_t)cur.bn * BN + wn * 64;
+
+    const float* rows = reinterpret_cast<const float*>(extra) + (jt & 1) * NV * BM;
+    if constexpr (EPI == EPI_LSE) {
+      float2* red = reinterpret_cast<float2*>(extra + G::kRows);          // [WGN][BM]
+      const bool edge = n0 + 64 > g.V;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        float m = -INFINITY;
+        const float c2 = F16 ? rows[wm * G::WTM + i * 32 + fr] : g.c2;
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            float v = acc[i][j][q] * c2;
+            if (edge && n0 + j * 32 + 8 * (q >> 2) + 4 * half + (q & 3) >= g.V) v = -INFINITY;
+            acc[i][j][q] = v;
+            m = fmaxf(m, v);
+          }
+        m = fmaxf(m, __shfl_xor(m, 32));
+        const float ref = m == -INFINITY ? 0.f : m;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 16; ++q) sum += __builtin_amdgcn_exp2f(acc[i][j][q] - ref);
+        sum += __shfl_xor(sum, 32);
+        if (half == 0) red[wn * BM + wm * G::WTM + i * 32 + fr] = make_float2(m, sum);
+      }
+      wait_lds();
+      barrier();
+      for (int r = tid; r < BM; r += G::NT) {
+        float m = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < WGN; ++w) m = fmaxf(m, red[w * BM + r].x);
+        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int w = 0; w < WGN; ++w)
+          sum += red[w * BM + r].y * __builtin_amdgcn_exp2f(red[w * BM + r].x - ref);
+        const int64_t row = (int64_t)cur.bm * BM + r;
+        if (row < g.M) g.part[(int64_t)cur.bn * g.M + row] = make_float2(m, sum);
+      }
+    } else if constexpr (EPI == EPI_DZ) {
+      const bool edge = n0 + 64 > g.V;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const float a = rows[wm * G::WTM + i * 32 + fr];
+        const float l = rows[BM + wm * G::WTM + i * 32 + fr];
+        const float c2 = F16 ? rows[2 * BM + wm * G::WTM + i * 32 + fr] : g.c2;
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            // rows without weight give zeros whatever their logits are
+            float v = a == 0.f ? 0.f : a * __builtin_amdgcn_exp2f(acc[i][j][q] * c2 - l);
+            if (edge && n0 + j * 32 + 8 * (q >> 2) + 4 * half + (q & 3) >= g.V) v = 0.f;
+            acc[i][j][q] = v;
+          }
+#pragma unroll
+        for (int p = 0; p < (F16 ? 2 : 1); ++p) {
+          if (i + p > 0) wave_sync();
+          // rows of 128 bytes, 16-byte chunk c of row r at c ^ r % 8
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t lo = pack2_f16(acc[i][j][4 * q], acc[i][j][4 * q + 1]);
+              const uint32_t hi = pack2_f16(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+              if (F16) {                             // what the high half leaves
+                acc[i][j][4 * q] -= lo_f16(lo);
+                acc[i][j][4 * q + 1] -= hi_f16(lo);
+                acc[i][j][4 * q + 2] -= lo_f16(hi);
+                acc[i][j][4 * q + 3] -= hi_f16(hi);
+              }
+              *reinterpret_cast<uint2*>(patch + fr * 128 + (((j * 4 + q) ^ (fr & 7)) * 16) +
+                                        half * 8) = make_uint2(lo, hi);
+            }
+          wave_sync();
+          if (n0 < g.Vpad) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int r = x * 8 + (lane >> 3), c = lane & 7;
+              const uint4 v = *reinterpret_cast<const uint4*>(patch + r * 128 + ((c ^ (r & 7)) * 16));
+              const int64_t row = m0 + i * 32 + r;
+              if (row < g.Mpad)
+                *reinterpret_cast<uint4*>(g.dz + p * g.dz_plane + row * g.ldz + n0 + c * 8) = v;
+            }
+          }
+        }
+      }
+    } else {
+      const int64_t so = (int64_t)cur.split * g.split_out;
+      const int all_exp = g.all_exp ? *g.all_exp : 0;
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          if (i + j > 0) wave_sync();
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<float4*>(patch + fr * 128 + (((2 * q + half) ^ (fr & 7)) * 16)) =
+                make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                            acc[i][j][4 * q + 3]);
+          wave_sync();
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = x * 8 + (lane >> 3), c = lane & 7;
+            const float4 f =
+                *reinterpret_cast<const float4*>(patch + r * 128 + ((c ^ (r & 7)) * 16));
+            const int64_t row = m0 + i * 32 + r, col = n0 + j * 32 + c * 4;
+            const int left = (int)(g.V - col < 4 ? g.V - col : 4);
+            if (row >= g.M || left <= 0) continue;
+            const int e = all_exp + (g.row_exp ? g.row_exp[row] : 0);
+            float v[4] = {ldexpf(f.x, e), ldexpf(f.y, e), ldexpf(f.z, e), ldexpf(f.w, e)};
+            if (g.prev) {
+              const float* pv = g.prev + row * g.ld_prev + col;
+              if (left == 4) {
+                float t[4];
+                __builtin_memcpy(t, pv, 16);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) v[u] += t[u];
+              } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  if (u < left) v[u] += pv[u];
+              }
+            }
+            if (g.out_bf16) {
+              uint16_t* o = static_cast<uint16_t*>(g.out) + so + row * g.ld_out + col;
+              const uint2 w = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
+              if (left == 4) {
+                __builtin_memcpy(o, &w, 8);
+              } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  if (u < left) o[u] = (uint16_t)(((u & 2) ? w.y : w.x) >> (16 * (u & 1)));
+              }
+            } else {
+              float* o = static_cast<float*>(g.out) + so + row * g.ld_out + col;
+              if (left == 4) {
+                __builtin_memcpy(o, v, 16);
+              } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  if (u < left) o[u] = v[u];
+              }
+            }
+          }
+        }
+    }
+    if (!more) {
+      wait_loads<0>();                               // no load lands behind the block's end
+      return;
+    }
+    // every wave is done with the scratch: the next tile's fourth slot may land there
+    wait_lds();
+    barrier();
+    ring0 = (ring0 + KS) & (kRing - 1);
+    cur = nxt;
+    issue_a((ring0 + 3) & (kRing - 1));
+  }
+}
+
+// One product's tiles. Consecutive tile numbers run on one of the 8 XCDs and
+// share panels in its L2; a block walks every 1/8 grid-th of its XCD's range.
+template <int EPI, bool F16, int BM, int BN, int WGM, int WGN>
+__global__ __launch_bounds__(64 * WGM * WGN) void head_tile_kernel(TileArgs g) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[Geo<BM, BN, WGM, WGN>::kLds];
+  const uint32_t total = (uint32_t)g.nbm * g.nbn * g.splits, per = total / 8;
+  const uint32_t grid = gridDim.x;
+  auto next = [&](int j) -> uint32_t {
+    if (grid == total) {                             // a tile each
+      if (j > 0) return 0xFFFFFFFFu;
+      const uint32_t b = blockIdx.x;
+      return b < per * 8 ? (b & 7) * per + (b >> 3) : b;
+    }
+    const uint32_t g8 = grid / 8, xcd = blockIdx.x & 7, c = blockIdx.x >> 3;
+    const uint32_t n_main = c < per ? (per - c + g8 - 1) / g8 : 0;
+    if ((uint32_t)j < n_main) return xcd * per + c + g8 * j;
+    if ((uint32_t)j == n_main && blockIdx.x < total - 8 * per) return 8 * per + blockIdx.x;
+    return 0xFFFFFFFFu;
+  };
+  walk_tiles<EPI, F16, BM, BN, WGM, WGN, false, false>(g, smem, next);
+}
+
+// Both gradients' products of a piece in one launch, a tile each: the first
+// nw blocks dT = dz^T h (both operands transposed), the others dh = dz T.
+template <int BM, int BN, int WGM, int WGN>
+__global__ __launch_bounds__(64 * WGM * WGN) void head_grad_kernel(TileArgs w, TileArgs h, uint32_t nw) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[Geo<BM, BN, WGM, WGN>::kLds];
+  auto one = [](uint32_t b, uint32_t total) {
+    const uint32_t per = total / 8;
+    return b < per * 8 ? (b & 7) * per + (b >> 3) : b;
+  };
+  if (blockIdx.x < nw) {
+    const uint32_t id = one(blockIdx.x, nw);
+    walk_tiles<EPI_OUT, true, BM, BN, WGM, WGN, true, true>(
+        w, smem, [&](int j) { return j ? 0xFFFFFFFFu : id; });
+  } else {
+    const uint32_t id = one(blockIdx.x - nw, gridDim.x - nw);
+    walk_tiles<EPI_OUT, true, BM, BN, WGM, WGN, false, true>(
+        h, smem, [&](int j) { return j ? 0xFFFFFFFFu : id; });
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+  return v;
+}
+
+// Dot product of two rows of d elements by one wave, in every lane.
+template <typename T>
+__device__ __forceinline__ float row_dot(const T* x, const T* y, int d, int lane) {
+  float s = 0.f;
+  for (int c = lane * 8; c < d; c += 512) {
+    const Raw8<T> a = load8(x + c, d - c), b = load8(y + c, d - c);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s = fmaf(a.get(u), b.get(u), s);
+  }
+  return wave_sum(s);
+}
+
+constexpr int kMaxK = 256;                 // teacher's entries a token
+constexpr int kPer = kMaxK / 64;           // of them a lane
+
+// The teacher's shares of a row by one wave: q[u] belongs to entry lane + 64 u,
+// 0 where there is none. Returns the sum of q log q; any: an entry has weight.
+__device__ __forceinline__ float teacher_shares(const int32_t* ids, const float* t, int k,
+                                                int64_t V, float inv_tau, int lane, int (&id)[kPer],
+                                                float (&q)[kPer], bool& any) {
+  float m = -INFINITY, x[kPer];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int j = lane + 64 * u;
+    id[u] = j < k ? ids[j] : -1;
+    if (id[u] < 0 || id[u] >= V) id[u] = -1;
+    x[u] = id[u] >= 0 ? t[j] * inv_tau : -INFINITY;
+    m = fmaxf(m, x[u]);
+  }
+  m = wave_max(m);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float s = 0.f;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    q[u] = id[u] >= 0 ? expf(x[u] - ref) : 0.f;
+    s += q[u];
+  }
+  s = wave_sum(s);
+  any = !(s == 0.f);
+  float e = 0.f;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    if (any) q[u] /= s;
+    if (q[u] != 0.f) e += q[u] * logf(q[u]);
+  }
+  return wave_sum(e);
+}
+
+// Joins the tiles' maxima and sums along the vocabulary and forms the losses:
+// blocks of 8 rows by 1024 threads, 128 threads a row for the join, then two
+// waves a row for the dot products that its targets name.
+struct JoinArgs {
+  const float2* part;
+  int64_t parts;
+  int64_t n;
+  int d;
+  const void* h;
+  int64_t ld;
+  const void* table;
+  int64_t V;
+  float scale, inv_tau;
+  const int32_t* ids;      // [n][k] (cross entropy: k = 1)
+  const float* teacher;    // nullable: cross entropy
+  int k;
+  float *loss, *lse, *logits;
+};
+constexpr int kJoinRows = 8;
+
+template <typename T>
+__global__ __launch_bounds__(1024) void head_join_kernel(JoinArgs g) {
+  __shared__ float2 red[16][kJoinRows];
+  __shared__ float lse_s[kJoinRows];
+  __shared__ float zs[kJoinRows][kMaxK];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t r0 = (int64_t)blockIdx.x * kJoinRows;
+  {
+    const int r = tid & (kJoinRows - 1);
+    const int64_t row = r0 + r < g.n ? r0 + r : g.n - 1;
+    float m = -INFINITY, s = 0.f;
+#pragma unroll 4
+    for (int64_t p = tid / kJoinRows; p < g.parts; p += 1024 / kJoinRows) {
+      const float2 v = g.part[p * g.n + row];
+      const float hi = fmaxf(m, v.x), ref = hi == -INFINITY ? 0.f : hi;
+      s = s * __builtin_amdgcn_exp2f(m - ref) + v.y * __builtin_amdgcn_exp2f(v.x - ref);
+      m = hi;
+    }
+#pragma unroll
+    for (int o = kJoinRows; o < 64; o <<= 1) {
+      const float om = __shfl_xor(m, o), os = __shfl_xor(s, o);
+      const float hi = fmaxf(m, om), ref = hi == -INFINITY ? 0.f : hi;
+      s = s * __builtin_amdgcn_exp2f(m - ref) + os * __builtin_amdgcn_exp2f(om - ref);
+      m = hi;
+    }
+    if (lane < kJoinRows) red[wave][lane] = make_float2(m, s);
+  }
+  __syncthreads();
+  if (tid < kJoinRows) {
+    float m = -INFINITY, s = 0.f;
+    for (int w = 0; w < 16; ++w) m = fmaxf(m, red[w][tid].x);
+    const float ref = m == -INFINITY ? 0.f : m;
+    for (int w = 0; w < 16; ++w) s += red[w][tid].y * __builtin_amdgcn_exp2f(red[w][tid].x - ref);
+    // log(s 2^m)
+    const float l = (m + log2f(s)) * kLn2;
+    lse_s[tid] = l;
+    if (r0 + tid < g.n) g.lse[r0 + tid] = l;
+  }
+  // dot products: two waves a row
+  const int r = wave >> 1;
+  const int64_t row = r0 + r;
+  const T* hr = static_cast<const T*>(g.h) + row * g.ld;
+  const T* tab = static_cast<const T*>(g.table);
+  if (row < g.n)
+    for (int j = wave & 1; j < g.k; j += 2) {
+      const int id = g.ids[row * g.k + j];
+      float z = 0.f;
+      if (id >= 0 && id < g.V) z = g.scale * row_dot(hr, tab + (int64_t)id * g.d, g.d, lane);
+      if (lane == 0) zs[r][j] = z;
+    }
+  __syncthreads();
+  if ((wave & 1) || row >= g.n) return;
+  const float l = lse_s[r];
+  if (!g.teacher) {
+    const int id = g.ids[row];
+    if (lane == 0) g.loss[row] = id >= 0 && id < g.V ? l - zs[r][0] : 0.f;
+    return;
+  }
+  int id[kPer];
+  float q[kPer];
+  bool any;
+  const float ent = teacher_shares(g.ids + row * g.k, g.teacher + row * g.k, g.k, g.V, g.inv_tau,
+                                   lane, id, q, any);
+  float x = 0.f;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int j = lane + 64 * u;
+    if (j < g.k) {
+      g.logits[row * g.k + j] = zs[r][j];
+      if (q[u] != 0.f) x += q[u] * (l - zs[r][j] * g.inv_tau);
+    }
+  }
+  x = wave_sum(x);
+  if (lane == 0) g.loss[row] = any ? (ent + x) / (g.inv_tau * g.inv_tau) : 0.f;
+}
+
+// ---------------------------------------------------------------------------
+// Operand copies
+
+__device__ __forceinline__ int wave_imax(int v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = max(v, __shfl_xor(v, o));
+  return v;
+}
+// Largest of n exponents, in every thread of a block of 256.
+__device__ __forceinline__ int block_exponent(const int* part, int n, int* sh) {
+  int e = kNone;
+  for (int i = threadIdx.x; i < n; i += 256) e = max(e, part[i]);
+  e = wave_imax(e);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = e;
+  __syncthreads();
+  e = max(max(sh[0], sh[1]), max(sh[2], sh[3]));
+  __syncthreads();
+  return e;
+}
+// 2^this brings a value of exponent e to 2^kTop.
+__device__ __forceinline__ int placement(int e) { return e == kNone ? 0 : kTop - e; }
+
+template <typename T>
+__device__ __forceinline__ int exponent_of8(const T* p, int left) {
+  const Raw8<T> v = load8(p, left);
+  float m = 0.f;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const float a = fabsf(v.get(u));
+    if (a < INFINITY) m = fmaxf(m, a);               // NaN and infinity aside
+  }
+  return exponent_of(m);
+}
+
+// src[c .. c + 8) times 2^e as fp16 halves (zeros behind d, or all zeros).
+template <typename T>
+__device__ __forceinline__ void put_halves(const T* src, int d, int c, bool keep, int e,
+                                           uint16_t* dst, int64_t plane) {
+  float x[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) x[u] = 0.f;
+  if (keep && c < d) {
+    const Raw8<T> v = load8(src + c, d - c);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) x[u] = ldexpf(v.get(u), e);
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) w[u] = pack2_f16(x[2 * u], x[2 * u + 1]);
+  *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) w[u] = pack2_f16(x[2 * u] - lo_f16(w[u]), x[2 * u + 1] - hi_f16(w[u]));
+    *reinterpret_cast<uint4*>(dst + plane + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+__device__ __forceinline__ void put_raw(const uint16_t* src, int d, int c, bool keep, uint16_t* dst) {
+  Raw8<uint16_t> v{};
+  if (keep && c < d) v = load8(src + c, d - c);
+  *reinterpret_cast<uint4*>(dst + c) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+}
+
+constexpr int kScanBlocks = 512;
+constexpr int kRowBlocks = 512;           // most blocks over rows, four waves each
+
+// What all row kernels know of a call's rows (row pieces: of the piece).
+struct RowArgs {
+  const void* h;
+  int64_t ld;
+  int64_t n, rows_pad, vec_pad;
+  int d, dp;
+  const void* table;
+  int64_t V;
+  float scale, inv_tau;
+  const int32_t* ids;
+  const float *teacher, *logits;    // distillation
+  int k;
+  const float *lse, *dloss, *dlse;
+  float *a, *lse2, *rowf;
+  int* row_exp;                     // dz's rows hold 2^-row_exp times their values; kNone: zeros
+  int32_t* sidx;
+  float* sval;
+  int *part_h, *part_w;             // exponents by block: of 2^row_exp h, of T
+  int *all_h, *all_w;               // what dT and dh undo: minus their placements
+  int nparts_h, nparts_w;
+  uint16_t *hp, *hz;                // fp16 h for dT; h for the logits (NULL: read in place)
+  float c2;
+};
+
+// First kernel of the backward pass. The first `row_blocks` blocks, a wave a
+// row: the weight a of the row's softmax (with scale), its lse in base 2, the
+// gradient at its sparse positions, and the placement of its dz. The others:
+// the exponent of T's largest element.
+template <typename T>
+__global__ __launch_bounds__(256) void head_stats_kernel(RowArgs g, int row_blocks) {
+  __shared__ int sh[4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int top = kNone;
+  if ((int)blockIdx.x >= row_blocks) {
+    const int64_t count = g.V * g.d, step = (int64_t)(gridDim.x - row_blocks) * 2048;
+    const T* t = static_cast<const T*>(g.table);
+#pragma unroll 4
+    for (int64_t i = ((int64_t)blockIdx.x - row_blocks) * 2048 + threadIdx.x * 8; i < count; i += step)
+      top = max(top, exponent_of8(t + i, (int)(count - i < 8 ? count - i : 8)));
+  } else {
+    for (int64_t row = (int64_t)blockIdx.x * 4 + wave; row < g.vec_pad; row += row_blocks * 4) {
+      const T* hr = static_cast<const T*>(g.h) + row * g.ld;
+      float a = 0.f, l2 = 0.f, w = 0.f;
+      int e = kNone, re = kNone;
+      if (row < g.n) {
+        const float l = g.lse[row], dl = g.dloss[row];
+        l2 = l * kLog2e;
+        float z = 0.f;
+        int id[kPer];
+        float q[kPer];
+        bool valid;
+        if (!g.teacher) {
+          id[0] = g.ids[row];
+          valid = id[0] >= 0 && id[0] < g.V;
+          w = valid ? g.scale * dl : 0.f;
+          a = w + (g.dlse ? g.scale * g.dlse[row] : 0.f);
+        } else {
+          teacher_shares(g.ids + row * g.k, g.teacher + row * g.k, g.k, g.V, g.inv_tau, lane, id,
+                         q, valid);
+          a = w = valid ? dl * g.scale / g.inv_tau : 0.f;
+        }
+        // a NaN weight stays one
+        const bool keep = !(a == 0.f && w == 0.f);
+        if (keep) {
+          const float bound = fabsf(a) + fabsf(w);
+          re = exponent_of(bound) - kTop;
+          if (exponent_of(bound) == kNone) re = 0;
+          for (int c = lane * 8; c < g.d; c += 512) e = max(e, exponent_of8(hr + c, g.d - c));
+          e = wave_imax(e);
+          if (e != kNone) top = max(top, e + re);
+        }
+        const int place = keep ? -re : 0;
+        if (!g.teacher) {
+          float val = 0.f;
+          if (valid && keep) {
+            z = g.scale * row_dot(hr, static_cast<const T*>(g.table) + (int64_t)id[0] * g.d, g.d, lane);
+            val = ldexpf(a, place) * __builtin_amdgcn_exp2f((z - l) * kLog2e);
+            val = (a == 0.f ? 0.f : val) - ldexpf(w, place);
+          }
+          if (lane == 0) {
+            g.sidx[row] = valid && keep ? id[0] : -1;
+            g.sval[row] = val;
+          }
+        } else {
+          // an id named more than once: its first entry carries the sum
+          float sum[kPer];
+          bool first[kPer];
+#pragma unroll
+          for (int u = 0; u < kPer; ++u) {
+            sum[u] = 0.f;
+            first[u] = id[u] >= 0;
+          }
+          for (int j = 0; j < g.k; ++j) {
+            int oid = 0;
+            float oq = 0.f;
+#pragma unroll
+            for (int u = 0; u < kPer; ++u)
+              if ((j >> 6) == u) {
+                oid = __shfl(id[u], j & 63);
+                oq = __shfl(q[u], j & 63);
+              }
+#pragma unroll
+            for (int u = 0; u < kPer; ++u)
+              if (oid >= 0 && id[u] == oid) {
+                sum[u] += oq;
+                if (j < lane + 64 * u) first[u] = false;
+              }
+          }
+#pragma unroll
+          for (int u = 0; u < kPer; ++u) {
+            const int j = lane + 64 * u;
+            if (j < g.k) {
+              const bool put = first[u] && keep;
+              const float p = __builtin_amdgcn_exp2f(
+                  (g.logits[row * g.k + j] * g.inv_tau - l) * kLog2e);
+              g.sidx[row * g.k + j] = put ? id[u] : -1;
+              g.sval[row * g.k + j] = put ? ldexpf(w, place) * (p - sum[u]) : 0.f;
+            }
+          }
+        }
+        a = ldexpf(a, place);
+      }
+      if (lane == 0) {
+        g.a[row] = a;
+        g.lse2[row] = l2;
+        g.row_exp[row] = re;
+      }
+    }
+  }
+  top = wave_imax(top);
+  if (lane == 0) sh[wave] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    top = max(max(sh[0], sh[1]), max(sh[2], sh[3]));
+    if ((int)blockIdx.x < row_blocks) g.part_h[blockIdx.x] = top;
+    else g.part_w[blockIdx.x - row_blocks] = top;
+  }
+}
+
+// Exponent of the largest element, for the forward pass of fp32 operands.
+template <typename T>
+__global__ __launch_bounds__(256) void head_scan_kernel(const T* t, int64_t count, int* part) {
+  __shared__ int sh[4];
+  int top = kNone;
+#pragma unroll 4
+  for (int64_t i = (int64_t)blockIdx.x * 2048 + threadIdx.x * 8; i < count; i += (int64_t)gridDim.x * 2048)
+    top = max(top, exponent_of8(t + i, (int)(count - i < 8 ? count - i : 8)));
+  top = wave_imax(top);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) part[blockIdx.x] = max(max(sh[0], sh[1]), max(sh[2], sh[3]));
+}
+
+// Copies of the operands. The first `row_blocks` blocks, a wave a row of h: for
+// the logits (hz: fp16 halves placed by the row's own largest element, or bf16
+// as it is) and for dT (hp). The others: rows of a piece of T, as fp16 (wp) and,
+// where the logits cannot read it in place, as bf16 (wz). Zeros behind d and
+// behind the rows.
+struct PieceArgs {
+  const void* src;
+  int64_t rows, rows_pad;
+  uint16_t *wp, *wz;
+};
+
+template <typename T>
+__global__ __launch_bounds__(256) void head_copy_kernel(RowArgs g, PieceArgs w, int row_blocks) {
+  __shared__ int sh[4];
+  constexpr bool F32 = sizeof(T) == 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool scaled = g.nparts_w > 0;
+  const int pw = scaled ? placement(block_exponent(g.part_w, g.nparts_w, sh)) : 0;
+  if ((int)blockIdx.x >= row_blocks) {
+    const int per = g.dp / 8;
+    const int64_t total = w.rows_pad * per, step = (int64_t)(gridDim.x - row_blocks) * 256;
+    for (int64_t i = ((int64_t)blockIdx.x - row_blocks) * 256 + threadIdx.x; i < total; i += step) {
+      const int64_t r = i / per;
+      const int c = (int)(i - r * per) * 8;
+      const bool in = r < w.rows;
+      const T* src = static_cast<const T*>(w.src) + (in ? r : 0) * g.d;
+      if (w.wp) put_halves(src, g.d, c, in, pw, w.wp + r * g.dp, w.rows_pad * g.dp);
+      if constexpr (!F32)
+        if (w.wz) put_raw(src, g.d, c, in, w.wz + r * g.dp);
+    }
+    return;
+  }
+  int ph = 0;
+  if (g.hp) ph = placement(block_exponent(g.part_h, g.nparts_h, sh));
+  if (blockIdx.x == 0 && threadIdx.x == 0 && g.hp) {
+    *g.all_h = -ph;
+    *g.all_w = -pw;
+  }
+  for (int64_t row = (int64_t)blockIdx.x * 4 + wave; row < g.vec_pad; row += row_blocks * 4) {
+    const bool in = row < g.n;
+    const T* src = static_cast<const T*>(g.h) + (in ? row : 0) * g.ld;
+    if constexpr (F32) {
+      // the logits' copy, and the factor that undoes its placement
+      int e = kNone;
+      if (in) {
+        for (int c = lane * 8; c < g.d; c += 512) e = max(e, exponent_of8(src + c, g.d - c));
+        e = wave_imax(e);
+      }
+      const int p = placement(e);
+      if (lane == 0) g.rowf[row] = ldexpf(g.c2, min(-p - pw, 100));
+      if (row < g.rows_pad)
+        for (int c = lane * 8; c < g.dp; c += 512)
+          put_halves(src, g.d, c, in, p, g.hz + row * g.dp, g.rows_pad * g.dp);
+    } else {
+      if (g.hz && row < g.rows_pad)
+        for (int c = lane * 8; c < g.dp; c += 512) put_raw(src, g.d, c, in, g.hz + row * g.dp);
+    }
+    if (g.hp && row < g.rows_pad) {
+      const int re = in ? g.row_exp[row] : kNone;
+      const bool keep = re != kNone;                 // rows without weight add zeros
+      for (int c = lane * 8; c < g.dp; c += 512)
+        put_halves(src, g.d, c, keep, keep ? ph + re : 0, g.hp + row * g.dp, g.rows_pad * g.dp);
+    }
+  }
+}
+
+// Writes the sparse positions of a piece over its dz.
+__global__ __launch_bounds__(256) void head_sparse_kernel(const int32_t* sidx, const float* sval,
+                                                          int64_t n, int k, int64_t v0, int64_t cols,
+                                                          uint16_t* dz, int64_t ldz,
+                                                          int64_t plane, int planes) {
+  const int64_t total = n * k;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t v = (int64_t)sidx[i] - v0;
+    if (v < 0 || v >= cols) continue;
+    const float x = sval[i];
+    uint16_t* p = dz + i / k * ldz + v;
+    const uint32_t w = pack2_f16(x, 0.f);
+    *p = (uint16_t)w;
+    if (planes > 1) p[plane] = (uint16_t)pack2_f16(x - lo_f16(w), 0.f);
+  }
+}
+
+// Sums the results of K's splits in order, adds prev, and stores: two products.
+struct SumArgs {
+  const float* part;
+  int splits;
+  int64_t stride, ld_part;             // elements
+  int64_t M, N;
+  const float* prev;
+  int64_t ld_prev;
+  void* out;
+  int64_t ld_out;
+  int out_bf16;
+};
+__global__ __launch_bounds__(256) void head_sum_kernel(SumArgs a, SumArgs b, int na) {
+  const bool first = (int)blockIdx.x < na;
+  const SumArgs& g = first ? a : b;
+  const int64_t per = (g.N + 3) / 4, total = g.M * per;
+  const int64_t step = (int64_t)(first ? na : (int)gridDim.x - na) * 256;
+  for (int64_t i = ((int64_t)blockIdx.x - (first ? 0 : na)) * 256 + threadIdx.x; i < total; i += step) {
+    const int64_t row = i / per, col = (i - row * per) * 4;
+    const float* p = g.part + row * g.ld_part + col;     // rows of whole tiles
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int s = 0; s < g.splits; ++s) {
+      const float4 x = *reinterpret_cast<const float4*>(p + s * g.stride);
+      v[0] += x.x;
+      v[1] += x.y;
+      v[2] += x.z;
+      v[3] += x.w;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (col + u < g.N) {
+        if (g.prev) v[u] += g.prev[row * g.ld_prev + col + u];
+        if (g.out_bf16)
+          static_cast<uint16_t*>(g.out)[row * g.ld_out + col + u] = (uint16_t)pack2_bf16(v[u], 0.f);
+        else
+          static_cast<float*>(g.out)[row * g.ld_out + col + u] = v[u];
+      }
+  }
+}
+
+__global__ __launch_bounds__(256) void head_zero_kernel(uint16_t* out, int64_t count) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256)
+    out[i] = 0;
+}
+
+int64_t pad(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+int64_t tiles_of(int64_t x, int b) { return (x + b - 1) / b; }
+int blocks_for(int64_t items, int most) {
+  const int64_t b = (items + 255) / 256;
+  return (int)(b < 1 ? 1 : b > most ? most : b);
+}
+int elt_size(int32_t dtype) { return dtype == PG_F32 ? 4 : 2; }
+
+// An operand that the logits' tiles can read where it lies: bf16 rows of whole
+// slots at 16-byte alignment.
+bool in_place(int32_t dtype, int d, int64_t ld, const void* p) {
+  return dtype == PG_BF16 && d % 64 == 0 && d >= 128 && ld % 8 == 0 && ld < (1 << 24) &&
+         (uintptr_t)p % 16 == 0;
+}
+
+bool big_tiles(int64_t M, int64_t N) {
+  return tiles_of(M, 256) * tiles_of(N, 256) >= kCUs / 2 && M > 128;
+}
+
+template <int EPI>
+hipError_t launch_tiles(TileArgs& g, int64_t M, int64_t N, bool f16, hipStream_t s) {
+  const bool big = big_tiles(M, N);
+  const int b = big ? 256 : 128;
+  g.splits = 1;
+  g.nbm = (int)tiles_of(M, b);
+  g.nbn = (int)tiles_of(N, b);
+  const int64_t total = (int64_t)g.nbm * g.nbn;
+  const int64_t most = big ? kCUs : 2 * kCUs;
+  const unsigned grid = (unsigned)(total < most ? total : most);
+  if (big && f16)
+    hipLaunchKernelGGL((head_tile_kernel<EPI, true, 256, 256, 2, 4>), dim3(grid), dim3(512), 0, s, g);
+  else if (big)
+    hipLaunchKernelGGL((head_tile_kernel<EPI, false, 256, 256, 2, 4>), dim3(grid), dim3(512), 0, s, g);
+  else if (f16)
+    hipLaunchKernelGGL((head_tile_kernel<EPI, true, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, s, g);
+  else
+    hipLaunchKernelGGL((head_tile_kernel<EPI, false, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, s, g);
+  return hipGetLastError();
+}
+
+void launch_copy(bool f32, const RowArgs& r, const PieceArgs& w, bool rows, hipStream_t s) {
+  const int rb = rows ? (int)(tiles_of(r.vec_pad, 4) < kRowBlocks ? tiles_of(r.vec_pad, 4) : kRowBlocks) : 0;
+  const int wb = w.rows ? blocks_for(w.rows_pad * r.dp / 8, 2048) : 0;
+  if (rb + wb == 0) return;
+  if (f32)
+    hipLaunchKernelGGL((head_copy_kernel<float>), dim3(rb + wb), dim3(256), 0, s, r, w, rb);
+  else
+    hipLaunchKernelGGL((head_copy_kernel<uint16_t>), dim3(rb + wb), dim3(256), 0, s, r, w, rb);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// Workspace geometry
+
+constexpr int kSplitBlocks = 512;         // most tiles of products whose K is split
+
+HeadPlan head_plan(int64_t n, int d, int64_t V, int32_t dtype, int k, bool backward) {
+  HeadPlan p{};
+  p.planes = dtype == PG_F32 ? 2 : 1;
+  p.dp = (int)pad(d < 128 ? 128 : d, 64);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t o = at;
+    at += pad(bytes, 256);
+    return o;
+  };
+  const int64_t row = (int64_t)p.dp * 2 * p.planes;
+  p.off_parts = take((kScanBlocks + kRowBlocks + 2) * 4);
+  if (!backward) {
+    p.rows = n;
+    // rows of the table are copied a piece at a time, about 256 MB of them
+    p.cols = pad(V, 256);
+    const int64_t most = ((int64_t)1 << 28) / row / 256 * 256;
+    if (p.cols > most) p.cols = most > 256 ? most : 256;
+    p.off_rowf = take(pad(n, 256) * 4);
+    p.off_hz = take(n * row);
+    p.off_wz = take(p.cols * row);
+    p.off_part = take((V + 127) / 128 * n * 8);
+  } else {
+    // dz of a piece: at most 2^29 elements (1 GiB) of both halves
+    p.rows = pad(n, 128);
+    if (p.rows > 32768) p.rows = 32768;
+    const int64_t elems = ((int64_t)1 << 29) / p.planes;
+    int64_t c = elems / p.rows / 256 * 256;
+    if (c > pad(V, 256)) c = pad(V, 256);
+    const int64_t pieces = (V + c - 1) / c;
+    p.cols = pad((V + pieces - 1) / pieces, 256);
+    const int64_t vec = pad(p.rows, 256);
+    p.off_a = take(vec * 4);
+    p.off_lse = take(vec * 4);
+    p.off_rowf = take(vec * 4);
+    p.off_exp = take(vec * 4);
+    p.off_sidx = take(p.rows * k * 4);
+    p.off_sval = take(p.rows * k * 4);
+    p.off_h = take(p.rows * row);
+    p.off_hz = take(p.rows * row);
+    p.off_w = take(p.cols * row);
+    p.off_wz = p.planes == 1 && !(d % 64 == 0 && d >= 128) ? take(p.cols * row) : at;
+    p.off_dz = take(p.rows * p.cols * 2 * p.planes);
+    p.off_dh = take(p.rows * d * 4);
+    p.off_dw = n > 32768 ? take(V * d * 4) : at;
+    p.off_split = take((int64_t)kSplitBlocks * 128 * 128 * 4);
+  }
+  p.bytes = at;
+  return p;
+}
+
+hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* workspace,
+                               hipStream_t s) {
+  auto* ws = static_cast<uint8_t*>(workspace);
+  const int es = elt_size(g.dtype);
+  const bool f32 = g.dtype == PG_F32;
+  const int64_t dp2 = (int64_t)p.dp * 2;
+  auto* parts_w = reinterpret_cast<int*>(ws + p.off_parts);
+  TileArgs t{};
+  t.nseg = f32 ? kSegs : 1;
+  t.c2 = (float)((double)g.scale * (double)g.inv_tau * 1.4426950408889634);
+  t.M = g.n;
+  t.rowf = reinterpret_cast<const float*>(ws + p.off_rowf);
+  t.slots = p.dp / 32;
+  RowArgs r{};
+  r.h = g.h;
+  r.ld = g.ld_h;
+  r.n = r.rows_pad = g.n;
+  r.vec_pad = pad(g.n, 256);
+  r.d = g.d;
+  r.dp = p.dp;
+  r.rowf = reinterpret_cast<float*>(ws + p.off_rowf);
+  r.part_w = parts_w;
+  r.c2 = t.c2;
+  if (f32) {
+    r.nparts_w = blocks_for((g.V * g.d + 7) / 8, kScanBlocks);
+    hipLaunchKernelGGL((head_scan_kernel<float>), dim3(r.nparts_w), dim3(256), 0, s,
+                       static_cast<const float*>(g.table), g.V * g.d, parts_w);
+  }
+  const bool h_here = in_place(g.dtype, g.d, g.ld_h, g.h);
+  if (h_here) {
+    t.A = Side{static_cast<const uint8_t*>(g.h), g.ld_h * 2, 0, g.n};
+  } else {
+    r.hz = reinterpret_cast<uint16_t*>(ws + p.off_hz);
+    t.A = Side{ws + p.off_hz, dp2, g.n * dp2, g.n};
+  }
+  const bool w_here = in_place(g.dtype, g.d, g.d, g.table);
+  const int64_t piece = w_here ? g.V : p.cols;
+  int64_t parts = 0;
+  for (int64_t v0 = 0; v0 < g.V; v0 += piece) {
+    const int64_t c = g.V - v0 < piece ? g.V - v0 : piece;
+    PieceArgs w{};
+    w.src = static_cast<const uint8_t*>(g.table) + v0 * g.d * es;
+    if (w_here) {
+      t.B = Side{static_cast<const uint8_t*>(w.src), (int64_t)g.d * 2, 0, c};
+    } else {
+      w.rows = w.rows_pad = c;
+      (f32 ? w.wp : w.wz) = reinterpret_cast<uint16_t*>(ws + p.off_wz);
+      t.B = Side{ws + p.off_wz, dp2, c * dp2, c};
+    }
+    launch_copy(f32, r, w, v0 == 0 && !h_here, s);
+    t.V = c;
+    t.part = reinterpret_cast<float2*>(ws + p.off_part) + parts * g.n;
+    const hipError_t e = launch_tiles<EPI_LSE>(t, g.n, c, f32, s);
+    if (e != hipSuccess) return e;
+    parts += t.nbn;
+  }
+  JoinArgs j{};
+  j.part = reinterpret_cast<const float2*>(ws + p.off_part);
+  j.parts = parts;
+  j.n = g.n;
+  j.d = g.d;
+  j.h = g.h;
+  j.ld = g.ld_h;
+  j.table = g.table;
+  j.V = g.V;
+  j.scale = g.scale;
+  j.inv_tau = g.inv_tau;
+  j.ids = g.ids;
+  j.teacher = g.teacher;
+  j.k = g.k;
+  j.loss = g.loss;
+  j.lse = g.lse;
+  j.logits = g.logits;
+  const unsigned grid = (unsigned)((g.n + kJoinRows - 1) / kJoinRows);
+  if (f32)
+    hipLaunchKernelGGL((head_join_kernel<float>), dim3(grid), dim3(1024), 0, s, j);
+  else
+    hipLaunchKernelGGL((head_join_kernel<uint16_t>), dim3(grid), dim3(1024), 0, s, j);
+  return hipGetLastError();
+}
+
+// The products of a piece: both in one launch; where their tiles are few, K is
+// split and a second launch joins the splits.
+static hipError_t launch_grads(TileArgs tw, TileArgs th, float* split, hipStream_t s) {
+  const bool w = tw.out != nullptr, h = th.out != nullptr;
+  const int64_t big_n = (w ? tiles_of(tw.M, 256) * tiles_of(tw.V, 256) : 0) +
+                        (h ? tiles_of(th.M, 256) * tiles_of(th.V, 256) : 0);
+  const bool big = big_n >= kCUs / 2;
+  const int b = big ? 256 : 128;
+  auto tiles = [&](TileArgs& t) {
+    t.nbm = (int)tiles_of(t.M, b);
+    t.nbn = (int)tiles_of(t.V, b);
+    t.splits = 1;
+    return (int64_t)t.nbm * t.nbn;
+  };
+  const int64_t nw = w ? tiles(tw) : 0, nh = h ? tiles(th) : 0;
+  // 128 x 128 tiles run two to a compute unit: K is shared until they fill the
+  // chip, down to 8 slots a tile
+  SumArgs sums[2] = {};
+  int64_t used = 0;
+  auto share = [&](TileArgs& t, int64_t n, int64_t budget, SumArgs& sa) {
+    if (n == 0) return;
+    int64_t k = budget / n;
+    const int64_t most = (int64_t)t.slots * t.nseg / 8;
+    if (k > most) k = most;
+    if (k > t.slots / 2) k = t.slots / 2;
+    if (k < 2) return;
+    sa = SumArgs{split + used, (int)k, 0, (int64_t)t.nbn * 128, t.M, t.V, t.prev, t.ld_prev,
+                 t.out, t.ld_out, t.out_bf16};
+    sa.stride = (int64_t)t.nbm * 128 * sa.ld_part;
+    t.splits = (int)k;
+    t.out = split + used;
+    t.ld_out = sa.ld_part;
+    t.split_out = sa.stride;
+    t.out_bf16 = 0;
+    t.prev = nullptr;
+    used += k * sa.stride;
+  };
+  if (!big && nw + nh < kSplitBlocks) {
+    // in proportion to the work, so that both end together
+    const double ww = (double)nw * tw.slots, wh = (double)nh * th.slots;
+    const int64_t bw = (int64_t)(kSplitBlocks * ww / (ww + wh));
+    share(tw, nw, bw, sums[0]);
+    share(th, nh, kSplitBlocks - bw, sums[1]);
+  }
+  const uint32_t gw = (uint32_t)(nw * tw.splits), gh = (uint32_t)(nh * th.splits);
+  if (big)
+    hipLaunchKernelGGL((head_grad_kernel<256, 256, 2, 4>), dim3(gw + gh), dim3(512), 0, s, tw, th, gw);
+  else
+    hipLaunchKernelGGL((head_grad_kernel<128, 128, 2, 2>), dim3(gw + gh), dim3(256), 0, s, tw, th, gw);
+  const int sw = sums[0].splits ? blocks_for(sums[0].M * ((sums[0].N + 3) / 4), 1024) : 0;
+  const int sh = sums[1].splits ? blocks_for(sums[1].M * ((sums[1].N + 3) / 4), 1024) : 0;
+  if (sw + sh)
+    hipLaunchKernelGGL(head_sum_kernel, dim3(sw + sh), dim3(256), 0, s, sums[0], sums[1], sw);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* workspace,
+                                hipStream_t s) {
+  auto* ws = static_cast<uint8_t*>(workspace);
+  const int es = elt_size(g.dtype);
+  const int64_t dp2 = (int64_t)p.dp * 2;
+  const bool f32 = g.dtype == PG_F32;
+  const int nseg = f32 ? kSegs : 1;
+  auto* dz = reinterpret_cast<uint16_t*>(ws + p.off_dz);
+  if (g.n == 0) {
+    const int64_t count = g.V * g.d * elt_size(g.dw_dtype) / 2;
+    if (g.dw && !g.accumulate)
+      hipLaunchKernelGGL(head_zero_kernel, dim3(blocks_for(count, 8192)), dim3(256), 0, s,
+                         static_cast<uint16_t*>(g.dw), count);
+    return hipGetLastError();
+  }
+  const bool w_here = in_place(g.dtype, g.d, g.d, g.table);
+  for (int64_t r0 = 0; r0 < g.n; r0 += p.rows) {
+    const int64_t n = g.n - r0 < p.rows ? g.n - r0 : p.rows;
+    const int64_t rows = pad(n, 128);
+    const bool first_rows = r0 == 0, last_rows = r0 + n == g.n;
+    RowArgs r{};
+    r.h = static_cast<const uint8_t*>(g.h) + r0 * g.ld_h * es;
+    r.ld = g.ld_h;
+    r.n = n;
+    r.rows_pad = rows;
+    r.vec_pad = pad(n, 256);
+    r.d = g.d;
+    r.dp = p.dp;
+    r.table = g.table;
+    r.V = g.V;
+    r.scale = g.scale;
+    r.inv_tau = g.inv_tau;
+    r.ids = g.ids + r0 * g.k;
+    r.teacher = g.teacher ? g.teacher + r0 * g.k : nullptr;
+    r.logits = g.logits ? g.logits + r0 * g.k : nullptr;
+    r.k = g.k;
+    r.lse = g.lse + r0;
+    r.dloss = g.dloss + r0;
+    r.dlse = g.dlse ? g.dlse + r0 : nullptr;
+    r.a = reinterpret_cast<float*>(ws + p.off_a);
+    r.lse2 = reinterpret_cast<float*>(ws + p.off_lse);
+    r.rowf = reinterpret_cast<float*>(ws + p.off_rowf);
+    r.row_exp = reinterpret_cast<int*>(ws + p.off_exp);
+    r.sidx = reinterpret_cast<int32_t*>(ws + p.off_sidx);
+    r.sval = reinterpret_cast<float*>(ws + p.off_sval);
+    r.part_w = reinterpret_cast<int*>(ws + p.off_parts);
+    r.part_h = r.part_w + kScanBlocks;
+    r.all_h = r.part_h + kRowBlocks;
+    r.all_w = r.all_h + 1;
+    r.nparts_w = blocks_for((g.V * g.d + 7) / 8, kScanBlocks);
+    r.nparts_h = (int)(tiles_of(r.vec_pad, 4) < kRowBlocks ? tiles_of(r.vec_pad, 4) : kRowBlocks);
+    r.hp = reinterpret_cast<uint16_t*>(ws + p.off_h);
+    const bool h_here = in_place(g.dtype, g.d, g.ld_h, r.h);
+    r.hz = h_here ? nullptr : reinterpret_cast<uint16_t*>(ws + p.off_hz);
+    r.c2 = (float)((double)g.scale * (double)g.inv_tau * 1.4426950408889634);
+    // T's exponent is the same for every piece of the rows
+    const unsigned grid = r.nparts_h + (first_rows ? r.nparts_w : 0);
+    if (f32)
+      hipLaunchKernelGGL((head_stats_kernel<float>), dim3(grid), dim3(256), 0, s, r, r.nparts_h);
+    else
+      hipLaunchKernelGGL((head_stats_kernel<uint16_t>), dim3(grid), dim3(256), 0, s, r, r.nparts_h);
+
+    for (int64_t v0 = 0; v0 < g.V; v0 += p.cols) {
+      const int64_t c = g.V - v0 < p.cols ? g.V - v0 : p.cols;
+      const int64_t cols = pad(c, 128);
+      const bool first = v0 == 0, last = v0 + c == g.V;
+      PieceArgs w{};
+      w.src = static_cast<const uint8_t*>(g.table) + v0 * g.d * es;
+      w.rows = c;
+      w.rows_pad = cols;
+      w.wp = reinterpret_cast<uint16_t*>(ws + p.off_w);
+      if (!f32 && !w_here) w.wz = reinterpret_cast<uint16_t*>(ws + p.off_wz);
+      launch_copy(f32, r, w, first, s);
+      const int64_t ldz = cols, plane = rows * cols;
+
+      TileArgs t{};
+      t.A = h_here ? Side{static_cast<const uint8_t*>(r.h), g.ld_h * 2, 0, n}
+                   : Side{ws + p.off_hz, dp2, rows * dp2, n};
+      t.B = f32 ? Side{ws + p.off_w, dp2, cols * dp2, c}
+                : w_here ? Side{static_cast<const uint8_t*>(w.src), (int64_t)g.d * 2, 0, c}
+                         : Side{ws + p.off_wz, dp2, 0, c};
+      t.nseg = nseg;
+      t.slots = p.dp / 32;
+      t.c2 = r.c2;
+      t.M = n;
+      t.V = c;
+      t.rowf = r.rowf;
+      t.a = r.a;
+      t.lse2 = r.lse2;
+      t.dz = dz;
+      t.ldz = ldz;
+      t.dz_plane = plane;
+      t.Mpad = rows;
+      t.Vpad = cols;
+      hipError_t e = launch_tiles<EPI_DZ>(t, rows, cols, f32, s);
+      if (e != hipSuccess) return e;
+      hipLaunchKernelGGL(head_sparse_kernel, dim3(blocks_for(n * g.k, 8192)), dim3(256), 0, s,
+                         r.sidx, r.sval, n, g.k, v0, c, dz, ldz, plane, p.planes);
+
+      // dT of the piece: [c x d], K over the rows
+      TileArgs tw{}, th{};
+      tw.A = Side{ws + p.off_dz, ldz * 2, plane * 2, cols};
+      tw.B = Side{ws + p.off_h, dp2, rows * dp2, p.dp};
+      tw.nseg = nseg;
+      tw.slots = (int)(rows / 32);
+      tw.M = c;
+      tw.V = g.d;
+      tw.all_exp = r.all_h;
+      if (g.dw) {
+        auto* acc = reinterpret_cast<float*>(ws + p.off_dw) + v0 * g.d;
+        auto* dw32 = static_cast<float*>(g.dw) + v0 * g.d;
+        const bool to16 = g.dw_dtype == PG_BF16;
+        tw.ld_out = tw.ld_prev = g.d;
+        if (to16) {
+          tw.out = last_rows ? static_cast<void*>(static_cast<uint16_t*>(g.dw) + v0 * g.d) : acc;
+          tw.out_bf16 = last_rows;
+          tw.prev = first_rows ? nullptr : acc;
+        } else {
+          tw.out = dw32;
+          tw.prev = first_rows && !g.accumulate ? nullptr : dw32;
+        }
+      }
+      // dh: [n x d], K over the piece's columns
+      th.A = Side{ws + p.off_dz, ldz * 2, plane * 2, rows};
+      th.B = Side{ws + p.off_w, dp2, cols * dp2, p.dp};
+      th.nseg = nseg;
+      th.slots = (int)(cols / 32);
+      th.M = n;
+      th.V = g.d;
+      th.row_exp = r.row_exp;
+      th.all_exp = r.all_w;
+      if (g.dh) {
+        auto* acc = reinterpret_cast<float*>(ws + p.off_dh);
+        auto* out = static_cast<uint8_t*>(g.dh) + r0 * g.ld_dh * es;
+        if (f32) {
+          th.out = out;
+          th.ld_out = th.ld_prev = g.ld_dh;
+          th.prev = first ? nullptr : reinterpret_cast<const float*>(out);
+        } else {
+          th.out = last ? static_cast<void*>(out) : acc;
+          th.ld_out = last ? g.ld_dh : g.d;
+          th.out_bf16 = last;
+          th.prev = first ? nullptr : acc;
+          th.ld_prev = g.d;
+        }
+      }
+      e = launch_grads(tw, th, reinterpret_cast<float*>(ws + p.off_split), s);
+      if (e != hipSuccess) return e;
+    }
+  }
+  return hipGetLastError();
+}
+
+}  // namespace pg

@@ -1,6 +1,6 @@
 // Declarations and small device helpers shared by the training-step operators:
-// token embedding (embed.hip), layer norm (norm.hip) and the orthogonalised
-// update (orthogonalize.hip). gfx950 only.
+// token embedding (embed.hip), layer norm (norm.hip), the orthogonalised
+// update (orthogonalize.hip) and the head's losses (head.hip). gfx950 only.
 #pragma once
 
 #include "common.h"
@@ -177,5 +177,45 @@ struct OrthoArgs {
 hipError_t launch_orthogonalize(const OrthoPlan& p, const void* G, int32_t dtype, int64_t n_mat,
                                 int rows, int cols, const OrthoArgs& oa, uint16_t* out,
                                 void* workspace, hipStream_t s);
+
+// Losses of the head: workspace geometry of n rows of d elements against V table
+// rows with k targets each; backward: its pieces of at most rows x cols.
+constexpr int kHeadMaxD = 16384;
+constexpr int kHeadMaxK = 256;
+struct HeadPlan {
+  int planes;                 // halves of an fp32 operand
+  int dp;                     // padded width
+  int64_t rows, cols;
+  int64_t off_parts, off_rowf, off_hz, off_wz, off_part;
+  int64_t off_a, off_lse, off_exp, off_sidx, off_sval, off_h, off_w, off_dz, off_dh,
+      off_dw, off_split;
+  int64_t bytes;
+};
+HeadPlan head_plan(int64_t n, int d, int64_t V, int32_t dtype, int k, bool backward);
+struct HeadArgs {
+  const void* h;
+  int32_t dtype;
+  int64_t n;
+  int d;
+  int64_t ld_h;
+  const void* table;
+  int64_t V;
+  float scale, inv_tau;
+  const int32_t* ids;         // [n][k]; cross entropy: the targets, k = 1
+  const float* teacher;       // [n][k]; NULL: cross entropy
+  int k;
+  float *loss, *lse;          // forward; backward reads lse
+  float* logits;              // distillation: z at the ids
+  const float *dloss, *dlse;
+  void* dh;
+  int64_t ld_dh;
+  void* dw;
+  int32_t dw_dtype;
+  int accumulate;
+};
+hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* workspace,
+                               hipStream_t s);
+hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* workspace,
+                                hipStream_t s);
 
 }  // namespace pg

@@ -737,6 +737,104 @@ PG_API int pg_orthogonalize(const void* G, int32_t dtype, int64_t n_mat,
                             hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Losses of the language model's head over the token table T that pg_embed
+ * reads (tied), with their gradients: what dL/d(residual stream) starts from.
+ * The conventions of the training step above hold. With
+ *   z_nv = scale * (h_n . T_v),  n < n_tok, v < V = table->n_rows,
+ * the [n_tok][V] logits are never kept: the forward calls form them tile by
+ * tile on the matrix cores with a running maximum and sum, the backward calls
+ * once more, piece by piece of the vocabulary, with
+ *   dh_n = scale sum_v dz_nv T_v,   dT_v = scale sum_n dz_nv h_n.
+ *   h       [n] rows of d elements of dtype, stride ld_h; 1 <= d <= 16384
+ *           (PG_EUNSUPPORTED beyond), n < 2^26 (PG_ERANGE)
+ *   table   PG_F32 or PG_BF16 data [V][d] of the same type as h (NF4 or
+ *           another type: PG_EUNSUPPORTED); 1 <= V < 2^31 - 1, and tiles of
+ *           128 x 128 fewer than 2^31 (PG_ERANGE)
+ *   scale   finite
+ * Logits, statistics and losses are fp32. fp32 operands are multiplied as
+ * three bf16 planes (24 bits), sums in fp32. For bf16 operands dz is rounded
+ * to bf16 once, scaled, before its two products, whose sums are fp32: dh and
+ * dT differ from exact ones by about one more rounding of bf16 (2^-9 of their
+ * size in the 2-norm), an fp32 dT of bf16 operands by that too.
+ * A row whose logits are not all below +infinity, or NaN, has lse NaN.
+ * A workspace sized for the largest batch serves every smaller one of the
+ * same d, V, k and dtype (256-byte aligned).
+ * ------------------------------------------------------------------------ */
+
+/* Device workspace bytes (negative pg_status for sizes that the calls refuse). */
+PG_API int64_t pg_head_loss_workspace_size(int64_t n, int32_t d, int64_t V, int32_t dtype);
+PG_API int64_t pg_head_loss_backward_workspace_size(int64_t n, int32_t d, int64_t V,
+                                                    int32_t dtype);
+PG_API int64_t pg_head_distill_workspace_size(int64_t n, int32_t d, int64_t V, int32_t k,
+                                              int32_t dtype);
+PG_API int64_t pg_head_distill_backward_workspace_size(int64_t n, int32_t d, int64_t V, int32_t k,
+                                                       int32_t dtype);
+
+/*
+ * pg_head_loss -- cross entropy of each row against a target token:
+ *   lse_n  = log sum_v exp(z_nv)
+ *   loss_n = lse_n - z_n,targets[n]; 0 for a target outside [0, V)
+ * targets int32 [n]; loss, lse fp32 [n] (device), lse written for every row.
+ * The mean over a batch is the caller's, by way of dloss.
+ */
+PG_API int pg_head_loss(const void* h, int32_t dtype, int64_t n, int32_t d, int64_t ld_h,
+                        const pg_table* table, float scale, const int32_t* targets, float* loss,
+                        float* lse, void* workspace, int64_t workspace_bytes,
+                        hipStream_t stream);
+
+/*
+ * pg_head_loss_backward -- dh and dT from lse (pg_head_loss's), the gradients
+ * dloss fp32 [n] of loss and dlse fp32 [n] of lse (nullable: zero):
+ *   dz_nv = a_n exp(z_nv - lse_n) - w_n [v = targets[n]],
+ *   w_n = dloss_n (0 for a target outside [0, V)), a_n = w_n + dlse_n.
+ * A row with a_n = w_n = 0 adds nothing to dT, whatever its h holds, and its
+ * dh is zero.
+ *   dh  [n] rows of d elements of dtype, stride ld_dh (nullable)
+ *   dw  dT, [V][d] of dw_dtype, PG_F32 or PG_BF16, written whole, or with
+ *       accumulate = 1 (fp32 only, PG_EUNSUPPORTED for bf16) added to: after
+ *       pg_embed_backward_dense the gradient of a tied table (nullable)
+ * Not both dh and dw may be NULL. n = 0 writes zeros to dw unless accumulate.
+ */
+PG_API int pg_head_loss_backward(const void* h, int32_t dtype, int64_t n, int32_t d, int64_t ld_h,
+                                 const pg_table* table, float scale, const int32_t* targets,
+                                 const float* lse, const float* dloss, const float* dlse,
+                                 void* dh, int64_t ld_dh, void* dw, int32_t dw_dtype,
+                                 int32_t accumulate, void* workspace, int64_t workspace_bytes,
+                                 hipStream_t stream);
+
+/*
+ * pg_head_distill -- distillation from the k largest logits of a teacher,
+ * at temperature tau (> 0, finite, as its reciprocal):
+ *   q_nj   = softmax over the row's entries j of teacher_nj / tau; an entry
+ *            whose id lies outside [0, V) is none (shorter lists)
+ *   lse_n  = log sum_v exp(z_nv / tau), over the whole vocabulary
+ *   loss_n = tau^2 sum_j q_nj (log q_nj - (z_n,id_j / tau - lse_n)),
+ * the Kullback-Leibler divergence, 0 for a row without entries or whose
+ * entries are all -infinity. An id may be named twice; its shares add up.
+ *   ids int32 [n][k], teacher fp32 [n][k], 1 <= k <= 256 (PG_EUNSUPPORTED
+ *   beyond); loss, lse fp32 [n]; logits fp32 [n][k]: z at the ids, 0 where
+ *   there is none, what the backward pass takes
+ */
+PG_API int pg_head_distill(const void* h, int32_t dtype, int64_t n, int32_t d, int64_t ld_h,
+                           const pg_table* table, float scale, const int32_t* ids,
+                           const float* teacher, int32_t k, float temperature, float* loss,
+                           float* lse, float* logits, void* workspace, int64_t workspace_bytes,
+                           hipStream_t stream);
+
+/*
+ * pg_head_distill_backward -- dh and dT (as pg_head_loss_backward's) from
+ * pg_head_distill's lse and logits and the gradient dloss fp32 [n] of loss:
+ *   dz_nv = dloss_n tau (exp(z_nv / tau - lse_n) - sum of q_nj with id_j = v).
+ */
+PG_API int pg_head_distill_backward(const void* h, int32_t dtype, int64_t n, int32_t d,
+                                    int64_t ld_h, const pg_table* table, float scale,
+                                    const int32_t* ids, const float* teacher, int32_t k,
+                                    float temperature, const float* lse, const float* logits,
+                                    const float* dloss, void* dh, int64_t ld_dh, void* dw,
+                                    int32_t dw_dtype, int32_t accumulate, void* workspace,
+                                    int64_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Flash page-cache simulation (host code; PageGram tech report §2.3, §3.3,
  * §8 Fig. 4a and appendix D). A table kept on flash is read in 4 KiB blocks;
  * a RAM page cache with LRU replacement holds whole blocks; each lookup whose
