@@ -35,6 +35,7 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16v2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
@@ -623,23 +624,218 @@ __global__ __launch_bounds__(64 * WGM * WGN) void head_tile_kernel(TileArgs g) {
   walk_tiles<EPI, F16, BM, BN, WGM, WGN, false, false>(g, smem, next);
 }
 
-// Both gradients' products of a piece in one launch, a tile each: the first
-// nw blocks dT = dz^T h (both operands transposed), the others dh = dz T.
+// Both gradients' products of a piece in one launch, a tile each: nw blocks of
+// dT = dz^T h (both operands transposed) and nh of dh = dz T, whichever has the
+// longer K first.
 template <int BM, int BN, int WGM, int WGN>
-__global__ __launch_bounds__(64 * WGM * WGN) void head_grad_kernel(TileArgs w, TileArgs h, uint32_t nw) {
+__global__ __launch_bounds__(64 * WGM * WGN) void head_grad_kernel(TileArgs w, TileArgs h,
+                                                                   uint32_t nw, uint32_t nh) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Geo<BM, BN, WGM, WGN>::kLds];
   auto one = [](uint32_t b, uint32_t total) {
     const uint32_t per = total / 8;
     return b < per * 8 ? (b & 7) * per + (b >> 3) : b;
   };
-  if (blockIdx.x < nw) {
-    const uint32_t id = one(blockIdx.x, nw);
+  const bool w_first = w.slots / w.splits > h.slots / h.splits;
+  const uint32_t b = blockIdx.x;
+  if (w_first ? b < nw : b >= nh) {
+    const uint32_t id = one(w_first ? b : b - nh, nw);
     walk_tiles<EPI_OUT, true, BM, BN, WGM, WGN, true, true>(
         w, smem, [&](int j) { return j ? 0xFFFFFFFFu : id; });
   } else {
-    const uint32_t id = one(blockIdx.x - nw, gridDim.x - nw);
+    const uint32_t id = one(w_first ? b - nw : b, nh);
     walk_tiles<EPI_OUT, true, BM, BN, WGM, WGN, false, true>(
         h, smem, [&](int j) { return j ? 0xFFFFFFFFu : id; });
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens
+
+// Maxima and sums of few tokens over 128 rows of the table: what counts is
+// reading the table once, from where it lies and whatever its width. Blocks of
+// up to 64 tokens, those of one tile of the table next to each other. A wave has
+// 32 rows to itself and takes the fragments of 16 x 16 x 32 products straight
+// from memory, 16 rows by 64 bytes a load; the next 128 of K are under way
+// while the last are multiplied. No barrier until the end. (Fragments of
+// 32 x 32 x 16, 32 bytes a row, read at 4.0 TB/s, 64 bytes at 6.1, as whole
+// rows would.) fp32 operands are split in registers into three bf16 planes (24
+// bits), six products for one, so nothing has to be placed or copied.
+struct FewArgs {
+  const void *h, *table;
+  int64_t ld, n, V;
+  int d, groups;           // of 64 tokens
+  float c2;
+  float2* part;            // [tiles of 128 rows][n]
+};
+
+template <typename T, int TB>
+__global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g) {
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int ST = F32 ? 2 : 4;                    // steps of 32 of K under way
+  constexpr int P = F32 ? 3 : 1, KC = 32 * ST;
+  constexpr int RB = KC * 2;                         // bytes of a token's row in LDS
+  constexpr int CH = 16 * TB * KC / 8;               // its 8-element chunks in all
+  constexpr int HL = (CH + 255) / 256;               // of them a thread
+  __shared__ __attribute__((aligned(256))) uint8_t hs[2][P][16 * TB * RB];
+  __shared__ float2 red[4][16 * TB];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, fr = lane & 15, kq = lane >> 4;
+  // a tile's groups run 8 blocks apart: on one XCD, where they share its L2
+  const uint32_t id = blockIdx.x;
+  const uint32_t grp = g.groups == 1 ? 0 : (id >> 3) % g.groups;
+  const uint32_t tile = g.groups == 1 ? id : (id >> 3) / g.groups * 8 + (id & 7);
+  if ((int64_t)tile * 128 >= g.V) return;
+  const int64_t v0 = (int64_t)tile * 128 + wave * 32, x0 = (int64_t)grp * 64;
+  const T* wp[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int64_t v = v0 + r * 16 + fr;
+    wp[r] = static_cast<const T*>(g.table) + (v < g.V ? v : g.V - 1) * g.d + kq * 8;
+  }
+  // 16-byte chunk c of token x in LDS: the 16 tokens a read serves together
+  // meet every bank once
+  auto place = [](int x, int c) {
+    return RB == 256 ? x * 256 + ((c ^ (x & 15)) * 16) : x * 128 + ((c ^ ((x >> 1) & 7)) * 16);
+  };
+  const T* hp[HL];
+  int hc[HL];
+#pragma unroll
+  for (int u = 0; u < HL; ++u) {
+    const int i = u * 256 + threadIdx.x, x = i / (KC / 8);
+    hc[u] = i % (KC / 8) * 8;
+    hp[u] = static_cast<const T*>(g.h) + (x0 + x < g.n ? x0 + x : g.n - 1) * g.ld + hc[u];
+  }
+  f32x4_t acc[TB][2] = {};
+  // a fragment's planes (bf16: itself)
+  auto planes = [](const Raw8<T>& v, uint4 (&f)[P]) {
+    if constexpr (F32) {
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = v.v[u];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        uint32_t w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          w[u] = pack2_bf16(x[2 * u], x[2 * u + 1]);
+          x[2 * u] -= __uint_as_float(w[u] << 16);
+          x[2 * u + 1] -= __uint_as_float(w[u] & 0xFFFF0000u);
+        }
+        f[p] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+      f[0] = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    }
+  };
+  Raw8<T> hr[HL], wr[2][ST][2];
+  auto load = [&](int k, Raw8<T> (&w)[ST][2]) {
+    const bool all = k + KC <= g.d;
+#pragma unroll
+    for (int u = 0; u < HL; ++u)
+      if (HL * 256 == CH || u * 256 + (int)threadIdx.x < CH)
+        hr[u] = load8(hp[u] + k, all ? 8 : g.d - k - hc[u]);
+#pragma unroll
+    for (int s = 0; s < ST; ++s)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        w[s][r] = load8(wp[r] + k + s * 32, all ? 8 : g.d - k - s * 32 - kq * 8);
+  };
+  auto stage = [&](int buf) {
+#pragma unroll
+    for (int u = 0; u < HL; ++u) {
+      const int i = u * 256 + threadIdx.x;
+      if (HL * 256 == CH || i < CH) {
+        uint4 f[P];
+        planes(hr[u], f);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          *reinterpret_cast<uint4*>(hs[buf][p] + place(i / (KC / 8), i % (KC / 8))) = f[p];
+      }
+    }
+  };
+  auto multiply = [&](int buf, const Raw8<T> (&w)[ST][2]) {
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      uint4 wf[2][P];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) planes(w[s][r], wf[r]);
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        uint4 hf[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          hf[p] = *reinterpret_cast<const uint4*>(hs[buf][p] + place(t * 16 + fr, s * 4 + kq));
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          auto mma = [&](int a, int b) {
+            acc[t][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8_t, wf[r][a]), __builtin_bit_cast(bf16x8_t, hf[b]),
+                acc[t][r], 0, 0, 0);
+          };
+          if constexpr (F32) {
+            mma(2, 0);
+            mma(0, 2);
+            mma(1, 1);
+            mma(1, 0);
+            mma(0, 1);
+          }
+          mma(0, 0);
+        }
+      }
+    }
+  };
+  // One barrier a chunk: a buffer is written again two chunks on, behind the
+  // barrier that every wave reaches with its reads of it done.
+  const int chunks = (g.d + KC - 1) / KC;
+  int at = (int)(tile % chunks);                     // tiles start apart
+  auto chunk = [&](int c, int buf, const Raw8<T> (&w)[ST][2], Raw8<T> (&next)[ST][2]) {
+    stage(buf);
+    at = at + 1 == chunks ? 0 : at + 1;
+    if (c + 1 < chunks) load(at * KC, next);
+    wait_lds();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    multiply(buf, w);
+  };
+  load(at * KC, wr[0]);
+  for (int c = 0; c < chunks; c += 2) {
+    chunk(c, 0, wr[0], wr[1]);
+    if (c + 1 < chunks) chunk(c + 1, 1, wr[1], wr[0]);
+  }
+
+  // a lane has rows 16 r + 4 kq + q of the wave's 32, token 16 t + fr
+#pragma unroll
+  for (int t = 0; t < TB; ++t) {
+    float z[2][4], m = -INFINITY;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        z[r][q] = v0 + r * 16 + 4 * kq + q < g.V ? acc[t][r][q] * g.c2 : -INFINITY;
+        m = fmaxf(m, z[r][q]);
+      }
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s += __builtin_amdgcn_exp2f(z[r][q] - ref);
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (kq == 0) red[wave][t * 16 + fr] = make_float2(m, s);
+  }
+  __syncthreads();
+  const int x = threadIdx.x;
+  if (x < 16 * TB && x0 + x < g.n) {
+    float m = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, red[w][x].x);
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) s += red[w][x].y * __builtin_amdgcn_exp2f(red[w][x].x - ref);
+    g.part[(int64_t)tile * g.n + x0 + x] = make_float2(m, s);
   }
 }
 
@@ -661,7 +857,14 @@ __device__ __forceinline__ float wave_max(float v) {
 template <typename T>
 __device__ __forceinline__ float row_dot(const T* x, const T* y, int d, int lane) {
   float s = 0.f;
-  for (int c = lane * 8; c < d; c += 512) {
+  int c = lane * 8;
+#pragma unroll 4
+  for (; c + 8 <= d; c += 512) {
+    const Raw8<T> a = load8(x + c, 8), b = load8(y + c, 8);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s = fmaf(a.get(u), b.get(u), s);
+  }
+  if (c < d) {
     const Raw8<T> a = load8(x + c, d - c), b = load8(y + c, d - c);
 #pragma unroll
     for (int u = 0; u < 8; ++u) s = fmaf(a.get(u), b.get(u), s);
@@ -706,8 +909,9 @@ __device__ __forceinline__ float teacher_shares(const int32_t* ids, const float*
 }
 
 // Joins the tiles' maxima and sums along the vocabulary and forms the losses:
-// blocks of 8 rows by 1024 threads, 128 threads a row for the join, then two
-// waves a row for the dot products that its targets name.
+// blocks of R rows by NT threads, NT / R threads a row for the join, whole waves
+// a row for the dot products that its targets name. Eight rows by 1024 threads,
+// or, where there are few, one by 256.
 struct JoinArgs {
   const float2* part;
   int64_t parts;
@@ -723,22 +927,34 @@ struct JoinArgs {
   int k;
   float *loss, *lse, *logits;
 };
-constexpr int kJoinRows = 8;
-
-template <typename T>
-__global__ __launch_bounds__(1024) void head_join_kernel(JoinArgs g) {
-  __shared__ float2 red[16][kJoinRows];
+template <typename T, int kJoinRows, int NT>
+__global__ __launch_bounds__(NT) void head_join_kernel(JoinArgs g) {
+  constexpr int NW = NT / 64, WR = NW / kJoinRows;   // waves, and of them a row
+  __shared__ float2 red[NW][kJoinRows];
   __shared__ float lse_s[kJoinRows];
   __shared__ float zs[kJoinRows][kMaxK];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t r0 = (int64_t)blockIdx.x * kJoinRows;
+  // dot products
+  const int r = wave / WR;
+  const int64_t row = r0 + r;
+  if (row < g.n) {
+    const T* hr = static_cast<const T*>(g.h) + row * g.ld;
+    const T* tab = static_cast<const T*>(g.table);
+    for (int j = wave % WR; j < g.k; j += WR) {
+      const int id = g.ids[row * g.k + j];
+      float z = 0.f;
+      if (id >= 0 && id < g.V) z = g.scale * row_dot(hr, tab + (int64_t)id * g.d, g.d, lane);
+      if (lane == 0) zs[r][j] = z;
+    }
+  }
   {
-    const int r = tid & (kJoinRows - 1);
-    const int64_t row = r0 + r < g.n ? r0 + r : g.n - 1;
+    const int rr = tid % kJoinRows;
+    const int64_t jr = r0 + rr < g.n ? r0 + rr : g.n - 1;
     float m = -INFINITY, s = 0.f;
 #pragma unroll 4
-    for (int64_t p = tid / kJoinRows; p < g.parts; p += 1024 / kJoinRows) {
-      const float2 v = g.part[p * g.n + row];
+    for (int64_t p = tid / kJoinRows; p < g.parts; p += NT / kJoinRows) {
+      const float2 v = g.part[p * g.n + jr];
       const float hi = fmaxf(m, v.x), ref = hi == -INFINITY ? 0.f : hi;
       s = s * __builtin_amdgcn_exp2f(m - ref) + v.y * __builtin_amdgcn_exp2f(v.x - ref);
       m = hi;
@@ -755,28 +971,18 @@ __global__ __launch_bounds__(1024) void head_join_kernel(JoinArgs g) {
   __syncthreads();
   if (tid < kJoinRows) {
     float m = -INFINITY, s = 0.f;
-    for (int w = 0; w < 16; ++w) m = fmaxf(m, red[w][tid].x);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) m = fmaxf(m, red[w][tid].x);
     const float ref = m == -INFINITY ? 0.f : m;
-    for (int w = 0; w < 16; ++w) s += red[w][tid].y * __builtin_amdgcn_exp2f(red[w][tid].x - ref);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) s += red[w][tid].y * __builtin_amdgcn_exp2f(red[w][tid].x - ref);
     // log(s 2^m)
     const float l = (m + log2f(s)) * kLn2;
     lse_s[tid] = l;
     if (r0 + tid < g.n) g.lse[r0 + tid] = l;
   }
-  // dot products: two waves a row
-  const int r = wave >> 1;
-  const int64_t row = r0 + r;
-  const T* hr = static_cast<const T*>(g.h) + row * g.ld;
-  const T* tab = static_cast<const T*>(g.table);
-  if (row < g.n)
-    for (int j = wave & 1; j < g.k; j += 2) {
-      const int id = g.ids[row * g.k + j];
-      float z = 0.f;
-      if (id >= 0 && id < g.V) z = g.scale * row_dot(hr, tab + (int64_t)id * g.d, g.d, lane);
-      if (lane == 0) zs[r][j] = z;
-    }
   __syncthreads();
-  if ((wave & 1) || row >= g.n) return;
+  if (wave % WR || row >= g.n) return;
   const float l = lse_s[r];
   if (!g.teacher) {
     const int id = g.ids[row];
@@ -863,6 +1069,9 @@ __device__ __forceinline__ void put_raw(const uint16_t* src, int d, int c, bool 
   *reinterpret_cast<uint4*>(dst + c) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
 }
 
+// tokens up to which the table's reading is all that counts: read in place, or
+// where tiles would need a copy of it
+constexpr int kFew = 64, kFewCopied = 256;
 constexpr int kScanBlocks = 512;
 constexpr int kRowBlocks = 512;           // most blocks over rows, four waves each
 
@@ -1159,7 +1368,7 @@ int elt_size(int32_t dtype) { return dtype == PG_F32 ? 4 : 2; }
 // An operand that the logits' tiles can read where it lies: bf16 rows of whole
 // slots at 16-byte alignment.
 bool in_place(int32_t dtype, int d, int64_t ld, const void* p) {
-  return dtype == PG_BF16 && d % 64 == 0 && d >= 128 && ld % 8 == 0 && ld < (1 << 24) &&
+  return dtype == PG_BF16 && d % 32 == 0 && d >= 128 && ld % 8 == 0 && ld < (1 << 24) &&
          (uintptr_t)p % 16 == 0;
 }
 
@@ -1203,12 +1412,10 @@ void launch_copy(bool f32, const RowArgs& r, const PieceArgs& w, bool rows, hipS
 // ---------------------------------------------------------------------------
 // Workspace geometry
 
-constexpr int kSplitBlocks = 512;         // most tiles of products whose K is split
-
 HeadPlan head_plan(int64_t n, int d, int64_t V, int32_t dtype, int k, bool backward) {
   HeadPlan p{};
   p.planes = dtype == PG_F32 ? 2 : 1;
-  p.dp = (int)pad(d < 128 ? 128 : d, 64);
+  p.dp = (int)pad(d < 128 ? 128 : d, 32);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;
@@ -1246,11 +1453,11 @@ HeadPlan head_plan(int64_t n, int d, int64_t V, int32_t dtype, int k, bool backw
     p.off_h = take(p.rows * row);
     p.off_hz = take(p.rows * row);
     p.off_w = take(p.cols * row);
-    p.off_wz = p.planes == 1 && !(d % 64 == 0 && d >= 128) ? take(p.cols * row) : at;
+    p.off_wz = p.planes == 1 && !(d % 32 == 0 && d >= 128) ? take(p.cols * row) : at;
     p.off_dz = take(p.rows * p.cols * 2 * p.planes);
     p.off_dh = take(p.rows * d * 4);
     p.off_dw = n > 32768 ? take(V * d * 4) : at;
-    p.off_split = take((int64_t)kSplitBlocks * 128 * 128 * 4);
+    p.off_split = take((int64_t)kCUs * 256 * 256 * 4);   // most tiles at once
   }
   p.bytes = at;
   return p;
@@ -1269,48 +1476,62 @@ hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* works
   t.M = g.n;
   t.rowf = reinterpret_cast<const float*>(ws + p.off_rowf);
   t.slots = p.dp / 32;
-  RowArgs r{};
-  r.h = g.h;
-  r.ld = g.ld_h;
-  r.n = r.rows_pad = g.n;
-  r.vec_pad = pad(g.n, 256);
-  r.d = g.d;
-  r.dp = p.dp;
-  r.rowf = reinterpret_cast<float*>(ws + p.off_rowf);
-  r.part_w = parts_w;
-  r.c2 = t.c2;
-  if (f32) {
-    r.nparts_w = blocks_for((g.V * g.d + 7) / 8, kScanBlocks);
-    hipLaunchKernelGGL((head_scan_kernel<float>), dim3(r.nparts_w), dim3(256), 0, s,
-                       static_cast<const float*>(g.table), g.V * g.d, parts_w);
-  }
-  const bool h_here = in_place(g.dtype, g.d, g.ld_h, g.h);
-  if (h_here) {
-    t.A = Side{static_cast<const uint8_t*>(g.h), g.ld_h * 2, 0, g.n};
-  } else {
-    r.hz = reinterpret_cast<uint16_t*>(ws + p.off_hz);
-    t.A = Side{ws + p.off_hz, dp2, g.n * dp2, g.n};
-  }
-  const bool w_here = in_place(g.dtype, g.d, g.d, g.table);
-  const int64_t piece = w_here ? g.V : p.cols;
   int64_t parts = 0;
-  for (int64_t v0 = 0; v0 < g.V; v0 += piece) {
-    const int64_t c = g.V - v0 < piece ? g.V - v0 : piece;
-    PieceArgs w{};
-    w.src = static_cast<const uint8_t*>(g.table) + v0 * g.d * es;
-    if (w_here) {
-      t.B = Side{static_cast<const uint8_t*>(w.src), (int64_t)g.d * 2, 0, c};
-    } else {
-      w.rows = w.rows_pad = c;
-      (f32 ? w.wp : w.wz) = reinterpret_cast<uint16_t*>(ws + p.off_wz);
-      t.B = Side{ws + p.off_wz, dp2, c * dp2, c};
+  const bool h_here = in_place(g.dtype, g.d, g.ld_h, g.h);
+  const bool w_here = in_place(g.dtype, g.d, g.d, g.table);
+  if (g.n <= (w_here ? kFew : kFewCopied)) {
+    const int groups = (int)tiles_of(g.n, 64);
+    const FewArgs f{g.h, g.table, g.ld_h, g.n, g.V, g.d, groups, t.c2,
+                    reinterpret_cast<float2*>(ws + p.off_part)};
+    parts = tiles_of(g.V, 128);
+    const int64_t blocks = groups == 1 ? parts : pad(parts, 8) * groups;
+    auto* kernel = f32 ? (g.n <= 16 ? head_few_kernel<float, 1> : g.n <= 32 ? head_few_kernel<float, 2>
+                                                                            : head_few_kernel<float, 4>)
+                       : (g.n <= 16   ? head_few_kernel<uint16_t, 1>
+                          : g.n <= 32 ? head_few_kernel<uint16_t, 2>
+                                      : head_few_kernel<uint16_t, 4>);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, s, f);
+  } else {
+    RowArgs r{};
+    r.h = g.h;
+    r.ld = g.ld_h;
+    r.n = r.rows_pad = g.n;
+    r.vec_pad = pad(g.n, 256);
+    r.d = g.d;
+    r.dp = p.dp;
+    r.rowf = reinterpret_cast<float*>(ws + p.off_rowf);
+    r.part_w = parts_w;
+    r.c2 = t.c2;
+    if (f32) {
+      r.nparts_w = blocks_for((g.V * g.d + 7) / 8, kScanBlocks);
+      hipLaunchKernelGGL((head_scan_kernel<float>), dim3(r.nparts_w), dim3(256), 0, s,
+                         static_cast<const float*>(g.table), g.V * g.d, parts_w);
     }
-    launch_copy(f32, r, w, v0 == 0 && !h_here, s);
-    t.V = c;
-    t.part = reinterpret_cast<float2*>(ws + p.off_part) + parts * g.n;
-    const hipError_t e = launch_tiles<EPI_LSE>(t, g.n, c, f32, s);
-    if (e != hipSuccess) return e;
-    parts += t.nbn;
+    if (h_here) {
+      t.A = Side{static_cast<const uint8_t*>(g.h), g.ld_h * 2, 0, g.n};
+    } else {
+      r.hz = reinterpret_cast<uint16_t*>(ws + p.off_hz);
+      t.A = Side{ws + p.off_hz, dp2, g.n * dp2, g.n};
+    }
+    const int64_t piece = w_here ? g.V : p.cols;
+    for (int64_t v0 = 0; v0 < g.V; v0 += piece) {
+      const int64_t c = g.V - v0 < piece ? g.V - v0 : piece;
+      PieceArgs w{};
+      w.src = static_cast<const uint8_t*>(g.table) + v0 * g.d * es;
+      if (w_here) {
+        t.B = Side{static_cast<const uint8_t*>(w.src), (int64_t)g.d * 2, 0, c};
+      } else {
+        w.rows = w.rows_pad = c;
+        (f32 ? w.wp : w.wz) = reinterpret_cast<uint16_t*>(ws + p.off_wz);
+        t.B = Side{ws + p.off_wz, dp2, c * dp2, c};
+      }
+      launch_copy(f32, r, w, v0 == 0 && !h_here, s);
+      t.V = c;
+      t.part = reinterpret_cast<float2*>(ws + p.off_part) + parts * g.n;
+      const hipError_t e = launch_tiles<EPI_LSE>(t, g.n, c, f32, s);
+      if (e != hipSuccess) return e;
+      parts += t.nbn;
+    }
   }
   JoinArgs j{};
   j.part = reinterpret_cast<const float2*>(ws + p.off_part);
@@ -1329,11 +1550,11 @@ hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* works
   j.loss = g.loss;
   j.lse = g.lse;
   j.logits = g.logits;
-  const unsigned grid = (unsigned)((g.n + kJoinRows - 1) / kJoinRows);
-  if (f32)
-    hipLaunchKernelGGL((head_join_kernel<float>), dim3(grid), dim3(1024), 0, s, j);
-  else
-    hipLaunchKernelGGL((head_join_kernel<uint16_t>), dim3(grid), dim3(1024), 0, s, j);
+  const bool alone = g.n <= 2 * kCUs;
+  const unsigned grid = (unsigned)(alone ? g.n : tiles_of(g.n, 8)), nt = alone ? 256 : 1024;
+  auto* join = f32 ? (alone ? head_join_kernel<float, 1, 256> : head_join_kernel<float, 8, 1024>)
+                   : (alone ? head_join_kernel<uint16_t, 1, 256> : head_join_kernel<uint16_t, 8, 1024>);
+  hipLaunchKernelGGL(join, dim3(grid), dim3(nt), 0, s, j);
   return hipGetLastError();
 }
 
@@ -1348,24 +1569,27 @@ static hipError_t launch_grads(TileArgs tw, TileArgs th, float* split, hipStream
   auto tiles = [&](TileArgs& t) {
     t.nbm = (int)tiles_of(t.M, b);
     t.nbn = (int)tiles_of(t.V, b);
-    t.splits = 1;
     return (int64_t)t.nbm * t.nbn;
   };
+  tw.splits = th.splits = 1;
   const int64_t nw = w ? tiles(tw) : 0, nh = h ? tiles(th) : 0;
-  // 128 x 128 tiles run two to a compute unit: K is shared until they fill the
-  // chip, down to 8 slots a tile
+  // A tile's chain of slots is not to take longer than the whole launch spread
+  // over the chip (256 large tiles at once, 512 small ones): longer ones share
+  // their K, down to 8 slots a tile.
+  const int at_once = big ? kCUs : 2 * kCUs;
+  const int64_t fair = ((w ? nw * tw.slots : 0) + (h ? nh * th.slots : 0)) / at_once + 1;
   SumArgs sums[2] = {};
   int64_t used = 0;
-  auto share = [&](TileArgs& t, int64_t n, int64_t budget, SumArgs& sa) {
+  auto share = [&](TileArgs& t, int64_t n, SumArgs& sa) {
     if (n == 0) return;
-    int64_t k = budget / n;
+    int64_t k = t.slots / fair;                      // n k <= at_once
     const int64_t most = (int64_t)t.slots * t.nseg / 8;
     if (k > most) k = most;
     if (k > t.slots / 2) k = t.slots / 2;
     if (k < 2) return;
-    sa = SumArgs{split + used, (int)k, 0, (int64_t)t.nbn * 128, t.M, t.V, t.prev, t.ld_prev,
+    sa = SumArgs{split + used, (int)k, 0, (int64_t)t.nbn * b, t.M, t.V, t.prev, t.ld_prev,
                  t.out, t.ld_out, t.out_bf16};
-    sa.stride = (int64_t)t.nbm * 128 * sa.ld_part;
+    sa.stride = (int64_t)t.nbm * b * sa.ld_part;
     t.splits = (int)k;
     t.out = split + used;
     t.ld_out = sa.ld_part;
@@ -1374,18 +1598,15 @@ static hipError_t launch_grads(TileArgs tw, TileArgs th, float* split, hipStream
     t.prev = nullptr;
     used += k * sa.stride;
   };
-  if (!big && nw + nh < kSplitBlocks) {
-    // in proportion to the work, so that both end together
-    const double ww = (double)nw * tw.slots, wh = (double)nh * th.slots;
-    const int64_t bw = (int64_t)(kSplitBlocks * ww / (ww + wh));
-    share(tw, nw, bw, sums[0]);
-    share(th, nh, kSplitBlocks - bw, sums[1]);
-  }
+  share(tw, nw, sums[0]);
+  share(th, nh, sums[1]);
   const uint32_t gw = (uint32_t)(nw * tw.splits), gh = (uint32_t)(nh * th.splits);
   if (big)
-    hipLaunchKernelGGL((head_grad_kernel<256, 256, 2, 4>), dim3(gw + gh), dim3(512), 0, s, tw, th, gw);
+    hipLaunchKernelGGL((head_grad_kernel<256, 256, 2, 4>), dim3(gw + gh), dim3(512), 0, s, tw, th, gw,
+                       gh);
   else
-    hipLaunchKernelGGL((head_grad_kernel<128, 128, 2, 2>), dim3(gw + gh), dim3(256), 0, s, tw, th, gw);
+    hipLaunchKernelGGL((head_grad_kernel<128, 128, 2, 2>), dim3(gw + gh), dim3(256), 0, s, tw, th, gw,
+                       gh);
   const int sw = sums[0].splits ? blocks_for(sums[0].M * ((sums[0].N + 3) / 4), 1024) : 0;
   const int sh = sums[1].splits ? blocks_for(sums[1].M * ((sums[1].N + 3) / 4), 1024) : 0;
   if (sw + sh)

@@ -6,7 +6,8 @@ relative to the value; a matrix instruction may add its terms with up to a
 whole step each, so a sum of m products is off by at most 2 m u times the sum
 of their magnitudes. fp32 operands, and dz with them, enter as two fp16 halves:
 3 d products instead of d, and 3 * 2^-22 of |x||y| for what they leave out (two
-halves hold x to 2^-22 of it, and the product of the low ones is dropped). fp16
+halves hold x to 2^-22 of it, and the product of the low ones is dropped); up to
+64 tokens' logits as three bf16 planes, 6 d products, of which less is left out. fp16
 values are placed with their largest between 2^14 and 2^15, where steps never
 get smaller than 2^-24: half of one is 2^-39 of the largest.
 """
@@ -58,7 +59,7 @@ class Workspace:
 
 def products(dt, d):
     """Relative error of a dot product of d terms by the sum of magnitudes."""
-    return 2 * d * U if dt == "bf16" else 2 * 3 * d * U + 3.1 * 2.0 ** -22
+    return 2 * d * U if dt == "bf16" else 2 * 6 * d * U + 3.1 * 2.0 ** -22
 
 
 def within(name, got, ref, bound):
