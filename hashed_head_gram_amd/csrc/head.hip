@@ -118,6 +118,15 @@ struct TileArgs {
   // running maximum and sum
   float2* part;        // [nbn][M]
   int64_t M, V;        // valid rows, valid columns
+  // the logits that the targets name, by tile (EPI_PICK): entries of row tile r
+  // and column tile c are list[r cap + starts[r (cols + 1) + c]] .. the next start
+  const uint32_t* list;    // row in the tile, column in it, entry of the row: 8 bits each
+  const int* starts;
+  int64_t cap;
+  int tiles, tile0;        // column tiles in all, of them before this launch
+  float* logits;           // [M][k]
+  int k;
+  float zf;                // base-2 logits to logits
   const float* rowf;       // fp16 operands: c2 with the placements undone, by row
   // gradient of the logits
   const float *a, *lse2;   // [rows padded to whole tiles]
@@ -134,7 +143,8 @@ struct TileArgs {
   const int* all_exp;
 };
 
-enum { EPI_LSE, EPI_DZ, EPI_OUT };
+enum { EPI_LSE, EPI_DZ, EPI_OUT, EPI_PICK };
+constexpr int kPicks = 256;               // entries of a tile that wait in LDS
 
 // One side's walk over K: this wave's part of every slot.
 template <int BX, bool TR, int NW>
@@ -212,9 +222,11 @@ struct Geo {
   static_assert(WTN == 64 && WTM % 32 == 0, "a wave's part");
   static constexpr int kA = BM * 64, kB = BN * 64;   // bytes of a slot
   static constexpr int kRingBytes = kRing * (kA + kB);
-  // row vectors (two tiles' up to three), then the waves' maxima and sums
+  // row vectors (two tiles' up to three), the waves' maxima and sums, two tiles'
+  // first entries
   static constexpr int kRows = 2 * 3 * BM * 4;
-  static constexpr int kExtra = kRows + BM * 8 * WGN;
+  static constexpr int kRed = BM * 8 * WGN;
+  static constexpr int kExtra = kRows + kRed + 2 * kPicks * 4;
   static constexpr int kLds = kRingBytes + kExtra;
   static_assert(kA + kB >= NW * 4096 || kRing * (kA + kB) >= NW * 4096, "patches");
 };
@@ -299,8 +311,25 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
     }
   };
   // a tile's row vectors into the half of its parity
+  constexpr bool LSE = EPI == EPI_LSE || EPI == EPI_PICK;
   constexpr int NV = (EPI == EPI_DZ ? 2 : 0) + (EPI != EPI_OUT && F16 ? 1 : 0);
+  auto picks_of = [&](const Tile& t, int& count) -> const uint32_t* {
+    const int* s = g.starts + (int64_t)t.bm * (g.tiles + 1) + g.tile0 + t.bn;
+    const int a = __builtin_amdgcn_readfirstlane(s[0]);
+    count = __builtin_amdgcn_readfirstlane(s[1]) - a;
+    return g.list + t.bm * g.cap + a;
+  };
+  // and its entries, behind which the list has room for a whole load
   auto issue_rows = [&](const Tile& t, int parity) {
+    if constexpr (EPI == EPI_PICK) {
+      int count;
+      const uint32_t* src = picks_of(t, count);
+#pragma unroll
+      for (int x = 0; x < kPicks / 64; ++x)
+        if (x % NW == wave && x * 64 < count)
+          load_to_lds4(src + x * 64, (uint32_t)lane * 4,
+                       lds0 + G::kRingBytes + G::kRows + G::kRed + parity * (kPicks * 4) + x * 256);
+    }
     constexpr int per = BM / 64;                     // loads of 64 rows
     if constexpr (NV > 0)
 #pragma unroll
@@ -434,7 +463,7 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
     uint8_t* patch;                                  // 4 KiB of the wave's own
     {
       constexpr int inA = G::kA / 4096 < NW ? G::kA / 4096 : NW;
-      if constexpr (EPI != EPI_LSE) static_assert(inA + G::kB / 4096 >= NW, "patches");
+      if constexpr (!LSE) static_assert(inA + G::kB / 4096 >= NW, "patches");
       patch = wave < inA ? smem + free_slot * G::kA + wave * 4096
                          : smemB + free_slot * G::kB + (wave - inA) * 4096;
     }
@@ -442,7 +471,7 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
     const int64_t n0 = (int64_t)cur.bn * BN + wn * 64;
 
     const float* rows = reinterpret_cast<const float*>(extra) + (jt & 1) * NV * BM;
-    if constexpr (EPI == EPI_LSE) {
+    if constexpr (LSE) {
       float2* red = reinterpret_cast<float2*>(extra + G::kRows);          // [WGN][BM]
       const bool edge = n0 + 64 > g.V;
 #pragma unroll
@@ -467,6 +496,35 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
           for (int q = 0; q < 16; ++q) sum += __builtin_amdgcn_exp2f(acc[i][j][q] - ref);
         sum += __shfl_xor(sum, 32);
         if (half == 0) red[wn * BM + wm * G::WTM + i * 32 + fr] = make_float2(m, sum);
+      }
+      if constexpr (EPI == EPI_PICK) {
+        int count;
+        const uint32_t* src = picks_of(cur, count);
+        const auto* near = reinterpret_cast<const uint32_t*>(extra + G::kRows + G::kRed) +
+                           (jt & 1) * kPicks;
+        for (int x = 0; x < count; x += 64) {
+          const uint32_t e = x + lane >= count ? 0xFFFFFFFFu : x < kPicks ? near[x + lane] : src[x + lane];
+          const int row = e & 255, col = (e >> 8) & 255;
+          uint64_t mine = __ballot(e != 0xFFFFFFFFu && row / G::WTM == wm && col / 64 == wn);
+          while (mine) {                             // one entry of this wave's part at a time
+            const int from = __ffsll((unsigned long long)mine) - 1;
+            mine &= mine - 1;
+            const uint32_t p = __builtin_amdgcn_readlane(e, from);
+            const int pr = p & 255, pc = (p >> 8) & 63;
+            const int at = (pr % G::WTM / 32 * FN + pc / 32) * 16 + pc % 32 / 8 * 4 + pc % 4;
+            float z = 0.f;
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+              for (int j = 0; j < FN; ++j)
+                if (at / 16 == i * FN + j)           // uniform
+#pragma unroll
+                  for (int q = 0; q < 16; ++q)
+                    if (at % 16 == q) z = acc[i][j][q];
+            if (lane == (pr & 31) + 32 * ((pc >> 2) & 1))
+              g.logits[((int64_t)cur.bm * BM + pr) * g.k + (p >> 16)] = z * g.zf;
+          }
+        }
       }
       wait_lds();
       barrier();
@@ -925,6 +983,7 @@ struct JoinArgs {
   const int32_t* ids;      // [n][k] (cross entropy: k = 1)
   const float* teacher;    // nullable: cross entropy
   int k;
+  int picked;              // logits holds z already
   float *loss, *lse, *logits;
 };
 template <typename T, int kJoinRows, int NT>
@@ -938,7 +997,12 @@ __global__ __launch_bounds__(NT) void head_join_kernel(JoinArgs g) {
   // dot products
   const int r = wave / WR;
   const int64_t row = r0 + r;
-  if (row < g.n) {
+  if (row < g.n && g.picked) {
+    for (int j = wave % WR * 64 + lane; j < g.k; j += WR * 64) {
+      const int id = g.ids[row * g.k + j];
+      zs[r][j] = id >= 0 && id < g.V ? g.logits[row * g.k + j] : 0.f;
+    }
+  } else if (row < g.n) {
     const T* hr = static_cast<const T*>(g.h) + row * g.ld;
     const T* tab = static_cast<const T*>(g.table);
     for (int j = wave % WR; j < g.k; j += WR) {
@@ -1005,6 +1069,65 @@ __global__ __launch_bounds__(NT) void head_join_kernel(JoinArgs g) {
   }
   x = wave_sum(x);
   if (lane == 0) g.loss[row] = any ? (ent + x) / (g.inv_tau * g.inv_tau) : 0.f;
+}
+
+// Sorts the entries of each row tile by column tile: a block a row tile, counts,
+// a running sum, places. The order inside a tile is free: every entry has a
+// place of its own to write to. Fetched as dot products of their own, 8,192
+// tokens' 64 entries at width 2,560 took 520 of 5,200 us; sorted, and picked
+// from the tiles' accumulators, 30.
+constexpr int kMostTiles = 8192;
+__global__ __launch_bounds__(1024) void head_bin_kernel(const int32_t* ids, int64_t n, int k, int64_t V,
+                                                        int b, int tiles, int64_t cap,
+                                                        uint32_t* list, int* starts) {
+  __shared__ int count[kMostTiles];
+  __shared__ int part[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t r0 = (int64_t)blockIdx.x * b;
+  const int total = (int)((n - r0 < b ? n - r0 : b) * k);
+  const int shift = b == 256 ? 8 : 7;
+  for (int i = tid; i < tiles; i += 1024) count[i] = 0;
+  __syncthreads();
+  const int32_t* src = ids + r0 * k;
+  for (int i = tid; i < total; i += 1024) {
+    const int id = src[i];
+    if (id >= 0 && id < V) atomicAdd(&count[id >> shift], 1);
+  }
+  __syncthreads();
+  int* out = starts + (int64_t)blockIdx.x * (tiles + 1);
+  int base = 0;
+  for (int t0 = 0; t0 < tiles; t0 += 1024) {         // exclusive running sum
+    const int v = t0 + tid < tiles ? count[t0 + tid] : 0;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int y = __shfl_up(x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 63) part[wave] = x;
+    __syncthreads();
+    int before = base, all = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      if (w < wave) before += part[w];
+      all += part[w];
+    }
+    if (t0 + tid < tiles) {
+      count[t0 + tid] = before + x - v;
+      out[t0 + tid] = before + x - v;
+    }
+    base += all;
+    __syncthreads();
+  }
+  if (tid == 0) out[tiles] = base;
+  for (int i = tid; i < total; i += 1024) {
+    const int id = src[i];
+    if (id >= 0 && id < V) {
+      const int row = i / k;
+      list[blockIdx.x * cap + atomicAdd(&count[id >> shift], 1)] =
+          (uint32_t)row | ((uint32_t)(id & (b - 1)) << 8) | ((uint32_t)(i - row * k) << 16);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1377,8 +1500,7 @@ bool big_tiles(int64_t M, int64_t N) {
 }
 
 template <int EPI>
-hipError_t launch_tiles(TileArgs& g, int64_t M, int64_t N, bool f16, hipStream_t s) {
-  const bool big = big_tiles(M, N);
+hipError_t launch_tiles(TileArgs& g, int64_t M, int64_t N, bool big, bool f16, hipStream_t s) {
   const int b = big ? 256 : 128;
   g.splits = 1;
   g.nbm = (int)tiles_of(M, b);
@@ -1434,6 +1556,9 @@ HeadPlan head_plan(int64_t n, int d, int64_t V, int32_t dtype, int k, bool backw
     p.off_hz = take(n * row);
     p.off_wz = take(p.cols * row);
     p.off_part = take((V + 127) / 128 * n * 8);
+    // entries by tile: whole row tiles, and room for a load behind the last
+    p.off_list = take((pad(n, 256) * k + kPicks) * 4);
+    p.off_starts = take(tiles_of(n, 128) * (tiles_of(V, 128) + 1) * 4);
   } else {
     // dz of a piece: at most 2^29 elements (1 GiB) of both halves
     p.rows = pad(n, 128);
@@ -1477,6 +1602,7 @@ hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* works
   t.rowf = reinterpret_cast<const float*>(ws + p.off_rowf);
   t.slots = p.dp / 32;
   int64_t parts = 0;
+  bool picked = false;
   const bool h_here = in_place(g.dtype, g.d, g.ld_h, g.h);
   const bool w_here = in_place(g.dtype, g.d, g.d, g.table);
   if (g.n <= (w_here ? kFew : kFewCopied)) {
@@ -1513,7 +1639,23 @@ hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* works
       r.hz = reinterpret_cast<uint16_t*>(ws + p.off_hz);
       t.A = Side{ws + p.off_hz, dp2, g.n * dp2, g.n};
     }
-    const int64_t piece = w_here ? g.V : p.cols;
+    const int64_t piece = w_here ? g.V : p.cols;       // all but the last of whole tiles
+    const bool big = big_tiles(g.n, g.V < piece ? g.V : piece);
+    const int b = big ? 256 : 128;
+    picked = g.teacher && tiles_of(g.V, b) <= kMostTiles;
+    if (picked) {
+      auto* list = reinterpret_cast<uint32_t*>(ws + p.off_list);
+      auto* starts = reinterpret_cast<int*>(ws + p.off_starts);
+      t.list = list;
+      t.starts = starts;
+      t.cap = (int64_t)b * g.k;
+      t.tiles = (int)tiles_of(g.V, b);
+      t.logits = g.logits;
+      t.k = g.k;
+      t.zf = (float)(0.6931471805599453 / (double)g.inv_tau);
+      hipLaunchKernelGGL(head_bin_kernel, dim3((unsigned)tiles_of(g.n, b)), dim3(1024), 0, s, g.ids,
+                         g.n, g.k, g.V, b, t.tiles, t.cap, list, starts);
+    }
     for (int64_t v0 = 0; v0 < g.V; v0 += piece) {
       const int64_t c = g.V - v0 < piece ? g.V - v0 : piece;
       PieceArgs w{};
@@ -1528,7 +1670,9 @@ hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* works
       launch_copy(f32, r, w, v0 == 0 && !h_here, s);
       t.V = c;
       t.part = reinterpret_cast<float2*>(ws + p.off_part) + parts * g.n;
-      const hipError_t e = launch_tiles<EPI_LSE>(t, g.n, c, f32, s);
+      t.tile0 = (int)parts;
+      const hipError_t e = picked ? launch_tiles<EPI_PICK>(t, g.n, c, big, f32, s)
+                                  : launch_tiles<EPI_LSE>(t, g.n, c, big, f32, s);
       if (e != hipSuccess) return e;
       parts += t.nbn;
     }
@@ -1547,6 +1691,7 @@ hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* works
   j.ids = g.ids;
   j.teacher = g.teacher;
   j.k = g.k;
+  j.picked = picked;
   j.loss = g.loss;
   j.lse = g.lse;
   j.logits = g.logits;
@@ -1708,7 +1853,7 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
       t.dz_plane = plane;
       t.Mpad = rows;
       t.Vpad = cols;
-      hipError_t e = launch_tiles<EPI_DZ>(t, rows, cols, f32, s);
+      hipError_t e = launch_tiles<EPI_DZ>(t, rows, cols, big_tiles(rows, cols), f32, s);
       if (e != hipSuccess) return e;
       hipLaunchKernelGGL(head_sparse_kernel, dim3(blocks_for(n * g.k, 8192)), dim3(256), 0, s,
                          r.sidx, r.sval, n, g.k, v0, c, dz, ldz, plane, p.planes);

@@ -186,7 +186,7 @@ struct HeadPlan {
   int planes;                 // halves of an fp32 operand
   int dp;                     // padded width
   int64_t rows, cols;
-  int64_t off_parts, off_rowf, off_hz, off_wz, off_part;
+  int64_t off_parts, off_rowf, off_hz, off_wz, off_part, off_list, off_starts;
   int64_t off_a, off_lse, off_exp, off_sidx, off_sval, off_h, off_w, off_dz, off_dh,
       off_dw, off_split;
   int64_t bytes;
