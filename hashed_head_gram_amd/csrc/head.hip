@@ -474,26 +474,38 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
     if constexpr (LSE) {
       float2* red = reinterpret_cast<float2*>(extra + G::kRows);          // [WGN][BM]
       const bool edge = n0 + 64 > g.V;
+      float flip = 1.f;
+      if (g.c2 < 0.f) {                              // the largest logit is the smallest product
+        flip = -1.f;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = -acc[i][j];
+      }
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
+        if (edge)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+              if (n0 + j * 32 + 8 * (q >> 2) + 4 * half + (q & 3) >= g.V) acc[i][j][q] = -INFINITY;
+        // (never 0, so that masked columns stay -infinity under it)
+        const float c2 = fmaxf(flip * (F16 ? rows[wm * G::WTM + i * 32 + fr] : g.c2), 1.2e-38f);
         float m = -INFINITY;
-        const float c2 = F16 ? rows[wm * G::WTM + i * 32 + fr] : g.c2;
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            float v = acc[i][j][q] * c2;
-            if (edge && n0 + j * 32 + 8 * (q >> 2) + 4 * half + (q & 3) >= g.V) v = -INFINITY;
-            acc[i][j][q] = v;
-            m = fmaxf(m, v);
-          }
+          for (int q = 0; q < 16; ++q) m = fmaxf(m, acc[i][j][q]);
         m = fmaxf(m, __shfl_xor(m, 32));
+        m *= c2;
         const float ref = m == -INFINITY ? 0.f : m;
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int q = 0; q < 16; ++q) sum += __builtin_amdgcn_exp2f(acc[i][j][q] - ref);
+          for (int q = 0; q < 16; ++q)
+            sum += __builtin_amdgcn_exp2f(fmaf(acc[i][j][q], c2, -ref));
         sum += __shfl_xor(sum, 32);
         if (half == 0) red[wn * BM + wm * G::WTM + i * 32 + fr] = make_float2(m, sum);
       }
@@ -522,7 +534,8 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
                   for (int q = 0; q < 16; ++q)
                     if (at % 16 == q) z = acc[i][j][q];
             if (lane == (pr & 31) + 32 * ((pc >> 2) & 1))
-              g.logits[((int64_t)cur.bm * BM + pr) * g.k + (p >> 16)] = z * g.zf;
+              g.logits[((int64_t)cur.bm * BM + pr) * g.k + (p >> 16)] =
+                  z * (flip * (F16 ? rows[pr] : g.c2)) * g.zf;
           }
         }
       }
@@ -550,11 +563,16 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
         for (int j = 0; j < FN; ++j)
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
-            // rows without weight give zeros whatever their logits are
-            float v = a == 0.f ? 0.f : a * __builtin_amdgcn_exp2f(acc[i][j][q] * c2 - l);
+            float v = a * __builtin_amdgcn_exp2f(fmaf(acc[i][j][q], c2, -l));
             if (edge && n0 + j * 32 + 8 * (q >> 2) + 4 * half + (q & 3) >= g.V) v = 0.f;
             acc[i][j][q] = v;
           }
+        // rows without weight give zeros whatever their logits are
+        if (__any(a == 0.f))
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) acc[i][j][q] = a == 0.f ? 0.f : acc[i][j][q];
 #pragma unroll
         for (int p = 0; p < (F16 ? 2 : 1); ++p) {
           if (i + p > 0) wave_sync();
@@ -663,7 +681,7 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
 // One product's tiles. Consecutive tile numbers run on one of the 8 XCDs and
 // share panels in its L2; a block walks every 1/8 grid-th of its XCD's range.
 template <int EPI, bool F16, int BM, int BN, int WGM, int WGN>
-__global__ __launch_bounds__(64 * WGM * WGN) void head_tile_kernel(TileArgs g) {
+__global__ __launch_bounds__(64 * WGM * WGN, 2) void head_tile_kernel(TileArgs g) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Geo<BM, BN, WGM, WGN>::kLds];
   const uint32_t total = (uint32_t)g.nbm * g.nbn * g.splits, per = total / 8;
   const uint32_t grid = gridDim.x;
@@ -686,7 +704,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void head_tile_kernel(TileArgs g) {
 // dT = dz^T h (both operands transposed) and nh of dh = dz T, whichever has the
 // longer K first.
 template <int BM, int BN, int WGM, int WGN>
-__global__ __launch_bounds__(64 * WGM * WGN) void head_grad_kernel(TileArgs w, TileArgs h,
+__global__ __launch_bounds__(64 * WGM * WGN, 2) void head_grad_kernel(TileArgs w, TileArgs h,
                                                                    uint32_t nw, uint32_t nh) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Geo<BM, BN, WGM, WGN>::kLds];
   auto one = [](uint32_t b, uint32_t total) {
