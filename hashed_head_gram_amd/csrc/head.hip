@@ -471,9 +471,10 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
     const int64_t n0 = (int64_t)cur.bn * BN + wn * 64;
 
     const float* rows = reinterpret_cast<const float*>(extra) + (jt & 1) * NV * BM;
+    const int live = (int)(g.V - n0 < 64 ? g.V - n0 : 64);     // columns of this wave's 64
+    const bool edge = live < 64;
     if constexpr (LSE) {
       float2* red = reinterpret_cast<float2*>(extra + G::kRows);          // [WGN][BM]
-      const bool edge = n0 + 64 > g.V;
       float flip = 1.f;
       if (g.c2 < 0.f) {                              // the largest logit is the smallest product
         flip = -1.f;
@@ -489,7 +490,7 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
           for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int q = 0; q < 16; ++q)
-              if (n0 + j * 32 + 8 * (q >> 2) + 4 * half + (q & 3) >= g.V) acc[i][j][q] = -INFINITY;
+              if (j * 32 + 8 * (q >> 2) + 4 * half + (q & 3) >= live) acc[i][j][q] = -INFINITY;
         // (never 0, so that masked columns stay -infinity under it)
         const float c2 = fmaxf(flip * (F16 ? rows[wm * G::WTM + i * 32 + fr] : g.c2), 1.2e-38f);
         float m = -INFINITY;
@@ -553,7 +554,6 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
         if (row < g.M) g.part[(int64_t)cur.bn * g.M + row] = make_float2(m, sum);
       }
     } else if constexpr (EPI == EPI_DZ) {
-      const bool edge = n0 + 64 > g.V;
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const float a = rows[wm * G::WTM + i * 32 + fr];
@@ -562,17 +562,16 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            float v = a * __builtin_amdgcn_exp2f(fmaf(acc[i][j][q], c2, -l));
-            if (edge && n0 + j * 32 + 8 * (q >> 2) + 4 * half + (q & 3) >= g.V) v = 0.f;
-            acc[i][j][q] = v;
-          }
-        // rows without weight give zeros whatever their logits are
-        if (__any(a == 0.f))
+          for (int q = 0; q < 16; ++q)
+            acc[i][j][q] = a * __builtin_amdgcn_exp2f(fmaf(acc[i][j][q], c2, -l));
+        // columns behind the last row of T, and rows without weight, give zeros
+        // whatever their logits are
+        if (edge || __any(a == 0.f))
 #pragma unroll
           for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int q = 0; q < 16; ++q) acc[i][j][q] = a == 0.f ? 0.f : acc[i][j][q];
+            for (int q = 0; q < 16; ++q)
+              if (a == 0.f || j * 32 + 8 * (q >> 2) + 4 * half + (q & 3) >= live) acc[i][j][q] = 0.f;
 #pragma unroll
         for (int p = 0; p < (F16 ? 2 : 1); ++p) {
           if (i + p > 0) wave_sync();
@@ -600,7 +599,7 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
               const uint4 v = *reinterpret_cast<const uint4*>(patch + r * 128 + ((c ^ (r & 7)) * 16));
               const int64_t row = m0 + i * 32 + r;
               if (row < g.Mpad)
-                *reinterpret_cast<uint4*>(g.dz + p * g.dz_plane + row * g.ldz + n0 + c * 8) = v;
+                store16<true>(g.dz + p * g.dz_plane + row * g.ldz + n0 + c * 8, v.x, v.y, v.z, v.w);
             }
           }
         }
