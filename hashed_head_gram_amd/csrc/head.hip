@@ -485,12 +485,15 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
       }
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        if (edge)
+        if (edge) {
+          int past = live - 4 * half;
+          asm volatile("" : "+v"(past));             // compared here, not held in masks all along
 #pragma unroll
           for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int q = 0; q < 16; ++q)
-              if (j * 32 + 8 * (q >> 2) + 4 * half + (q & 3) >= live) acc[i][j][q] = -INFINITY;
+              if (j * 32 + 8 * (q >> 2) + (q & 3) >= past) acc[i][j][q] = -INFINITY;
+        }
         // (never 0, so that masked columns stay -infinity under it)
         const float c2 = fmaxf(flip * (F16 ? rows[wm * G::WTM + i * 32 + fr] : g.c2), 1.2e-38f);
         float m = -INFINITY;
@@ -566,12 +569,15 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
             acc[i][j][q] = a * __builtin_amdgcn_exp2f(fmaf(acc[i][j][q], c2, -l));
         // columns behind the last row of T, and rows without weight, give zeros
         // whatever their logits are
-        if (edge || __any(a == 0.f))
+        if (edge || __any(a == 0.f)) {
+          int past = a == 0.f ? 0 : live - 4 * half;
+          asm volatile("" : "+v"(past));             // compared here, not held in masks all along
 #pragma unroll
           for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int q = 0; q < 16; ++q)
-              if (a == 0.f || j * 32 + 8 * (q >> 2) + 4 * half + (q & 3) >= live) acc[i][j][q] = 0.f;
+              if (j * 32 + 8 * (q >> 2) + (q & 3) >= past) acc[i][j][q] = 0.f;
+        }
 #pragma unroll
         for (int p = 0; p < (F16 ? 2 : 1); ++p) {
           if (i + p > 0) wave_sync();
