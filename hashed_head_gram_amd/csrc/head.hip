@@ -1726,6 +1726,26 @@ hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* works
   return hipGetLastError();
 }
 
+// Time until na tiles of length la, then nb of length lb <= la, have run on m
+// units, each taking the next tile as it gets free.
+static double makespan(int64_t na, double la, int64_t nb, double lb, int m) {
+  const int64_t full = na / m, rest = na % m;
+  const double t0 = full * la, t1 = t0 + (rest ? la : 0);
+  if (nb == 0) return t1;
+  // m - rest units are free from t0 on, the others from t1
+  const int64_t early = lb > 0 && rest ? (int64_t)((t1 - t0) / lb) : 0;
+  const int64_t before = (m - rest) * early;
+  if (rest && nb <= before) return t1;
+  const int64_t left = nb - before;
+  const double te = t0 + early * lb;                 // the early units' next start
+  if (!rest) return t0 + (double)((left + m - 1) / m) * lb;
+  const int64_t rounds = left / m, more = left % m;
+  if (more == 0) return t1 + rounds * lb;
+  return more <= m - rest ? (te + (rounds + 1) * lb > t1 + rounds * lb ? te + (rounds + 1) * lb
+                                                                     : t1 + rounds * lb)
+                          : t1 + (rounds + 1) * lb;
+}
+
 // The products of a piece: both in one launch; where their tiles are few, K is
 // split and a second launch joins the splits.
 static hipError_t launch_grads(TileArgs tw, TileArgs th, float* split, hipStream_t s) {
@@ -1741,24 +1761,43 @@ static hipError_t launch_grads(TileArgs tw, TileArgs th, float* split, hipStream
   };
   tw.splits = th.splits = 1;
   const int64_t nw = w ? tiles(tw) : 0, nh = h ? tiles(th) : 0;
-  // A tile's chain of slots is not to take longer than the whole launch spread
-  // over the chip (256 large tiles at once, 512 small ones): longer ones share
-  // their K, down to 8 slots a tile.
+  // K's splits: tiles run longest first on 256 compute units (two small ones to
+  // each); splitting evens out their end, but writes and reads a result more.
+  // Times in us, from a large tile's 0.95 us a slot and 5 MB/us for partial results.
   const int at_once = big ? kCUs : 2 * kCUs;
-  const int64_t fair = ((w ? nw * tw.slots : 0) + (h ? nh * th.slots : 0)) / at_once + 1;
+  const double slot = (big ? 0.95 : 0.48) * tw.nseg;
+  const int64_t tile_bytes = (int64_t)b * b * 4;
+  int kw = 1, kh = 1;
+  double best = 1e30;
+  auto splits_up_to = [&](const TileArgs& t, int64_t n) {
+    int64_t most = (int64_t)t.slots * t.nseg / 8;    // 8 slots a tile at least
+    if (most > t.slots / 2) most = t.slots / 2;
+    if (most > at_once / (n ? n : 1)) most = at_once / (n ? n : 1);
+    return n == 0 || most < 1 ? 1 : (int)most;
+  };
+  // at most at_once split tiles in all: what the workspace holds
+  for (int i = 1; i <= splits_up_to(tw, nw); i = i < 16 ? i + 1 : i * 5 / 4)
+    for (int j = 1; j <= splits_up_to(th, nh); j = j < 16 ? j + 1 : j * 5 / 4) {
+      const int64_t split_tiles = (i > 1 ? nw * i : 0) + (j > 1 ? nh * j : 0);
+      if (split_tiles > at_once) continue;
+      const double lw = nw ? (double)tw.slots / i : 0, lh = nh ? (double)th.slots / j : 0;
+      double t = slot * (lw > lh ? makespan(nw * i, lw, nh * j, lh, at_once)
+                                 : makespan(nh * j, lh, nw * i, lw, at_once));
+      if (split_tiles) t += 6 + (double)split_tiles * tile_bytes * 2 / 5e6;
+      if (t < best) {
+        best = t;
+        kw = i;
+        kh = j;
+      }
+    }
   SumArgs sums[2] = {};
   int64_t used = 0;
-  auto share = [&](TileArgs& t, int64_t n, SumArgs& sa) {
-    if (n == 0) return;
-    int64_t k = t.slots / fair;                      // n k <= at_once
-    const int64_t most = (int64_t)t.slots * t.nseg / 8;
-    if (k > most) k = most;
-    if (k > t.slots / 2) k = t.slots / 2;
+  auto share = [&](TileArgs& t, int k, SumArgs& sa) {
     if (k < 2) return;
-    sa = SumArgs{split + used, (int)k, 0, (int64_t)t.nbn * b, t.M, t.V, t.prev, t.ld_prev,
+    sa = SumArgs{split + used, k, 0, (int64_t)t.nbn * b, t.M, t.V, t.prev, t.ld_prev,
                  t.out, t.ld_out, t.out_bf16};
     sa.stride = (int64_t)t.nbm * b * sa.ld_part;
-    t.splits = (int)k;
+    t.splits = k;
     t.out = split + used;
     t.ld_out = sa.ld_part;
     t.split_out = sa.stride;
@@ -1766,8 +1805,8 @@ static hipError_t launch_grads(TileArgs tw, TileArgs th, float* split, hipStream
     t.prev = nullptr;
     used += k * sa.stride;
   };
-  share(tw, nw, sums[0]);
-  share(th, nh, sums[1]);
+  share(tw, kw, sums[0]);
+  share(th, kh, sums[1]);
   const uint32_t gw = (uint32_t)(nw * tw.splits), gh = (uint32_t)(nh * th.splits);
   if (big)
     hipLaunchKernelGGL((head_grad_kernel<256, 256, 2, 4>), dim3(gw + gh), dim3(512), 0, s, tw, th, gw,
