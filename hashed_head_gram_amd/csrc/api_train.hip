@@ -72,7 +72,7 @@ int check_head_call(const pg::HeadArgs& g, const pg_table* table, int32_t d, flo
   if (!float_dtype(g.dtype)) return PG_EINVAL;
   if (g.dtype != table->dtype) return PG_EUNSUPPORTED;
   if (!isfinite(g.scale) || !(temperature > 0.f) || !isfinite(temperature) ||
-      !isfinite(1.f / temperature))
+      !isfinite(1.f / temperature) || !isfinite(g.scale / temperature * 1.4427f))
     return PG_EINVAL;
   if (g.ld_h < d) return PG_EINVAL;
   if (g.n == 0) return PG_OK;

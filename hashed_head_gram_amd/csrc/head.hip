@@ -1584,7 +1584,7 @@ HeadPlan head_plan(int64_t n, int d, int64_t V, int32_t dtype, int k, bool backw
     p.off_starts = take(tiles_of(n, 128) * (tiles_of(V, 128) + 1) * 4);
   } else {
     // dz of a piece: at most 2^29 elements (1 GiB) of both halves
-    p.rows = pad(n, 128);
+    p.rows = pad(n < 1 ? 1 : n, 128);
     if (p.rows > 32768) p.rows = 32768;
     const int64_t elems = ((int64_t)1 << 29) / p.planes;
     int64_t c = elems / p.rows / 256 * 256;
@@ -1831,9 +1831,9 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
   auto* dz = reinterpret_cast<uint16_t*>(ws + p.off_dz);
   if (g.n == 0) {
     const int64_t count = g.V * g.d * elt_size(g.dw_dtype) / 2;
-    if (g.dw && !g.accumulate)
-      hipLaunchKernelGGL(head_zero_kernel, dim3(blocks_for(count, 8192)), dim3(256), 0, s,
-                         static_cast<uint16_t*>(g.dw), count);
+    if (!g.dw || g.accumulate) return hipSuccess;
+    hipLaunchKernelGGL(head_zero_kernel, dim3(blocks_for(count, 8192)), dim3(256), 0, s,
+                       static_cast<uint16_t*>(g.dw), count);
     return hipGetLastError();
   }
   const bool w_here = in_place(g.dtype, g.d, g.d, g.table);

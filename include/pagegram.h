@@ -750,7 +750,7 @@ PG_API int pg_orthogonalize(const void* G, int32_t dtype, int64_t n_mat,
  *   table   PG_F32 or PG_BF16 data [V][d] of the same type as h (NF4 or
  *           another type: PG_EUNSUPPORTED); 1 <= V < 2^31 - 1, and tiles of
  *           128 x 128 fewer than 2^31 (PG_ERANGE)
- *   scale   finite
+ *   scale   finite (divided by the temperature too)
  * Logits, statistics and losses are fp32. fp32 operands are multiplied as
  * three bf16 planes (24 bits), sums in fp32. For bf16 operands dz is rounded
  * to bf16 once, scaled, before its two products, whose sums are fp32: dh and
