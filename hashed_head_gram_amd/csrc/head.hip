@@ -463,7 +463,7 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
     uint8_t* patch;                                  // 4 KiB of the wave's own
     {
       constexpr int inA = G::kA / 4096 < NW ? G::kA / 4096 : NW;
-      if constexpr (!LSE) static_assert(inA + G::kB / 4096 >= NW, "patches");
+      static_assert(inA + G::kB / 4096 >= NW, "patches");
       patch = wave < inA ? smem + free_slot * G::kA + wave * 4096
                          : smemB + free_slot * G::kB + (wave - inA) * 4096;
     }
@@ -518,30 +518,44 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
         const uint32_t* src = picks_of(cur, count);
         const auto* near = reinterpret_cast<const uint32_t*>(extra + G::kRows + G::kRed) +
                            (jt & 1) * kPicks;
+        // block by block through the wave's scratch, 64 entries at a time
+        auto entry = [&](int x) -> uint32_t {
+          const uint32_t e = x + lane >= count ? 0xFFFFFFFFu
+                             : x < kPicks ? near[x + lane] : src[x + lane];
+          return (e & 255) / G::WTM == (uint32_t)wm && ((e >> 8) & 255) / 64 == (uint32_t)wn
+                     ? e : 0xFFFFFFFFu;
+        };
+        uint64_t blocks = 0;                         // of this wave's, those with entries
         for (int x = 0; x < count; x += 64) {
-          const uint32_t e = x + lane >= count ? 0xFFFFFFFFu : x < kPicks ? near[x + lane] : src[x + lane];
-          const int row = e & 255, col = (e >> 8) & 255;
-          uint64_t mine = __ballot(e != 0xFFFFFFFFu && row / G::WTM == wm && col / 64 == wn);
-          while (mine) {                             // one entry of this wave's part at a time
-            const int from = __ffsll((unsigned long long)mine) - 1;
-            mine &= mine - 1;
-            const uint32_t p = __builtin_amdgcn_readlane(e, from);
-            const int pr = p & 255, pc = (p >> 8) & 63;
-            const int at = (pr % G::WTM / 32 * FN + pc / 32) * 16 + pc % 32 / 8 * 4 + pc % 4;
-            float z = 0.f;
+          const uint32_t e = entry(x);
+          const int at = (int)(e & 255) % G::WTM / 32 * FN + (int)((e >> 8) & 63) / 32;
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-              for (int j = 0; j < FN; ++j)
-                if (at / 16 == i * FN + j)           // uniform
-#pragma unroll
-                  for (int q = 0; q < 16; ++q)
-                    if (at % 16 == q) z = acc[i][j][q];
-            if (lane == (pr & 31) + 32 * ((pc >> 2) & 1))
-              g.logits[((int64_t)cur.bm * BM + pr) * g.k + (p >> 16)] =
-                  z * (flip * (F16 ? rows[pr] : g.c2)) * g.zf;
-          }
+          for (int t = 0; t < FM * FN; ++t)
+            if (__any(e != 0xFFFFFFFFu && at == t)) blocks |= 1ull << t;
         }
+        float* z = reinterpret_cast<float*>(patch);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            if (blocks >> (i * FN + j) & 1) {
+              const float f = flip * (F16 ? rows[wm * G::WTM + i * 32 + fr] : g.c2) * g.zf;
+              wave_sync();
+              // 16-byte chunk c of row r at c ^ r % 8
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<float4*>(z + fr * 32 + (((2 * q + half) ^ (fr & 7)) * 4)) =
+                    make_float4(acc[i][j][4 * q] * f, acc[i][j][4 * q + 1] * f,
+                                acc[i][j][4 * q + 2] * f, acc[i][j][4 * q + 3] * f);
+              wave_sync();
+              for (int x = 0; x < count; x += 64) {
+                const uint32_t e = entry(x);
+                const int r = e & 255, c = (e >> 8) & 63;
+                if (e != 0xFFFFFFFFu && r % G::WTM / 32 == i && c / 32 == j)
+                  g.logits[((int64_t)cur.bm * BM + r) * g.k + (e >> 16)] =
+                      z[(r & 31) * 32 + ((((c & 31) >> 2) ^ (r & 7)) * 4) + (c & 3)];
+              }
+            }
       }
       wait_lds();
       barrier();
@@ -749,6 +763,45 @@ struct FewArgs {
   float2* part;            // [tiles of 128 rows][n]
 };
 
+// A fragment of 8 elements as bf16 (fp32: its three planes).
+template <typename T>
+__device__ __forceinline__ void planes_of(const Raw8<T>& v, uint4 (&f)[sizeof(T) == 4 ? 3 : 1]) {
+  if constexpr (sizeof(T) == 4) {
+    float x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) x[u] = v.v[u];
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      uint32_t w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        w[u] = pack2_bf16(x[2 * u], x[2 * u + 1]);
+        x[2 * u] -= __uint_as_float(w[u] << 16);
+        x[2 * u + 1] -= __uint_as_float(w[u] & 0xFFFF0000u);
+      }
+      f[p] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+    f[0] = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+  }
+}
+// acc += w h of two fragments' planes, small products first.
+template <int P>
+__device__ __forceinline__ void mma_planes(const uint4 (&w)[P], const uint4 (&h)[P], f32x4_t& acc) {
+  auto mma = [&](int a, int b) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w[a]),
+                                                  __builtin_bit_cast(bf16x8_t, h[b]), acc, 0, 0, 0);
+  };
+  if constexpr (P == 3) {
+    mma(2, 0);
+    mma(0, 2);
+    mma(1, 1);
+    mma(1, 0);
+    mma(0, 1);
+  }
+  mma(0, 0);
+}
+
 template <typename T, int TB>
 __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g) {
   constexpr bool F32 = sizeof(T) == 4;
@@ -786,27 +839,6 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g) {
     hp[u] = static_cast<const T*>(g.h) + (x0 + x < g.n ? x0 + x : g.n - 1) * g.ld + hc[u];
   }
   f32x4_t acc[TB][2] = {};
-  // a fragment's planes (bf16: itself)
-  auto planes = [](const Raw8<T>& v, uint4 (&f)[P]) {
-    if constexpr (F32) {
-      float x[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) x[u] = v.v[u];
-#pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        uint32_t w[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          w[u] = pack2_bf16(x[2 * u], x[2 * u + 1]);
-          x[2 * u] -= __uint_as_float(w[u] << 16);
-          x[2 * u + 1] -= __uint_as_float(w[u] & 0xFFFF0000u);
-        }
-        f[p] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    } else {
-      f[0] = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
-    }
-  };
   Raw8<T> hr[HL], wr[2][ST][2];
   auto load = [&](int k, Raw8<T> (&w)[ST][2]) {
     const bool all = k + KC <= g.d;
@@ -826,7 +858,7 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g) {
       const int i = u * 256 + threadIdx.x;
       if (HL * 256 == CH || i < CH) {
         uint4 f[P];
-        planes(hr[u], f);
+        planes_of(hr[u], f);
 #pragma unroll
         for (int p = 0; p < P; ++p)
           *reinterpret_cast<uint4*>(hs[buf][p] + place(i / (KC / 8), i % (KC / 8))) = f[p];
@@ -838,7 +870,7 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g) {
     for (int s = 0; s < ST; ++s) {
       uint4 wf[2][P];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) planes(w[s][r], wf[r]);
+      for (int r = 0; r < 2; ++r) planes_of(w[s][r], wf[r]);
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
         uint4 hf[P];
@@ -846,21 +878,7 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g) {
         for (int p = 0; p < P; ++p)
           hf[p] = *reinterpret_cast<const uint4*>(hs[buf][p] + place(t * 16 + fr, s * 4 + kq));
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          auto mma = [&](int a, int b) {
-            acc[t][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8_t, wf[r][a]), __builtin_bit_cast(bf16x8_t, hf[b]),
-                acc[t][r], 0, 0, 0);
-          };
-          if constexpr (F32) {
-            mma(2, 0);
-            mma(0, 2);
-            mma(1, 1);
-            mma(1, 0);
-            mma(0, 1);
-          }
-          mma(0, 0);
-        }
+        for (int r = 0; r < 2; ++r) mma_planes(wf[r], hf, acc[t][r]);
       }
     }
   };
@@ -918,6 +936,133 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g) {
     for (int w = 0; w < 4; ++w) s += red[w][x].y * __builtin_amdgcn_exp2f(red[w][x].x - ref);
     g.part[(int64_t)tile * g.n + x0 + x] = make_float2(m, s);
   }
+}
+
+// The same where the table is short too and blocks of 128 rows would leave most
+// of the chip idle: a block has 32 rows, its four waves share K and their sums
+// meet in LDS, so a chain of loads is a quarter as long. Fragments of the tokens
+// come straight from memory here. DZ: leaves dz (rows_pad rows, zeros behind the
+// tokens and behind the table) instead of maxima and sums.
+struct FewDz {
+  const float *a, *lse2;
+  uint16_t* dz;
+  int64_t ldz, plane;      // elements
+  int rows_pad;
+};
+
+template <typename T, int TB, bool DZ>
+__global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_few_split_kernel(FewArgs g, FewDz z) {
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int ST = F32 ? 2 : 4, P = F32 ? 3 : 1, KC = 32 * ST;
+  __shared__ f32x4_t join[4][TB * 2][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, fr = lane & 15, kq = lane >> 4;
+  const int64_t v0 = (int64_t)blockIdx.x * 32;
+  const T *wp[2], *hp[TB];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int64_t v = v0 + r * 16 + fr;
+    wp[r] = static_cast<const T*>(g.table) + (v < g.V ? v : g.V - 1) * g.d + kq * 8;
+  }
+#pragma unroll
+  for (int t = 0; t < TB; ++t) {
+    const int64_t x = t * 16 + fr;
+    hp[t] = static_cast<const T*>(g.h) + (x < g.n ? x : g.n - 1) * g.ld + kq * 8;
+  }
+  f32x4_t acc[TB][2] = {};
+  struct Step {
+    Raw8<T> w[2], h[TB];
+  };
+  auto load = [&](int k, Step (&to)[ST]) {
+    const bool all = k + KC <= g.d;
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      const int left = all ? 8 : g.d - k - s * 32 - kq * 8;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) to[s].w[r] = load8(wp[r] + k + s * 32, left);
+#pragma unroll
+      for (int t = 0; t < TB; ++t) to[s].h[t] = load8(hp[t] + k + s * 32, left);
+    }
+  };
+  auto multiply = [&](const Step (&x)[ST]) {
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      uint4 wf[2][P];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) planes_of(x[s].w[r], wf[r]);
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        uint4 hf[P];
+        planes_of(x[s].h[t], hf);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) mma_planes(wf[r], hf, acc[t][r]);
+      }
+    }
+  };
+  Step x[2][ST];
+  int k = wave * KC;
+  if (k < g.d) load(k, x[0]);
+  for (; k < g.d; k += 8 * KC) {
+    if (k + 4 * KC < g.d) load(k + 4 * KC, x[1]);
+    multiply(x[0]);
+    if (k + 4 * KC < g.d) {
+      if (k + 8 * KC < g.d) load(k + 8 * KC, x[0]);
+      multiply(x[1]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TB; ++t)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) join[wave][t * 2 + r][lane] = acc[t][r];
+  __syncthreads();
+  // wave t has token block t from here on: rows 16 r + 4 kq + q, token 16 t + fr
+  if (wave < TB) {
+    const int64_t tok = wave * 16 + fr;
+    float v[2][4], m = -INFINITY;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const f32x4_t sum = (join[0][wave * 2 + r][lane] + join[1][wave * 2 + r][lane]) +
+                          (join[2][wave * 2 + r][lane] + join[3][wave * 2 + r][lane]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[r][q] = v0 + r * 16 + 4 * kq + q < g.V ? sum[q] * g.c2 : -INFINITY;
+        m = fmaxf(m, v[r][q]);
+      }
+    }
+    if constexpr (!DZ) {
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
+      const float ref = m == -INFINITY ? 0.f : m;
+      float s = 0.f;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s += __builtin_amdgcn_exp2f(v[r][q] - ref);
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
+      if (kq == 0 && tok < g.n) g.part[(int64_t)blockIdx.x * g.n + tok] = make_float2(m, s);
+    } else {
+      const float a = tok < g.n ? z.a[tok] : 0.f, l = tok < g.n ? z.lse2[tok] : 0.f;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float f[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) f[q] = a == 0.f ? 0.f : a * __builtin_amdgcn_exp2f(v[r][q] - l);
+        const uint2 w = make_uint2(pack2_f16(f[0], f[1]), pack2_f16(f[2], f[3]));
+        uint16_t* to = z.dz + tok * z.ldz + v0 + r * 16 + 4 * kq;
+        *reinterpret_cast<uint2*>(to) = w;
+        if constexpr (F32)
+          *reinterpret_cast<uint2*>(to + z.plane) =
+              make_uint2(pack2_f16(f[0] - lo_f16(w.x), f[1] - hi_f16(w.x)),
+                         pack2_f16(f[2] - lo_f16(w.y), f[3] - hi_f16(w.y)));
+      }
+    }
+  }
+  if constexpr (DZ)                                  // rows behind the token blocks
+    for (int i = threadIdx.x; i < (z.rows_pad - 16 * TB) * 8; i += 256) {
+      uint16_t* to = z.dz + (16 * TB + (i >> 3)) * z.ldz + v0 + (i & 7) * 4;
+      *reinterpret_cast<uint2*>(to) = make_uint2(0, 0);
+      if constexpr (F32) *reinterpret_cast<uint2*>(to + z.plane) = make_uint2(0, 0);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -1218,6 +1363,9 @@ __device__ __forceinline__ void put_raw(const uint16_t* src, int d, int c, bool 
 // tokens up to which the table's reading is all that counts: read in place, or
 // where tiles would need a copy of it
 constexpr int kFew = 64, kFewCopied = 256;
+// and rows of the table up to which they are read 32 a block, one block a compute
+// unit (2048 wide, 32 tokens: 15 us for 23 at 8,192 rows, 26 for 24 at 16,384)
+constexpr int64_t kFewShort = 8192;
 constexpr int kScanBlocks = 512;
 constexpr int kRowBlocks = 512;           // most blocks over rows, four waves each
 
@@ -1470,31 +1618,52 @@ struct SumArgs {
   int out_bf16;
 };
 __global__ __launch_bounds__(256) void head_sum_kernel(SumArgs a, SumArgs b, int na) {
+  // 32 groups of four columns a block; eight threads a group take every eighth
+  // split (one thread took 66 us for 180 splits of 32 x 59)
+  __shared__ float4 sh[8][32];
   const bool first = (int)blockIdx.x < na;
   const SumArgs& g = first ? a : b;
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int64_t per = (g.N + 3) / 4, total = g.M * per;
-  const int64_t step = (int64_t)(first ? na : (int)gridDim.x - na) * 256;
-  for (int64_t i = ((int64_t)blockIdx.x - (first ? 0 : na)) * 256 + threadIdx.x; i < total; i += step) {
+  const int64_t step = (int64_t)(first ? na : (int)gridDim.x - na) * 32;
+  for (int64_t i0 = ((int64_t)blockIdx.x - (first ? 0 : na)) * 32; i0 < total; i0 += step) {
+    const int64_t i = i0 + x;
     const int64_t row = i / per, col = (i - row * per) * 4;
-    const float* p = g.part + row * g.ld_part + col;     // rows of whole tiles
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int s = 0; s < g.splits; ++s) {
-      const float4 x = *reinterpret_cast<const float4*>(p + s * g.stride);
-      v[0] += x.x;
-      v[1] += x.y;
-      v[2] += x.z;
-      v[3] += x.w;
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (col + u < g.N) {
-        if (g.prev) v[u] += g.prev[row * g.ld_prev + col + u];
-        if (g.out_bf16)
-          static_cast<uint16_t*>(g.out)[row * g.ld_out + col + u] = (uint16_t)pack2_bf16(v[u], 0.f);
-        else
-          static_cast<float*>(g.out)[row * g.ld_out + col + u] = v[u];
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < total) {
+      const float* p = g.part + row * g.ld_part + col;   // rows of whole tiles
+#pragma unroll 4
+      for (int s = y; s < g.splits; s += 8) {
+        const float4 t = *reinterpret_cast<const float4*>(p + s * g.stride);
+        v.x += t.x;
+        v.y += t.y;
+        v.z += t.z;
+        v.w += t.w;
       }
+    }
+    sh[y][x] = v;
+    __syncthreads();
+    if (y == 0 && i < total) {
+#pragma unroll
+      for (int s = 1; s < 8; ++s) {
+        const float4 t = sh[s][x];
+        v.x += t.x;
+        v.y += t.y;
+        v.z += t.z;
+        v.w += t.w;
+      }
+      const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (col + u < g.N) {
+          const float r = g.prev ? f[u] + g.prev[row * g.ld_prev + col + u] : f[u];
+          if (g.out_bf16)
+            static_cast<uint16_t*>(g.out)[row * g.ld_out + col + u] = (uint16_t)pack2_bf16(r, 0.f);
+          else
+            static_cast<float*>(g.out)[row * g.ld_out + col + u] = r;
+        }
+    }
+    __syncthreads();
   }
 }
 
@@ -1578,7 +1747,9 @@ HeadPlan head_plan(int64_t n, int d, int64_t V, int32_t dtype, int k, bool backw
     p.off_rowf = take(pad(n, 256) * 4);
     p.off_hz = take(n * row);
     p.off_wz = take(p.cols * row);
-    p.off_part = take((V + 127) / 128 * n * 8);
+    const int64_t few = tiles_of(V < kFewShort ? V : kFewShort, 32) * (n < kFew ? n : kFew);
+    const int64_t parts = tiles_of(V, 128) * n;
+    p.off_part = take((parts > few ? parts : few) * 8);
     // entries by tile: whole row tiles, and room for a load behind the last
     p.off_list = take((pad(n, 256) * k + kPicks) * 4);
     p.off_starts = take(tiles_of(n, 128) * (tiles_of(V, 128) + 1) * 4);
@@ -1632,6 +1803,16 @@ hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* works
     const int groups = (int)tiles_of(g.n, 64);
     const FewArgs f{g.h, g.table, g.ld_h, g.n, g.V, g.d, groups, t.c2,
                     reinterpret_cast<float2*>(ws + p.off_part)};
+    if (groups == 1 && g.V <= kFewShort) {
+      parts = tiles_of(g.V, 32);
+      auto* kernel = f32 ? (g.n <= 16   ? head_few_split_kernel<float, 1, false>
+                            : g.n <= 32 ? head_few_split_kernel<float, 2, false>
+                                        : head_few_split_kernel<float, 4, false>)
+                         : (g.n <= 16   ? head_few_split_kernel<uint16_t, 1, false>
+                            : g.n <= 32 ? head_few_split_kernel<uint16_t, 2, false>
+                                        : head_few_split_kernel<uint16_t, 4, false>);
+      hipLaunchKernelGGL(kernel, dim3((unsigned)parts), dim3(256), 0, s, f, FewDz{});
+    } else {
     parts = tiles_of(g.V, 128);
     const int64_t blocks = groups == 1 ? parts : pad(parts, 8) * groups;
     auto* kernel = f32 ? (g.n <= 16 ? head_few_kernel<float, 1> : g.n <= 32 ? head_few_kernel<float, 2>
@@ -1640,6 +1821,7 @@ hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* works
                           : g.n <= 32 ? head_few_kernel<uint16_t, 2>
                                       : head_few_kernel<uint16_t, 4>);
     hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, s, f);
+    }
   } else {
     RowArgs r{};
     r.h = g.h;
@@ -1750,46 +1932,50 @@ static double makespan(int64_t na, double la, int64_t nb, double lb, int m) {
 // split and a second launch joins the splits.
 static hipError_t launch_grads(TileArgs tw, TileArgs th, float* split, hipStream_t s) {
   const bool w = tw.out != nullptr, h = th.out != nullptr;
-  const int64_t big_n = (w ? tiles_of(tw.M, 256) * tiles_of(tw.V, 256) : 0) +
-                        (h ? tiles_of(th.M, 256) * tiles_of(th.V, 256) : 0);
-  const bool big = big_n >= kCUs / 2;
+  tw.splits = th.splits = 1;
+  // Tile size and K's splits: tiles run longest first, a large one to a compute
+  // unit or two small ones; splitting evens out their end, but writes and reads a
+  // result more. Times in us: 0.95 a slot of a large tile, 0.6 of a small one
+  // (twice as many run at once), 5 MB/us for partial results.
+  double best = 1e30;
+  bool big = false;
+  int kw = 1, kh = 1;
+  for (int large = 0; large < 2; ++large) {
+    const int b = large ? 256 : 128, at_once = large ? kCUs : 2 * kCUs;
+    const double slot = (large ? 0.95 : 0.6) * tw.nseg;
+    const int64_t nw = w ? tiles_of(tw.M, b) * tiles_of(tw.V, b) : 0;
+    const int64_t nh = h ? tiles_of(th.M, b) * tiles_of(th.V, b) : 0;
+    auto splits_up_to = [&](const TileArgs& t, int64_t n) {
+      int64_t most = (int64_t)t.slots * t.nseg / 8;    // 8 slots a tile at least
+      if (most > t.slots / 2) most = t.slots / 2;
+      if (n == 0 || most > at_once / n) most = n == 0 ? 1 : at_once / n;
+      return most < 1 ? 1 : (int)most;
+    };
+    const int mw = splits_up_to(tw, nw), mh = splits_up_to(th, nh);
+    // at most at_once split tiles in all: what the workspace holds
+    for (int i = 1; i <= mw; i = i < 16 ? i + 1 : i * 5 / 4)
+      for (int j = 1; j <= mh; j = j < 16 ? j + 1 : j * 5 / 4) {
+        const int64_t split_tiles = (i > 1 ? nw * i : 0) + (j > 1 ? nh * j : 0);
+        if (split_tiles > at_once) continue;
+        const double lw = nw ? (double)tw.slots / i : 0, lh = nh ? (double)th.slots / j : 0;
+        double t = slot * (lw > lh ? makespan(nw * i, lw, nh * j, lh, at_once)
+                                   : makespan(nh * j, lh, nw * i, lw, at_once));
+        if (split_tiles) t += 6 + (double)split_tiles * b * b * 8 / 5e6;
+        if (t < best) {
+          best = t;
+          big = large;
+          kw = i;
+          kh = j;
+        }
+      }
+  }
   const int b = big ? 256 : 128;
   auto tiles = [&](TileArgs& t) {
     t.nbm = (int)tiles_of(t.M, b);
     t.nbn = (int)tiles_of(t.V, b);
     return (int64_t)t.nbm * t.nbn;
   };
-  tw.splits = th.splits = 1;
   const int64_t nw = w ? tiles(tw) : 0, nh = h ? tiles(th) : 0;
-  // K's splits: tiles run longest first on 256 compute units (two small ones to
-  // each); splitting evens out their end, but writes and reads a result more.
-  // Times in us, from a large tile's 0.95 us a slot and 5 MB/us for partial results.
-  const int at_once = big ? kCUs : 2 * kCUs;
-  const double slot = (big ? 0.95 : 0.48) * tw.nseg;
-  const int64_t tile_bytes = (int64_t)b * b * 4;
-  int kw = 1, kh = 1;
-  double best = 1e30;
-  auto splits_up_to = [&](const TileArgs& t, int64_t n) {
-    int64_t most = (int64_t)t.slots * t.nseg / 8;    // 8 slots a tile at least
-    if (most > t.slots / 2) most = t.slots / 2;
-    if (most > at_once / (n ? n : 1)) most = at_once / (n ? n : 1);
-    return n == 0 || most < 1 ? 1 : (int)most;
-  };
-  // at most at_once split tiles in all: what the workspace holds
-  for (int i = 1; i <= splits_up_to(tw, nw); i = i < 16 ? i + 1 : i * 5 / 4)
-    for (int j = 1; j <= splits_up_to(th, nh); j = j < 16 ? j + 1 : j * 5 / 4) {
-      const int64_t split_tiles = (i > 1 ? nw * i : 0) + (j > 1 ? nh * j : 0);
-      if (split_tiles > at_once) continue;
-      const double lw = nw ? (double)tw.slots / i : 0, lh = nh ? (double)th.slots / j : 0;
-      double t = slot * (lw > lh ? makespan(nw * i, lw, nh * j, lh, at_once)
-                                 : makespan(nh * j, lh, nw * i, lw, at_once));
-      if (split_tiles) t += 6 + (double)split_tiles * tile_bytes * 2 / 5e6;
-      if (t < best) {
-        best = t;
-        kw = i;
-        kh = j;
-      }
-    }
   SumArgs sums[2] = {};
   int64_t used = 0;
   auto share = [&](TileArgs& t, int k, SumArgs& sa) {
@@ -1814,8 +2000,8 @@ static hipError_t launch_grads(TileArgs tw, TileArgs th, float* split, hipStream
   else
     hipLaunchKernelGGL((head_grad_kernel<128, 128, 2, 2>), dim3(gw + gh), dim3(256), 0, s, tw, th, gw,
                        gh);
-  const int sw = sums[0].splits ? blocks_for(sums[0].M * ((sums[0].N + 3) / 4), 1024) : 0;
-  const int sh = sums[1].splits ? blocks_for(sums[1].M * ((sums[1].N + 3) / 4), 1024) : 0;
+  const int sw = sums[0].splits ? blocks_for(sums[0].M * ((sums[0].N + 3) / 4) * 8, 2048) : 0;
+  const int sh = sums[1].splits ? blocks_for(sums[1].M * ((sums[1].N + 3) / 4) * 8, 2048) : 0;
   if (sw + sh)
     hipLaunchKernelGGL(head_sum_kernel, dim3(sw + sh), dim3(256), 0, s, sums[0], sums[1], sw);
   return hipGetLastError();
@@ -1915,7 +2101,20 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
       t.dz_plane = plane;
       t.Mpad = rows;
       t.Vpad = cols;
-      hipError_t e = launch_tiles<EPI_DZ>(t, rows, cols, big_tiles(rows, cols), f32, s);
+      hipError_t e = hipSuccess;
+      if (n <= kFew && c <= kFewShort) {
+        const FewArgs f{r.h, w.src, g.ld_h, n, c, g.d, 1, r.c2, nullptr};
+        const FewDz z{r.a, r.lse2, dz, ldz, plane, (int)rows};
+        auto* kernel = f32 ? (n <= 16   ? head_few_split_kernel<float, 1, true>
+                              : n <= 32 ? head_few_split_kernel<float, 2, true>
+                                        : head_few_split_kernel<float, 4, true>)
+                           : (n <= 16   ? head_few_split_kernel<uint16_t, 1, true>
+                              : n <= 32 ? head_few_split_kernel<uint16_t, 2, true>
+                                        : head_few_split_kernel<uint16_t, 4, true>);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(cols / 32)), dim3(256), 0, s, f, z);
+      } else {
+        e = launch_tiles<EPI_DZ>(t, rows, cols, big_tiles(rows, cols), f32, s);
+      }
       if (e != hipSuccess) return e;
       hipLaunchKernelGGL(head_sparse_kernel, dim3(blocks_for(n * g.k, 8192)), dim3(256), 0, s,
                          r.sidx, r.sval, n, g.k, v0, c, dz, ldz, plane, p.planes);
