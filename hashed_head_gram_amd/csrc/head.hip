@@ -64,6 +64,19 @@ __device__ __forceinline__ float lo_f16(uint32_t w) {
 __device__ __forceinline__ float hi_f16(uint32_t w) {
   return (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16));
 }
+// The type that dz is held in: fp16, or bf16.
+template <bool F16>
+struct Half {
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    return F16 ? pack2_f16(a, b) : pack2_bf16(a, b);
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) {
+    return F16 ? lo_f16(w) : __uint_as_float(w << 16);
+  }
+  static __device__ __forceinline__ float hi(uint32_t w) {
+    return F16 ? hi_f16(w) : __uint_as_float(w & 0xFFFF0000u);
+  }
+};
 // x with 2^e: floor(log2 |x|); nothing for zeros, infinities and NaN.
 __device__ __forceinline__ int exponent_of(float x) {
   const float a = fabsf(x);
@@ -106,6 +119,10 @@ struct Side {
   int64_t ld;          // bytes between rows
   int64_t plane;       // bytes between planes
   int64_t outer;       // valid rows (plain) or columns, a multiple of 8 (transposed)
+  // transposed: slots of K from tail_slot on lie tail bytes further (elsewhere:
+  // the last rows of T, copied to whole slots); 0: none
+  int64_t tail;
+  int tail_slot;
 };
 
 struct TileArgs {
@@ -143,7 +160,8 @@ struct TileArgs {
   const int* all_exp;
 };
 
-enum { EPI_LSE, EPI_DZ, EPI_OUT, EPI_PICK };
+// EPI_DZB: dz as two bf16 halves, unplaced
+enum { EPI_LSE, EPI_DZ, EPI_OUT, EPI_PICK, EPI_DZB };
 constexpr int kPicks = 256;               // entries of a tile that wait in LDS
 
 // One side's walk over K: this wave's part of every slot.
@@ -285,14 +303,18 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
   WB wb;
   const uint8_t *a00 = nullptr, *b00 = nullptr;
   int seg_slots = 0, seg_at = 0, seg = 0;
+  constexpr bool kTail = EPI == EPI_OUT && !TA && TB;
+  int first_slot = 0;
   auto set_seg = [&] {
     wa.base = a00 + seg_a(seg) * g.A.plane;
     wb.base = b00 + seg_b(seg) * g.B.plane;
+    if (kTail && g.B.tail && first_slot >= g.B.tail_slot) wb.base += g.B.tail;
     seg_at = 0;
   };
   auto start_walk = [&](const Tile& t) {
     int s0;
     slot_range(t.split, s0, seg_slots);
+    first_slot = s0;
     wa.start(g.A, (int64_t)t.bm * BM, s0, wave, lane);
     wb.start(g.B, (int64_t)t.bn * BN, s0, wave, lane);
     a00 = wa.base;
@@ -305,14 +327,17 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
     wb.issue(lds0 + kRing * G::kA + ring * G::kB, wave);
     wa.base += wa.step;
     wb.base += wb.step;
-    if (++seg_at == seg_slots) {
+    ++seg_at;
+    if (kTail && first_slot + seg_at == g.B.tail_slot) wb.base += g.B.tail;
+    if (seg_at == seg_slots) {
       ++seg;
       if (seg < kSegs) set_seg();
     }
   };
   // a tile's row vectors into the half of its parity
   constexpr bool LSE = EPI == EPI_LSE || EPI == EPI_PICK;
-  constexpr int NV = (EPI == EPI_DZ ? 2 : 0) + (EPI != EPI_OUT && F16 ? 1 : 0);
+  constexpr bool DZ = EPI == EPI_DZ || EPI == EPI_DZB;
+  constexpr int NV = (DZ ? 2 : 0) + (EPI != EPI_OUT && F16 ? 1 : 0);
   auto picks_of = [&](const Tile& t, int& count) -> const uint32_t* {
     const int* s = g.starts + (int64_t)t.bm * (g.tiles + 1) + g.tile0 + t.bn;
     const int a = __builtin_amdgcn_readfirstlane(s[0]);
@@ -570,7 +595,7 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
         const int64_t row = (int64_t)cur.bm * BM + r;
         if (row < g.M) g.part[(int64_t)cur.bn * g.M + row] = make_float2(m, sum);
       }
-    } else if constexpr (EPI == EPI_DZ) {
+    } else if constexpr (DZ) {
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const float a = rows[wm * G::WTM + i * 32 + fr];
@@ -593,20 +618,21 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
               if (j * 32 + 8 * (q >> 2) + (q & 3) >= past) acc[i][j][q] = 0.f;
         }
 #pragma unroll
-        for (int p = 0; p < (F16 ? 2 : 1); ++p) {
+        for (int p = 0; p < (F16 || EPI == EPI_DZB ? 2 : 1); ++p) {
           if (i + p > 0) wave_sync();
           // rows of 128 bytes, 16-byte chunk c of row r at c ^ r % 8
 #pragma unroll
           for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const uint32_t lo = pack2_f16(acc[i][j][4 * q], acc[i][j][4 * q + 1]);
-              const uint32_t hi = pack2_f16(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
-              if (F16) {                             // what the high half leaves
-                acc[i][j][4 * q] -= lo_f16(lo);
-                acc[i][j][4 * q + 1] -= hi_f16(lo);
-                acc[i][j][4 * q + 2] -= lo_f16(hi);
-                acc[i][j][4 * q + 3] -= hi_f16(hi);
+              using H = Half<EPI != EPI_DZB>;
+              const uint32_t lo = H::pack(acc[i][j][4 * q], acc[i][j][4 * q + 1]);
+              const uint32_t hi = H::pack(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+              if (F16 || EPI == EPI_DZB) {           // what the high half leaves
+                acc[i][j][4 * q] -= H::lo(lo);
+                acc[i][j][4 * q + 1] -= H::hi(lo);
+                acc[i][j][4 * q + 2] -= H::lo(hi);
+                acc[i][j][4 * q + 3] -= H::hi(hi);
               }
               *reinterpret_cast<uint2*>(patch + fr * 128 + (((j * 4 + q) ^ (fr & 7)) * 16) +
                                         half * 8) = make_uint2(lo, hi);
@@ -722,7 +748,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void head_tile_kernel(TileArgs g
 // Both gradients' products of a piece in one launch, a tile each: nw blocks of
 // dT = dz^T h (both operands transposed) and nh of dh = dz T, whichever has the
 // longer K first.
-template <int BM, int BN, int WGM, int WGN>
+template <bool F16, int BM, int BN, int WGM, int WGN>
 __global__ __launch_bounds__(64 * WGM * WGN, 2) void head_grad_kernel(TileArgs w, TileArgs h,
                                                                    uint32_t nw, uint32_t nh) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Geo<BM, BN, WGM, WGN>::kLds];
@@ -734,11 +760,11 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void head_grad_kernel(TileArgs w
   const uint32_t b = blockIdx.x;
   if (w_first ? b < nw : b >= nh) {
     const uint32_t id = one(w_first ? b : b - nh, nw);
-    walk_tiles<EPI_OUT, true, BM, BN, WGM, WGN, true, true>(
+    walk_tiles<EPI_OUT, F16, BM, BN, WGM, WGN, true, true>(
         w, smem, [&](int j) { return j ? 0xFFFFFFFFu : id; });
   } else {
     const uint32_t id = one(w_first ? b - nw : b, nh);
-    walk_tiles<EPI_OUT, true, BM, BN, WGM, WGN, false, true>(
+    walk_tiles<EPI_OUT, F16, BM, BN, WGM, WGN, false, true>(
         h, smem, [&](int j) { return j ? 0xFFFFFFFFu : id; });
   }
 }
@@ -950,7 +976,7 @@ struct FewDz {
   int rows_pad;
 };
 
-template <typename T, int TB, bool DZ>
+template <typename T, int TB, int DZ>
 __global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_few_split_kernel(FewArgs g, FewDz z) {
   constexpr bool F32 = sizeof(T) == 4;
   constexpr int ST = F32 ? 2 : 4, P = F32 ? 3 : 1, KC = 32 * ST;
@@ -1028,7 +1054,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_f
         m = fmaxf(m, v[r][q]);
       }
     }
-    if constexpr (!DZ) {
+    if constexpr (DZ == 0) {
       m = fmaxf(m, __shfl_xor(m, 16));
       m = fmaxf(m, __shfl_xor(m, 32));
       const float ref = m == -INFINITY ? 0.f : m;
@@ -1047,21 +1073,22 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_f
         float f[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) f[q] = a == 0.f ? 0.f : a * __builtin_amdgcn_exp2f(v[r][q] - l);
-        const uint2 w = make_uint2(pack2_f16(f[0], f[1]), pack2_f16(f[2], f[3]));
+        using H = Half<DZ == 1>;
+        const uint2 w = make_uint2(H::pack(f[0], f[1]), H::pack(f[2], f[3]));
         uint16_t* to = z.dz + tok * z.ldz + v0 + r * 16 + 4 * kq;
         *reinterpret_cast<uint2*>(to) = w;
-        if constexpr (F32)
+        if constexpr (F32 || DZ == 2)
           *reinterpret_cast<uint2*>(to + z.plane) =
-              make_uint2(pack2_f16(f[0] - lo_f16(w.x), f[1] - hi_f16(w.x)),
-                         pack2_f16(f[2] - lo_f16(w.y), f[3] - hi_f16(w.y)));
+              make_uint2(H::pack(f[0] - H::lo(w.x), f[1] - H::hi(w.x)),
+                         H::pack(f[2] - H::lo(w.y), f[3] - H::hi(w.y)));
       }
     }
   }
-  if constexpr (DZ)                                  // rows behind the token blocks
+  if constexpr (DZ != 0)                             // rows behind the token blocks
     for (int i = threadIdx.x; i < (z.rows_pad - 16 * TB) * 8; i += 256) {
       uint16_t* to = z.dz + (16 * TB + (i >> 3)) * z.ldz + v0 + (i & 7) * 4;
       *reinterpret_cast<uint2*>(to) = make_uint2(0, 0);
-      if constexpr (F32) *reinterpret_cast<uint2*>(to + z.plane) = make_uint2(0, 0);
+      if constexpr (F32 || DZ == 2) *reinterpret_cast<uint2*>(to + z.plane) = make_uint2(0, 0);
     }
 }
 
@@ -1366,6 +1393,10 @@ constexpr int kFew = 64, kFewCopied = 256;
 // and rows of the table up to which they are read 32 a block, one block a compute
 // unit (2048 wide, 32 tokens: 15 us for 23 at 8,192 rows, 26 for 24 at 16,384)
 constexpr int64_t kFewShort = 8192;
+// Tokens up to which bf16 tables are used as they are for dh too: dz is then two
+// bf16 halves (16 bits), two products for one, and the fp16 copies, three more
+// passes over the table, fall away. 65,536 rows of 2048, 8 tokens: WIDE_US.
+constexpr int kWide = 256;
 constexpr int kScanBlocks = 512;
 constexpr int kRowBlocks = 512;           // most blocks over rows, four waves each
 
@@ -1389,6 +1420,7 @@ struct RowArgs {
   int *part_h, *part_w;             // exponents by block: of 2^row_exp h, of T
   int *all_h, *all_w;               // what dT and dh undo: minus their placements
   int nparts_h, nparts_w;
+  int placed;                       // dz in fp16, placed by powers of two; 0: two bf16 halves
   uint16_t *hp, *hz;                // fp16 h for dT; h for the logits (NULL: read in place)
   float c2;
 };
@@ -1434,11 +1466,12 @@ __global__ __launch_bounds__(256) void head_stats_kernel(RowArgs g, int row_bloc
         const bool keep = !(a == 0.f && w == 0.f);
         if (keep) {
           const float bound = fabsf(a) + fabsf(w);
-          re = exponent_of(bound) - kTop;
-          if (exponent_of(bound) == kNone) re = 0;
-          for (int c = lane * 8; c < g.d; c += 512) e = max(e, exponent_of8(hr + c, g.d - c));
-          e = wave_imax(e);
-          if (e != kNone) top = max(top, e + re);
+          re = g.placed && exponent_of(bound) != kNone ? exponent_of(bound) - kTop : 0;
+          if (g.placed) {
+            for (int c = lane * 8; c < g.d; c += 512) e = max(e, exponent_of8(hr + c, g.d - c));
+            e = wave_imax(e);
+            if (e != kNone) top = max(top, e + re);
+          }
         }
         const int place = keep ? -re : 0;
         if (!g.teacher) {
@@ -1496,6 +1529,10 @@ __global__ __launch_bounds__(256) void head_stats_kernel(RowArgs g, int row_bloc
         g.lse2[row] = l2;
         g.row_exp[row] = re;
       }
+      if constexpr (sizeof(T) == 2)
+        if (!g.placed && row < g.rows_pad)           // all that dT needs of h: rows without weight are zeros
+          for (int c = lane * 8; c < g.dp; c += 512)
+            put_raw(row < g.n ? hr : static_cast<const T*>(g.h), g.d, c, re != kNone, g.hp + row * g.dp);
     }
   }
   top = wave_imax(top);
@@ -1592,16 +1629,17 @@ __global__ __launch_bounds__(256) void head_copy_kernel(RowArgs g, PieceArgs w, 
 __global__ __launch_bounds__(256) void head_sparse_kernel(const int32_t* sidx, const float* sval,
                                                           int64_t n, int k, int64_t v0, int64_t cols,
                                                           uint16_t* dz, int64_t ldz,
-                                                          int64_t plane, int planes) {
+                                                          int64_t plane, int planes, int f16) {
   const int64_t total = n * k;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t v = (int64_t)sidx[i] - v0;
     if (v < 0 || v >= cols) continue;
     const float x = sval[i];
     uint16_t* p = dz + i / k * ldz + v;
-    const uint32_t w = pack2_f16(x, 0.f);
+    const uint32_t w = f16 ? pack2_f16(x, 0.f) : pack2_bf16(x, 0.f);
     *p = (uint16_t)w;
-    if (planes > 1) p[plane] = (uint16_t)pack2_f16(x - lo_f16(w), 0.f);
+    const float left = x - (f16 ? lo_f16(w) : __uint_as_float(w << 16));
+    if (planes > 1) p[plane] = (uint16_t)(f16 ? pack2_f16(left, 0.f) : pack2_bf16(left, 0.f));
   }
 }
 
@@ -1700,14 +1738,12 @@ hipError_t launch_tiles(TileArgs& g, int64_t M, int64_t N, bool big, bool f16, h
   const int64_t total = (int64_t)g.nbm * g.nbn;
   const int64_t most = big ? kCUs : 2 * kCUs;
   const unsigned grid = (unsigned)(total < most ? total : most);
-  if (big && f16)
-    hipLaunchKernelGGL((head_tile_kernel<EPI, true, 256, 256, 2, 4>), dim3(grid), dim3(512), 0, s, g);
-  else if (big)
-    hipLaunchKernelGGL((head_tile_kernel<EPI, false, 256, 256, 2, 4>), dim3(grid), dim3(512), 0, s, g);
-  else if (f16)
-    hipLaunchKernelGGL((head_tile_kernel<EPI, true, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, s, g);
-  else
-    hipLaunchKernelGGL((head_tile_kernel<EPI, false, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, s, g);
+  constexpr bool H = EPI != EPI_DZB;                 // its dz is bf16, as its operands
+  auto* kernel = big ? (H && f16 ? head_tile_kernel<EPI, H, 256, 256, 2, 4>
+                                 : head_tile_kernel<EPI, false, 256, 256, 2, 4>)
+                     : (H && f16 ? head_tile_kernel<EPI, H, 128, 128, 2, 2>
+                                 : head_tile_kernel<EPI, false, 128, 128, 2, 2>);
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(big ? 512 : 256), 0, s, g);
   return hipGetLastError();
 }
 
@@ -1755,9 +1791,10 @@ HeadPlan head_plan(int64_t n, int d, int64_t V, int32_t dtype, int k, bool backw
     p.off_starts = take(tiles_of(n, 128) * (tiles_of(V, 128) + 1) * 4);
   } else {
     // dz of a piece: at most 2^29 elements (1 GiB) of both halves
+    const int halves = n <= kWide ? 2 : p.planes;
     p.rows = pad(n < 1 ? 1 : n, 128);
     if (p.rows > 32768) p.rows = 32768;
-    const int64_t elems = ((int64_t)1 << 29) / p.planes;
+    const int64_t elems = ((int64_t)1 << 29) / halves;
     int64_t c = elems / p.rows / 256 * 256;
     if (c > pad(V, 256)) c = pad(V, 256);
     const int64_t pieces = (V + c - 1) / c;
@@ -1772,8 +1809,9 @@ HeadPlan head_plan(int64_t n, int d, int64_t V, int32_t dtype, int k, bool backw
     p.off_h = take(p.rows * row);
     p.off_hz = take(p.rows * row);
     p.off_w = take(p.cols * row);
-    p.off_wz = p.planes == 1 && !(d % 32 == 0 && d >= 128) ? take(p.cols * row) : at;
-    p.off_dz = take(p.rows * p.cols * 2 * p.planes);
+    // bf16 rows that cannot be read in place: all, or the last ones
+    p.off_wz = p.planes == 2 ? at : take((d % 32 == 0 && d >= 128 ? 128 : p.cols) * row);
+    p.off_dz = take(p.rows * p.cols * 2 * halves);
     p.off_dh = take(p.rows * d * 4);
     p.off_dw = n > 32768 ? take(V * d * 4) : at;
     p.off_split = take((int64_t)kCUs * 256 * 256 * 4);   // most tiles at once
@@ -1805,12 +1843,12 @@ hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* works
                     reinterpret_cast<float2*>(ws + p.off_part)};
     if (groups == 1 && g.V <= kFewShort) {
       parts = tiles_of(g.V, 32);
-      auto* kernel = f32 ? (g.n <= 16   ? head_few_split_kernel<float, 1, false>
-                            : g.n <= 32 ? head_few_split_kernel<float, 2, false>
-                                        : head_few_split_kernel<float, 4, false>)
-                         : (g.n <= 16   ? head_few_split_kernel<uint16_t, 1, false>
-                            : g.n <= 32 ? head_few_split_kernel<uint16_t, 2, false>
-                                        : head_few_split_kernel<uint16_t, 4, false>);
+      auto* kernel = f32 ? (g.n <= 16   ? head_few_split_kernel<float, 1, 0>
+                            : g.n <= 32 ? head_few_split_kernel<float, 2, 0>
+                                        : head_few_split_kernel<float, 4, 0>)
+                         : (g.n <= 16   ? head_few_split_kernel<uint16_t, 1, 0>
+                            : g.n <= 32 ? head_few_split_kernel<uint16_t, 2, 0>
+                                        : head_few_split_kernel<uint16_t, 4, 0>);
       hipLaunchKernelGGL(kernel, dim3((unsigned)parts), dim3(256), 0, s, f, FewDz{});
     } else {
     parts = tiles_of(g.V, 128);
@@ -1930,7 +1968,7 @@ static double makespan(int64_t na, double la, int64_t nb, double lb, int m) {
 
 // The products of a piece: both in one launch; where their tiles are few, K is
 // split and a second launch joins the splits.
-static hipError_t launch_grads(TileArgs tw, TileArgs th, float* split, hipStream_t s) {
+static hipError_t launch_grads(TileArgs tw, TileArgs th, bool f16, float* split, hipStream_t s) {
   const bool w = tw.out != nullptr, h = th.out != nullptr;
   tw.splits = th.splits = 1;
   // Tile size and K's splits: tiles run longest first, a large one to a compute
@@ -1994,12 +2032,9 @@ static hipError_t launch_grads(TileArgs tw, TileArgs th, float* split, hipStream
   share(tw, kw, sums[0]);
   share(th, kh, sums[1]);
   const uint32_t gw = (uint32_t)(nw * tw.splits), gh = (uint32_t)(nh * th.splits);
-  if (big)
-    hipLaunchKernelGGL((head_grad_kernel<256, 256, 2, 4>), dim3(gw + gh), dim3(512), 0, s, tw, th, gw,
-                       gh);
-  else
-    hipLaunchKernelGGL((head_grad_kernel<128, 128, 2, 2>), dim3(gw + gh), dim3(256), 0, s, tw, th, gw,
-                       gh);
+  auto* kernel = big ? (f16 ? head_grad_kernel<true, 256, 256, 2, 4> : head_grad_kernel<false, 256, 256, 2, 4>)
+                     : (f16 ? head_grad_kernel<true, 128, 128, 2, 2> : head_grad_kernel<false, 128, 128, 2, 2>);
+  hipLaunchKernelGGL(kernel, dim3(gw + gh), dim3(big ? 512 : 256), 0, s, tw, th, gw, gh);
   const int sw = sums[0].splits ? blocks_for(sums[0].M * ((sums[0].N + 3) / 4) * 8, 2048) : 0;
   const int sh = sums[1].splits ? blocks_for(sums[1].M * ((sums[1].N + 3) / 4) * 8, 2048) : 0;
   if (sw + sh)
@@ -2013,7 +2048,8 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
   const int es = elt_size(g.dtype);
   const int64_t dp2 = (int64_t)p.dp * 2;
   const bool f32 = g.dtype == PG_F32;
-  const int nseg = f32 ? kSegs : 1;
+  const bool wide = !f32 && g.n <= kWide;
+  const int nseg = f32 ? kSegs : 1, nseg_grad = wide ? 2 : nseg;
   auto* dz = reinterpret_cast<uint16_t*>(ws + p.off_dz);
   if (g.n == 0) {
     const int64_t count = g.V * g.d * elt_size(g.dw_dtype) / 2;
@@ -2056,7 +2092,8 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
     r.part_h = r.part_w + kScanBlocks;
     r.all_h = r.part_h + kRowBlocks;
     r.all_w = r.all_h + 1;
-    r.nparts_w = blocks_for((g.V * g.d + 7) / 8, kScanBlocks);
+    r.placed = !wide;
+    r.nparts_w = wide ? 0 : blocks_for((g.V * g.d + 7) / 8, kScanBlocks);
     r.nparts_h = (int)(tiles_of(r.vec_pad, 4) < kRowBlocks ? tiles_of(r.vec_pad, 4) : kRowBlocks);
     r.hp = reinterpret_cast<uint16_t*>(ws + p.off_h);
     const bool h_here = in_place(g.dtype, g.d, g.ld_h, r.h);
@@ -2075,16 +2112,25 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
       const bool first = v0 == 0, last = v0 + c == g.V;
       PieceArgs w{};
       w.src = static_cast<const uint8_t*>(g.table) + v0 * g.d * es;
+      auto* wz = reinterpret_cast<uint16_t*>(ws + p.off_wz);
       w.rows = c;
       w.rows_pad = cols;
-      w.wp = reinterpret_cast<uint16_t*>(ws + p.off_w);
-      if (!f32 && !w_here) w.wz = reinterpret_cast<uint16_t*>(ws + p.off_wz);
-      launch_copy(f32, r, w, first, s);
+      if (!wide) w.wp = reinterpret_cast<uint16_t*>(ws + p.off_w);
+      if (!f32 && !w_here) w.wz = wz;
+      PieceArgs copies = w;
+      const int64_t odd = c % 128;
+      if (wide && w_here) {                          // only the last rows, to whole slots
+        copies.src = static_cast<const uint8_t*>(w.src) + (c - odd) * g.d * es;
+        copies.rows = odd;
+        copies.rows_pad = odd ? 128 : 0;
+        copies.wz = wz;
+      }
+      launch_copy(f32, r, copies, first && !wide, s);
       const int64_t ldz = cols, plane = rows * cols;
 
       TileArgs t{};
       t.A = h_here ? Side{static_cast<const uint8_t*>(r.h), g.ld_h * 2, 0, n}
-                   : Side{ws + p.off_hz, dp2, rows * dp2, n};
+                   : Side{ws + (wide ? p.off_h : p.off_hz), dp2, rows * dp2, n};
       t.B = f32 ? Side{ws + p.off_w, dp2, cols * dp2, c}
                 : w_here ? Side{static_cast<const uint8_t*>(w.src), (int64_t)g.d * 2, 0, c}
                          : Side{ws + p.off_wz, dp2, 0, c};
@@ -2105,29 +2151,31 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
       if (n <= kFew && c <= kFewShort) {
         const FewArgs f{r.h, w.src, g.ld_h, n, c, g.d, 1, r.c2, nullptr};
         const FewDz z{r.a, r.lse2, dz, ldz, plane, (int)rows};
-        auto* kernel = f32 ? (n <= 16   ? head_few_split_kernel<float, 1, true>
-                              : n <= 32 ? head_few_split_kernel<float, 2, true>
-                                        : head_few_split_kernel<float, 4, true>)
-                           : (n <= 16   ? head_few_split_kernel<uint16_t, 1, true>
-                              : n <= 32 ? head_few_split_kernel<uint16_t, 2, true>
-                                        : head_few_split_kernel<uint16_t, 4, true>);
+        auto* kernel = f32 ? (n <= 16   ? head_few_split_kernel<float, 1, 1>
+                              : n <= 32 ? head_few_split_kernel<float, 2, 1>
+                                        : head_few_split_kernel<float, 4, 1>)
+                           : (n <= 16   ? head_few_split_kernel<uint16_t, 1, 2>
+                              : n <= 32 ? head_few_split_kernel<uint16_t, 2, 2>
+                                        : head_few_split_kernel<uint16_t, 4, 2>);
         hipLaunchKernelGGL(kernel, dim3((unsigned)(cols / 32)), dim3(256), 0, s, f, z);
       } else {
-        e = launch_tiles<EPI_DZ>(t, rows, cols, big_tiles(rows, cols), f32, s);
+        const bool big = big_tiles(rows, cols);
+        e = wide ? launch_tiles<EPI_DZB>(t, rows, cols, big, false, s)
+                 : launch_tiles<EPI_DZ>(t, rows, cols, big, f32, s);
       }
       if (e != hipSuccess) return e;
       hipLaunchKernelGGL(head_sparse_kernel, dim3(blocks_for(n * g.k, 8192)), dim3(256), 0, s,
-                         r.sidx, r.sval, n, g.k, v0, c, dz, ldz, plane, p.planes);
+                         r.sidx, r.sval, n, g.k, v0, c, dz, ldz, plane, wide ? 2 : p.planes, !wide);
 
       // dT of the piece: [c x d], K over the rows
       TileArgs tw{}, th{};
       tw.A = Side{ws + p.off_dz, ldz * 2, plane * 2, cols};
       tw.B = Side{ws + p.off_h, dp2, rows * dp2, p.dp};
-      tw.nseg = nseg;
+      tw.nseg = nseg_grad;
       tw.slots = (int)(rows / 32);
       tw.M = c;
       tw.V = g.d;
-      tw.all_exp = r.all_h;
+      if (!wide) tw.all_exp = r.all_h;
       if (g.dw) {
         auto* acc = reinterpret_cast<float*>(ws + p.off_dw) + v0 * g.d;
         auto* dw32 = static_cast<float*>(g.dw) + v0 * g.d;
@@ -2144,13 +2192,22 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
       }
       // dh: [n x d], K over the piece's columns
       th.A = Side{ws + p.off_dz, ldz * 2, plane * 2, rows};
-      th.B = Side{ws + p.off_w, dp2, cols * dp2, p.dp};
-      th.nseg = nseg;
+      th.B = Side{ws + (wide ? p.off_wz : p.off_w), dp2, cols * dp2, p.dp};
+      if (wide && w_here) {
+        th.B.p = static_cast<const uint8_t*>(w.src);
+        if (odd) {
+          th.B.tail_slot = (int)((c - odd) / 32);
+          th.B.tail = (int64_t)((uintptr_t)wz - ((uintptr_t)w.src + (c - odd) * dp2));
+        }
+      }
+      th.nseg = nseg_grad;
       th.slots = (int)(cols / 32);
       th.M = n;
       th.V = g.d;
-      th.row_exp = r.row_exp;
-      th.all_exp = r.all_w;
+      if (!wide) {
+        th.row_exp = r.row_exp;
+        th.all_exp = r.all_w;
+      }
       if (g.dh) {
         auto* acc = reinterpret_cast<float*>(ws + p.off_dh);
         auto* out = static_cast<uint8_t*>(g.dh) + r0 * g.ld_dh * es;
@@ -2166,7 +2223,7 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
           th.ld_prev = g.d;
         }
       }
-      e = launch_grads(tw, th, reinterpret_cast<float*>(ws + p.off_split), s);
+      e = launch_grads(tw, th, !wide, reinterpret_cast<float*>(ws + p.off_split), s);
       if (e != hipSuccess) return e;
     }
   }

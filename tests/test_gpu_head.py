@@ -113,7 +113,8 @@ class Case:
         mag = np.abs(dz) + edz
         dh, dt = s * (edz @ T), s * (edz.T @ H)
         # sums over whole slots, splits and pieces; halves: three times as many
-        k, drop = (1, 0) if one else (3, 3.1 * 2.0 ** -22)
+        # products, for bf16 and few tokens (dz alone in halves) twice
+        k, drop = (2, 0) if one else (3, 3.1 * 2.0 ** -22)
         dh += s * (mag @ T) * (2 * (k * V + 1000) * U + drop)
         dt += s * (mag.T @ H) * (2 * (k * n + 1000) * U + drop)
         # the placed copies of T and h: T by its largest element, h times its
