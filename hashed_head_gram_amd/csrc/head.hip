@@ -745,12 +745,15 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void head_tile_kernel(TileArgs g
   walk_tiles<EPI, F16, BM, BN, WGM, WGN, false, false>(g, smem, next);
 }
 
-// Both gradients' products of a piece in one launch, a tile each: nw blocks of
-// dT = dz^T h (both operands transposed) and nh of dh = dz T, whichever has the
-// longer K first.
-template <bool F16, int BM, int BN, int WGM, int WGN>
+// Both gradients' products of a piece in one launch: nw blocks of dT = dz^T h
+// (both operands transposed) and nh of dh = dz T, whichever has the longer K
+// first. Where K is short a block takes `per` tiles in a row, the next one's
+// first slots under way in the last one's epilogue (MANY; 185 tokens of 105,456
+// x 545: 181 us, 211 a tile each; the walk itself costs a long product 1 %).
+template <bool F16, bool MANY, int BM, int BN, int WGM, int WGN>
 __global__ __launch_bounds__(64 * WGM * WGN, 2) void head_grad_kernel(TileArgs w, TileArgs h,
-                                                                   uint32_t nw, uint32_t nh) {
+                                                                   uint32_t nw, uint32_t nh,
+                                                                   uint32_t per_w, uint32_t per_h) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Geo<BM, BN, WGM, WGN>::kLds];
   auto one = [](uint32_t b, uint32_t total) {
     const uint32_t per = total / 8;
@@ -758,15 +761,19 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void head_grad_kernel(TileArgs w
   };
   const bool w_first = w.slots / w.splits > h.slots / h.splits;
   const uint32_t b = blockIdx.x;
-  if (w_first ? b < nw : b >= nh) {
-    const uint32_t id = one(w_first ? b : b - nh, nw);
-    walk_tiles<EPI_OUT, F16, BM, BN, WGM, WGN, true, true>(
-        w, smem, [&](int j) { return j ? 0xFFFFFFFFu : id; });
-  } else {
-    const uint32_t id = one(w_first ? b - nw : b, nh);
-    walk_tiles<EPI_OUT, F16, BM, BN, WGM, WGN, false, true>(
-        h, smem, [&](int j) { return j ? 0xFFFFFFFFu : id; });
-  }
+  const bool is_w = w_first ? b < nw : b >= nh;
+  const uint32_t id = (is_w ? one(w_first ? b : b - nh, nw) : one(w_first ? b - nw : b, nh)) *
+                      (is_w ? per_w : per_h);
+  const TileArgs& g = is_w ? w : h;
+  const uint32_t total = (uint32_t)g.nbm * g.nbn * g.splits, per = is_w ? per_w : per_h;
+  auto next = [&](int j) -> uint32_t {
+    if constexpr (!MANY) return j ? 0xFFFFFFFFu : id;
+    return (uint32_t)j < per && id + j < total ? id + j : 0xFFFFFFFFu;
+  };
+  if (is_w)
+    walk_tiles<EPI_OUT, F16, BM, BN, WGM, WGN, true, true>(w, smem, next);
+  else
+    walk_tiles<EPI_OUT, F16, BM, BN, WGM, WGN, false, true>(h, smem, next);
 }
 
 // ---------------------------------------------------------------------------
@@ -788,6 +795,43 @@ struct FewArgs {
   float c2;
   float2* part;            // [tiles of 128 rows][n]
 };
+
+// dz instead of maxima and sums: rows_pad rows, zeros behind the tokens and
+// behind the table.
+struct FewDz {
+  const float *a, *lse2;
+  uint16_t* dz;
+  int64_t ldz, plane;      // elements
+  int rows_pad;
+};
+// dz of token tok at four columns from col on, from their logits in base 2; MODE
+// 1: fp16, two halves where F32; 2: two bf16 halves.
+template <int MODE, bool F32>
+__device__ __forceinline__ void few_dz(const FewDz& z, int64_t tok, int64_t n, int64_t col,
+                                       const float (&v)[4]) {
+  using H = Half<MODE == 1>;
+  const float a = tok < n ? z.a[tok] : 0.f, l = tok < n ? z.lse2[tok] : 0.f;
+  float f[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) f[q] = a == 0.f ? 0.f : a * __builtin_amdgcn_exp2f(v[q] - l);
+  const uint2 w = make_uint2(H::pack(f[0], f[1]), H::pack(f[2], f[3]));
+  uint16_t* to = z.dz + tok * z.ldz + col;
+  *reinterpret_cast<uint2*>(to) = w;
+  if constexpr (F32 || MODE == 2)
+    *reinterpret_cast<uint2*>(to + z.plane) =
+        make_uint2(H::pack(f[0] - H::lo(w.x), f[1] - H::hi(w.x)),
+                   H::pack(f[2] - H::lo(w.y), f[3] - H::hi(w.y)));
+}
+// Zeros in dz's rows from `from` on, `cols` (a multiple of 4) from col on; by the block.
+template <int MODE, bool F32>
+__device__ __forceinline__ void few_dz_zero(const FewDz& z, int from, int64_t col, int cols) {
+  const int per = cols / 4;
+  for (int i = threadIdx.x; i < (z.rows_pad - from) * per; i += 256) {
+    uint16_t* to = z.dz + (from + i / per) * z.ldz + col + i % per * 4;
+    *reinterpret_cast<uint2*>(to) = make_uint2(0, 0);
+    if constexpr (F32 || MODE == 2) *reinterpret_cast<uint2*>(to + z.plane) = make_uint2(0, 0);
+  }
+}
 
 // A fragment of 8 elements as bf16 (fp32: its three planes).
 template <typename T>
@@ -828,8 +872,8 @@ __device__ __forceinline__ void mma_planes(const uint4 (&w)[P], const uint4 (&h)
   mma(0, 0);
 }
 
-template <typename T, int TB>
-__global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g) {
+template <typename T, int TB, int DZ>
+__global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
   constexpr bool F32 = sizeof(T) == 4;
   constexpr int ST = F32 ? 2 : 4;                    // steps of 32 of K under way
   constexpr int P = F32 ? 3 : 1, KC = 32 * ST;
@@ -843,7 +887,7 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g) {
   const uint32_t id = blockIdx.x;
   const uint32_t grp = g.groups == 1 ? 0 : (id >> 3) % g.groups;
   const uint32_t tile = g.groups == 1 ? id : (id >> 3) / g.groups * 8 + (id & 7);
-  if ((int64_t)tile * 128 >= g.V) return;
+  if (DZ == 0 && (int64_t)tile * 128 >= g.V) return;
   const int64_t v0 = (int64_t)tile * 128 + wave * 32, x0 = (int64_t)grp * 64;
   const T* wp[2];
 #pragma unroll
@@ -932,6 +976,16 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g) {
 #pragma unroll
   for (int t = 0; t < TB; ++t) {
     float z[2][4], m = -INFINITY;
+    if constexpr (DZ != 0) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          z[r][q] = v0 + r * 16 + 4 * kq + q < g.V ? acc[t][r][q] * g.c2 : -INFINITY;
+        few_dz<DZ, F32>(dz, t * 16 + fr, g.n, v0 + r * 16 + 4 * kq, z[r]);
+      }
+      continue;
+    }
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -951,6 +1005,10 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g) {
     s += __shfl_xor(s, 32);
     if (kq == 0) red[wave][t * 16 + fr] = make_float2(m, s);
   }
+  if constexpr (DZ != 0) {
+    few_dz_zero<DZ, F32>(dz, 16 * TB, (int64_t)tile * 128, 128);
+    return;
+  }
   __syncthreads();
   const int x = threadIdx.x;
   if (x < 16 * TB && x0 + x < g.n) {
@@ -969,13 +1027,6 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g) {
 // meet in LDS, so a chain of loads is a quarter as long. Fragments of the tokens
 // come straight from memory here. DZ: leaves dz (rows_pad rows, zeros behind the
 // tokens and behind the table) instead of maxima and sums.
-struct FewDz {
-  const float *a, *lse2;
-  uint16_t* dz;
-  int64_t ldz, plane;      // elements
-  int rows_pad;
-};
-
 template <typename T, int TB, int DZ>
 __global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_few_split_kernel(FewArgs g, FewDz z) {
   constexpr bool F32 = sizeof(T) == 4;
@@ -1067,29 +1118,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_f
       s += __shfl_xor(s, 32);
       if (kq == 0 && tok < g.n) g.part[(int64_t)blockIdx.x * g.n + tok] = make_float2(m, s);
     } else {
-      const float a = tok < g.n ? z.a[tok] : 0.f, l = tok < g.n ? z.lse2[tok] : 0.f;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float f[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) f[q] = a == 0.f ? 0.f : a * __builtin_amdgcn_exp2f(v[r][q] - l);
-        using H = Half<DZ == 1>;
-        const uint2 w = make_uint2(H::pack(f[0], f[1]), H::pack(f[2], f[3]));
-        uint16_t* to = z.dz + tok * z.ldz + v0 + r * 16 + 4 * kq;
-        *reinterpret_cast<uint2*>(to) = w;
-        if constexpr (F32 || DZ == 2)
-          *reinterpret_cast<uint2*>(to + z.plane) =
-              make_uint2(H::pack(f[0] - H::lo(w.x), f[1] - H::hi(w.x)),
-                         H::pack(f[2] - H::lo(w.y), f[3] - H::hi(w.y)));
-      }
+      for (int r = 0; r < 2; ++r) few_dz<DZ, F32>(z, tok, g.n, v0 + r * 16 + 4 * kq, v[r]);
     }
   }
-  if constexpr (DZ != 0)                             // rows behind the token blocks
-    for (int i = threadIdx.x; i < (z.rows_pad - 16 * TB) * 8; i += 256) {
-      uint16_t* to = z.dz + (16 * TB + (i >> 3)) * z.ldz + v0 + (i & 7) * 4;
-      *reinterpret_cast<uint2*>(to) = make_uint2(0, 0);
-      if constexpr (F32 || DZ == 2) *reinterpret_cast<uint2*>(to + z.plane) = make_uint2(0, 0);
-    }
+  if constexpr (DZ != 0) few_dz_zero<DZ, F32>(z, 16 * TB, v0, 32);
 }
 
 // ---------------------------------------------------------------------------
@@ -1395,7 +1428,7 @@ constexpr int kFew = 64, kFewCopied = 256;
 constexpr int64_t kFewShort = 8192;
 // Tokens up to which bf16 tables are used as they are for dh too: dz is then two
 // bf16 halves (16 bits), two products for one, and the fp16 copies, three more
-// passes over the table, fall away. 65,536 rows of 2048, 8 tokens: WIDE_US.
+// passes over the table, fall away (65,536 rows of 2048, 8 tokens: 354 us, 430).
 constexpr int kWide = 256;
 constexpr int kScanBlocks = 512;
 constexpr int kRowBlocks = 512;           // most blocks over rows, four waves each
@@ -1711,7 +1744,7 @@ __global__ __launch_bounds__(256) void head_zero_kernel(uint16_t* out, int64_t c
 }
 
 int64_t pad(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
-int64_t tiles_of(int64_t x, int b) { return (x + b - 1) / b; }
+int64_t tiles_of(int64_t x, int64_t b) { return (x + b - 1) / b; }
 int blocks_for(int64_t items, int most) {
   const int64_t b = (items + 255) / 256;
   return (int)(b < 1 ? 1 : b > most ? most : b);
@@ -1853,12 +1886,12 @@ hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* works
     } else {
     parts = tiles_of(g.V, 128);
     const int64_t blocks = groups == 1 ? parts : pad(parts, 8) * groups;
-    auto* kernel = f32 ? (g.n <= 16 ? head_few_kernel<float, 1> : g.n <= 32 ? head_few_kernel<float, 2>
-                                                                            : head_few_kernel<float, 4>)
-                       : (g.n <= 16   ? head_few_kernel<uint16_t, 1>
-                          : g.n <= 32 ? head_few_kernel<uint16_t, 2>
-                                      : head_few_kernel<uint16_t, 4>);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, s, f);
+    auto* kernel = f32 ? (g.n <= 16 ? head_few_kernel<float, 1, 0> : g.n <= 32 ? head_few_kernel<float, 2, 0>
+                                                                            : head_few_kernel<float, 4, 0>)
+                       : (g.n <= 16   ? head_few_kernel<uint16_t, 1, 0>
+                          : g.n <= 32 ? head_few_kernel<uint16_t, 2, 0>
+                                      : head_few_kernel<uint16_t, 4, 0>);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, s, f, FewDz{});
     }
   } else {
     RowArgs r{};
@@ -1974,7 +2007,7 @@ static hipError_t launch_grads(TileArgs tw, TileArgs th, bool f16, float* split,
   // Tile size and K's splits: tiles run longest first, a large one to a compute
   // unit or two small ones; splitting evens out their end, but writes and reads a
   // result more. Times in us: 0.95 a slot of a large tile, 0.6 of a small one
-  // (twice as many run at once), 5 MB/us for partial results.
+  // (4 more for its start and end; twice as many run at once), 5 MB/us for partial results.
   double best = 1e30;
   bool big = false;
   int kw = 1, kh = 1;
@@ -1995,7 +2028,7 @@ static hipError_t launch_grads(TileArgs tw, TileArgs th, bool f16, float* split,
       for (int j = 1; j <= mh; j = j < 16 ? j + 1 : j * 5 / 4) {
         const int64_t split_tiles = (i > 1 ? nw * i : 0) + (j > 1 ? nh * j : 0);
         if (split_tiles > at_once) continue;
-        const double lw = nw ? (double)tw.slots / i : 0, lh = nh ? (double)th.slots / j : 0;
+        const double lw = nw ? (double)tw.slots / i + 4 : 0, lh = nh ? (double)th.slots / j + 4 : 0;
         double t = slot * (lw > lh ? makespan(nw * i, lw, nh * j, lh, at_once)
                                    : makespan(nh * j, lh, nw * i, lw, at_once));
         if (split_tiles) t += 6 + (double)split_tiles * b * b * 8 / 5e6;
@@ -2031,10 +2064,28 @@ static hipError_t launch_grads(TileArgs tw, TileArgs th, bool f16, float* split,
   };
   share(tw, kw, sums[0]);
   share(th, kh, sums[1]);
-  const uint32_t gw = (uint32_t)(nw * tw.splits), gh = (uint32_t)(nh * th.splits);
-  auto* kernel = big ? (f16 ? head_grad_kernel<true, 256, 256, 2, 4> : head_grad_kernel<false, 256, 256, 2, 4>)
-                     : (f16 ? head_grad_kernel<true, 128, 128, 2, 2> : head_grad_kernel<false, 128, 128, 2, 2>);
-  hipLaunchKernelGGL(kernel, dim3(gw + gh), dim3(big ? 512 : 256), 0, s, tw, th, gw, gh);
+  // short tiles: about 64 slots a block, while that leaves blocks enough
+  const int at_once = big ? kCUs : 2 * kCUs;
+  auto per_block = [&](const TileArgs& t, int64_t n) {
+    int64_t per = 64 / ((int64_t)t.slots * t.nseg / t.splits);
+    if (per > n / (4 * at_once)) per = n / (4 * at_once);
+    return (uint32_t)(per < 1 ? 1 : per);
+  };
+  const uint32_t per_w = per_block(tw, nw * tw.splits), per_h = per_block(th, nh * th.splits);
+  const uint32_t gw = (uint32_t)tiles_of(nw * tw.splits, per_w);
+  const uint32_t gh = (uint32_t)tiles_of(nh * th.splits, per_h);
+  const bool many = per_w > 1 || per_h > 1;
+  auto pick = [&](auto* f, auto* b, auto* fm, auto* bm) { return many ? (f16 ? fm : bm) : f16 ? f : b; };
+  auto* kernel = big ? pick(head_grad_kernel<true, false, 256, 256, 2, 4>,
+                            head_grad_kernel<false, false, 256, 256, 2, 4>,
+                            head_grad_kernel<true, true, 256, 256, 2, 4>,
+                            head_grad_kernel<false, true, 256, 256, 2, 4>)
+                     : pick(head_grad_kernel<true, false, 128, 128, 2, 2>,
+                            head_grad_kernel<false, false, 128, 128, 2, 2>,
+                            head_grad_kernel<true, true, 128, 128, 2, 2>,
+                            head_grad_kernel<false, true, 128, 128, 2, 2>);
+  hipLaunchKernelGGL(kernel, dim3(gw + gh), dim3(big ? 512 : 256), 0, s, tw, th, gw, gh,
+                     per_w, per_h);
   const int sw = sums[0].splits ? blocks_for(sums[0].M * ((sums[0].N + 3) / 4) * 8, 2048) : 0;
   const int sh = sums[1].splits ? blocks_for(sums[1].M * ((sums[1].N + 3) / 4) * 8, 2048) : 0;
   if (sw + sh)
@@ -2061,7 +2112,7 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
   const bool w_here = in_place(g.dtype, g.d, g.d, g.table);
   for (int64_t r0 = 0; r0 < g.n; r0 += p.rows) {
     const int64_t n = g.n - r0 < p.rows ? g.n - r0 : p.rows;
-    const int64_t rows = pad(n, 128);
+    const int64_t rows = pad(n, nseg_grad > 1 ? 64 : 128);   // four slots of K at least
     const bool first_rows = r0 == 0, last_rows = r0 + n == g.n;
     RowArgs r{};
     r.h = static_cast<const uint8_t*>(g.h) + r0 * g.ld_h * es;
@@ -2148,16 +2199,19 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
       t.Mpad = rows;
       t.Vpad = cols;
       hipError_t e = hipSuccess;
-      if (n <= kFew && c <= kFewShort) {
+      if (n <= kFew) {
         const FewArgs f{r.h, w.src, g.ld_h, n, c, g.d, 1, r.c2, nullptr};
         const FewDz z{r.a, r.lse2, dz, ldz, plane, (int)rows};
-        auto* kernel = f32 ? (n <= 16   ? head_few_split_kernel<float, 1, 1>
-                              : n <= 32 ? head_few_split_kernel<float, 2, 1>
-                                        : head_few_split_kernel<float, 4, 1>)
-                           : (n <= 16   ? head_few_split_kernel<uint16_t, 1, 2>
-                              : n <= 32 ? head_few_split_kernel<uint16_t, 2, 2>
-                                        : head_few_split_kernel<uint16_t, 4, 2>);
-        hipLaunchKernelGGL(kernel, dim3((unsigned)(cols / 32)), dim3(256), 0, s, f, z);
+        const bool one = c <= kFewShort;             // 32 rows of T a block
+        auto pick = [&](auto* split, auto* whole) { return one ? split : whole; };
+        auto* kernel =
+            f32 ? (n <= 16   ? pick(head_few_split_kernel<float, 1, 1>, head_few_kernel<float, 1, 1>)
+                   : n <= 32 ? pick(head_few_split_kernel<float, 2, 1>, head_few_kernel<float, 2, 1>)
+                             : pick(head_few_split_kernel<float, 4, 1>, head_few_kernel<float, 4, 1>))
+                : (n <= 16   ? pick(head_few_split_kernel<uint16_t, 1, 2>, head_few_kernel<uint16_t, 1, 2>)
+                   : n <= 32 ? pick(head_few_split_kernel<uint16_t, 2, 2>, head_few_kernel<uint16_t, 2, 2>)
+                             : pick(head_few_split_kernel<uint16_t, 4, 2>, head_few_kernel<uint16_t, 4, 2>));
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(cols / (one ? 32 : 128))), dim3(256), 0, s, f, z);
       } else {
         const bool big = big_tiles(rows, cols);
         e = wide ? launch_tiles<EPI_DZB>(t, rows, cols, big, false, s)
