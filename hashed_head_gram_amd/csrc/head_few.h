@@ -1,0 +1,360 @@
+// The head's logits for few tokens, where reading the table once is what counts.
+#pragma once
+
+#include "head_tile.h"
+
+namespace pg {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Few tokens
+
+// Maxima and sums of few tokens over 128 rows of the table: what counts is
+// reading the table once, from where it lies and whatever its width. Blocks of
+// up to 64 tokens, those of one tile of the table next to each other. A wave has
+// 32 rows to itself and takes the fragments of 16 x 16 x 32 products straight
+// from memory, 16 rows by 64 bytes a load; the next 128 of K are under way
+// while the last are multiplied. No barrier until the end. (Fragments of
+// 32 x 32 x 16, 32 bytes a row, read at 4.0 TB/s, 64 bytes at 6.1, as whole
+// rows would.) fp32 operands are split in registers into three bf16 planes (24
+// bits), six products for one, so nothing has to be placed or copied.
+struct FewArgs {
+  const void *h, *table;
+  int64_t ld, n, V;
+  int d, groups;           // of 64 tokens
+  float c2;
+  float2* part;            // [tiles of 128 rows][n]
+};
+
+// dz instead of maxima and sums: rows_pad rows, zeros behind the tokens and
+// behind the table.
+struct FewDz {
+  const float *a, *lse2;
+  uint16_t* dz;
+  int64_t ldz, plane;      // elements
+  int rows_pad;
+};
+// dz of token tok at four columns from col on, from their logits in base 2; MODE
+// 1: fp16, two halves where F32; 2: two bf16 halves.
+template <int MODE, bool F32>
+__device__ __forceinline__ void few_dz(const FewDz& z, int64_t tok, int64_t n, int64_t col,
+                                       const float (&v)[4]) {
+  using H = Half<MODE == 1>;
+  const float a = tok < n ? z.a[tok] : 0.f, l = tok < n ? z.lse2[tok] : 0.f;
+  float f[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) f[q] = a == 0.f ? 0.f : a * __builtin_amdgcn_exp2f(v[q] - l);
+  const uint2 w = make_uint2(H::pack(f[0], f[1]), H::pack(f[2], f[3]));
+  uint16_t* to = z.dz + tok * z.ldz + col;
+  *reinterpret_cast<uint2*>(to) = w;
+  if constexpr (F32 || MODE == 2)
+    *reinterpret_cast<uint2*>(to + z.plane) =
+        make_uint2(H::pack(f[0] - H::lo(w.x), f[1] - H::hi(w.x)),
+                   H::pack(f[2] - H::lo(w.y), f[3] - H::hi(w.y)));
+}
+// Zeros in dz's rows from `from` on, `cols` (a multiple of 4) from col on; by the block.
+template <int MODE, bool F32>
+__device__ __forceinline__ void few_dz_zero(const FewDz& z, int from, int64_t col, int cols) {
+  const int per = cols / 4;
+  for (int i = threadIdx.x; i < (z.rows_pad - from) * per; i += 256) {
+    uint16_t* to = z.dz + (from + i / per) * z.ldz + col + i % per * 4;
+    *reinterpret_cast<uint2*>(to) = make_uint2(0, 0);
+    if constexpr (F32 || MODE == 2) *reinterpret_cast<uint2*>(to + z.plane) = make_uint2(0, 0);
+  }
+}
+
+// A fragment of 8 elements as bf16 (fp32: its three planes).
+template <typename T>
+__device__ __forceinline__ void planes_of(const Raw8<T>& v, uint4 (&f)[sizeof(T) == 4 ? 3 : 1]) {
+  if constexpr (sizeof(T) == 4) {
+    float x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) x[u] = v.v[u];
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      uint32_t w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        w[u] = pack2_bf16(x[2 * u], x[2 * u + 1]);
+        x[2 * u] -= __uint_as_float(w[u] << 16);
+        x[2 * u + 1] -= __uint_as_float(w[u] & 0xFFFF0000u);
+      }
+      f[p] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+    f[0] = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+  }
+}
+// acc += w h of two fragments' planes, small products first.
+template <int P>
+__device__ __forceinline__ void mma_planes(const uint4 (&w)[P], const uint4 (&h)[P], f32x4_t& acc) {
+  auto mma = [&](int a, int b) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w[a]),
+                                                  __builtin_bit_cast(bf16x8_t, h[b]), acc, 0, 0, 0);
+  };
+  if constexpr (P == 3) {
+    mma(2, 0);
+    mma(0, 2);
+    mma(1, 1);
+    mma(1, 0);
+    mma(0, 1);
+  }
+  mma(0, 0);
+}
+
+template <typename T, int TB, int DZ>
+__global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int ST = F32 ? 2 : 4;                    // steps of 32 of K under way
+  constexpr int P = F32 ? 3 : 1, KC = 32 * ST;
+  constexpr int RB = KC * 2;                         // bytes of a token's row in LDS
+  constexpr int CH = 16 * TB * KC / 8;               // its 8-element chunks in all
+  constexpr int HL = (CH + 255) / 256;               // of them a thread
+  __shared__ __attribute__((aligned(256))) uint8_t hs[2][P][16 * TB * RB];
+  __shared__ float2 red[4][16 * TB];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, fr = lane & 15, kq = lane >> 4;
+  // a tile's groups run 8 blocks apart: on one XCD, where they share its L2
+  const uint32_t id = blockIdx.x;
+  const uint32_t grp = g.groups == 1 ? 0 : (id >> 3) % g.groups;
+  const uint32_t tile = g.groups == 1 ? id : (id >> 3) / g.groups * 8 + (id & 7);
+  if (DZ == 0 && (int64_t)tile * 128 >= g.V) return;
+  const int64_t v0 = (int64_t)tile * 128 + wave * 32, x0 = (int64_t)grp * 64;
+  const T* wp[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int64_t v = v0 + r * 16 + fr;
+    wp[r] = static_cast<const T*>(g.table) + (v < g.V ? v : g.V - 1) * g.d + kq * 8;
+  }
+  // 16-byte chunk c of token x in LDS: the 16 tokens a read serves together
+  // meet every bank once
+  auto place = [](int x, int c) {
+    return RB == 256 ? x * 256 + ((c ^ (x & 15)) * 16) : x * 128 + ((c ^ ((x >> 1) & 7)) * 16);
+  };
+  const T* hp[HL];
+  int hc[HL];
+#pragma unroll
+  for (int u = 0; u < HL; ++u) {
+    const int i = u * 256 + threadIdx.x, x = i / (KC / 8);
+    hc[u] = i % (KC / 8) * 8;
+    hp[u] = static_cast<const T*>(g.h) + (x0 + x < g.n ? x0 + x : g.n - 1) * g.ld + hc[u];
+  }
+  f32x4_t acc[TB][2] = {};
+  Raw8<T> hr[HL], wr[2][ST][2];
+  auto load = [&](int k, Raw8<T> (&w)[ST][2]) {
+    const bool all = k + KC <= g.d;
+#pragma unroll
+    for (int u = 0; u < HL; ++u)
+      if (HL * 256 == CH || u * 256 + (int)threadIdx.x < CH)
+        hr[u] = load8(hp[u] + k, all ? 8 : g.d - k - hc[u]);
+#pragma unroll
+    for (int s = 0; s < ST; ++s)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        w[s][r] = load8(wp[r] + k + s * 32, all ? 8 : g.d - k - s * 32 - kq * 8);
+  };
+  auto stage = [&](int buf) {
+#pragma unroll
+    for (int u = 0; u < HL; ++u) {
+      const int i = u * 256 + threadIdx.x;
+      if (HL * 256 == CH || i < CH) {
+        uint4 f[P];
+        planes_of(hr[u], f);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          *reinterpret_cast<uint4*>(hs[buf][p] + place(i / (KC / 8), i % (KC / 8))) = f[p];
+      }
+    }
+  };
+  auto multiply = [&](int buf, const Raw8<T> (&w)[ST][2]) {
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      uint4 wf[2][P];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) planes_of(w[s][r], wf[r]);
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        uint4 hf[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          hf[p] = *reinterpret_cast<const uint4*>(hs[buf][p] + place(t * 16 + fr, s * 4 + kq));
+#pragma unroll
+        for (int r = 0; r < 2; ++r) mma_planes(wf[r], hf, acc[t][r]);
+      }
+    }
+  };
+  // One barrier a chunk: a buffer is written again two chunks on, behind the
+  // barrier that every wave reaches with its reads of it done.
+  const int chunks = (g.d + KC - 1) / KC;
+  int at = (int)(tile % chunks);                     // tiles start apart
+  auto chunk = [&](int c, int buf, const Raw8<T> (&w)[ST][2], Raw8<T> (&next)[ST][2]) {
+    stage(buf);
+    at = at + 1 == chunks ? 0 : at + 1;
+    if (c + 1 < chunks) load(at * KC, next);
+    wait_lds();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    multiply(buf, w);
+  };
+  load(at * KC, wr[0]);
+  for (int c = 0; c < chunks; c += 2) {
+    chunk(c, 0, wr[0], wr[1]);
+    if (c + 1 < chunks) chunk(c + 1, 1, wr[1], wr[0]);
+  }
+
+  // a lane has rows 16 r + 4 kq + q of the wave's 32, token 16 t + fr
+#pragma unroll
+  for (int t = 0; t < TB; ++t) {
+    float z[2][4], m = -INFINITY;
+    if constexpr (DZ != 0) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          z[r][q] = v0 + r * 16 + 4 * kq + q < g.V ? acc[t][r][q] * g.c2 : -INFINITY;
+        few_dz<DZ, F32>(dz, t * 16 + fr, g.n, v0 + r * 16 + 4 * kq, z[r]);
+      }
+      continue;
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        z[r][q] = v0 + r * 16 + 4 * kq + q < g.V ? acc[t][r][q] * g.c2 : -INFINITY;
+        m = fmaxf(m, z[r][q]);
+      }
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s += __builtin_amdgcn_exp2f(z[r][q] - ref);
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (kq == 0) red[wave][t * 16 + fr] = make_float2(m, s);
+  }
+  if constexpr (DZ != 0) {
+    few_dz_zero<DZ, F32>(dz, 16 * TB, (int64_t)tile * 128, 128);
+    return;
+  }
+  __syncthreads();
+  const int x = threadIdx.x;
+  if (x < 16 * TB && x0 + x < g.n) {
+    float m = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, red[w][x].x);
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) s += red[w][x].y * __builtin_amdgcn_exp2f(red[w][x].x - ref);
+    g.part[(int64_t)tile * g.n + x0 + x] = make_float2(m, s);
+  }
+}
+
+// The same where the table is short too and blocks of 128 rows would leave most
+// of the chip idle: a block has 32 rows, its four waves share K and their sums
+// meet in LDS, so a chain of loads is a quarter as long. Fragments of the tokens
+// come straight from memory here. DZ: leaves dz (rows_pad rows, zeros behind the
+// tokens and behind the table) instead of maxima and sums.
+template <typename T, int TB, int DZ>
+__global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_few_split_kernel(
+    FewArgs g, FewDz z) {
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int ST = F32 ? 2 : 4, P = F32 ? 3 : 1, KC = 32 * ST;
+  __shared__ f32x4_t join[4][TB * 2][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, fr = lane & 15, kq = lane >> 4;
+  const int64_t v0 = (int64_t)blockIdx.x * 32;
+  const T *wp[2], *hp[TB];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int64_t v = v0 + r * 16 + fr;
+    wp[r] = static_cast<const T*>(g.table) + (v < g.V ? v : g.V - 1) * g.d + kq * 8;
+  }
+#pragma unroll
+  for (int t = 0; t < TB; ++t) {
+    const int64_t x = t * 16 + fr;
+    hp[t] = static_cast<const T*>(g.h) + (x < g.n ? x : g.n - 1) * g.ld + kq * 8;
+  }
+  f32x4_t acc[TB][2] = {};
+  struct Step {
+    Raw8<T> w[2], h[TB];
+  };
+  auto load = [&](int k, Step (&to)[ST]) {
+    const bool all = k + KC <= g.d;
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      const int left = all ? 8 : g.d - k - s * 32 - kq * 8;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) to[s].w[r] = load8(wp[r] + k + s * 32, left);
+#pragma unroll
+      for (int t = 0; t < TB; ++t) to[s].h[t] = load8(hp[t] + k + s * 32, left);
+    }
+  };
+  auto multiply = [&](const Step (&x)[ST]) {
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      uint4 wf[2][P];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) planes_of(x[s].w[r], wf[r]);
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        uint4 hf[P];
+        planes_of(x[s].h[t], hf);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) mma_planes(wf[r], hf, acc[t][r]);
+      }
+    }
+  };
+  Step x[2][ST];
+  int k = wave * KC;
+  if (k < g.d) load(k, x[0]);
+  for (; k < g.d; k += 8 * KC) {
+    if (k + 4 * KC < g.d) load(k + 4 * KC, x[1]);
+    multiply(x[0]);
+    if (k + 4 * KC < g.d) {
+      if (k + 8 * KC < g.d) load(k + 8 * KC, x[0]);
+      multiply(x[1]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TB; ++t)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) join[wave][t * 2 + r][lane] = acc[t][r];
+  __syncthreads();
+  // wave t has token block t from here on: rows 16 r + 4 kq + q, token 16 t + fr
+  if (wave < TB) {
+    const int64_t tok = wave * 16 + fr;
+    float v[2][4], m = -INFINITY;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const f32x4_t sum = (join[0][wave * 2 + r][lane] + join[1][wave * 2 + r][lane]) +
+                          (join[2][wave * 2 + r][lane] + join[3][wave * 2 + r][lane]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[r][q] = v0 + r * 16 + 4 * kq + q < g.V ? sum[q] * g.c2 : -INFINITY;
+        m = fmaxf(m, v[r][q]);
+      }
+    }
+    if constexpr (DZ == 0) {
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
+      const float ref = m == -INFINITY ? 0.f : m;
+      float s = 0.f;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s += __builtin_amdgcn_exp2f(v[r][q] - ref);
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
+      if (kq == 0 && tok < g.n) g.part[(int64_t)blockIdx.x * g.n + tok] = make_float2(m, s);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) few_dz<DZ, F32>(z, tok, g.n, v0 + r * 16 + 4 * kq, v[r]);
+    }
+  }
+  if constexpr (DZ != 0) few_dz_zero<DZ, F32>(z, 16 * TB, v0, 32);
+}
+
+}  // namespace
+}  // namespace pg

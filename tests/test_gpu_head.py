@@ -173,6 +173,11 @@ SIZES = [  # n, V, d, dtype, scale, spread, pad
     (1500, 6144, 256, "f32", 1.0, 1.0, 0),
     (2500, 300, 320, "bf16", 1.0, 1.0, 0),
     (16, 3000, 16, "bf16", 1.0, 40.0, 0),            # logits of several hundred
+    (200, 1000, 128, "bf16", 1.0, 1.0, 0),           # the last rows of the table apart
+    (60, 9001, 160, "bf16", 1.0, 1.0, 3),
+    (17, 8193, 40, "f32", 1.0, 1.0, 1),
+    (200, 777, 97, "bf16", 1.0, 1.0, 0),
+    (250, 700, 64, "f32", 1.0, 1.0, 0),
 ]
 
 

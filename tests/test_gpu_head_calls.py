@@ -227,11 +227,14 @@ def test_gradient_of_a_tied_table(n, V, d, dt):
 
 def test_pieces_of_the_vocabulary_and_of_the_batch():
     """Many tokens against a wide table: 2 pieces of columns; more rows than a
-    piece of the batch: 2 of those; in bf16 and fp32, against float64."""
+    piece of the batch: 2 of those, the last one short; few tokens against many
+    rows, several tiles a block; in bf16 and fp32, against float64."""
     g = torch.Generator(device="cuda").manual_seed(3)
     for n, V, d, dt in ((16500, 33001, 128, "bf16"), (33000, 20000, 64, "bf16"),
                         (9000, 33000, 32, "f32"), (33000, 300, 40, "f32"),
-                        (33000, 301, 129, "bf16")):
+                        (33000, 301, 129, "bf16"), (32800, 300, 128, "bf16"),
+                        (32800, 300, 40, "f32"), (100, 70001, 1024, "bf16"),
+                        (40, 70000, 1024, "bf16"), (40, 40000, 1024, "f32")):
         h = torch.randn(n, d, device="cuda", generator=g).to(DT[dt])
         t = (torch.randn(V, d, device="cuda", generator=g) / d ** 0.5).to(DT[dt])
         tok = torch.randint(-1, V, (n,), device="cuda", generator=g, dtype=torch.int32)
@@ -249,7 +252,9 @@ def test_pieces_of_the_vocabulary_and_of_the_batch():
         T, e = t.double(), products(dt, d)
         wt = torch.where(tok >= 0, dl, 0.0).double()
         rt, bt = torch.zeros_like(T), torch.zeros_like(T)
-        sums = 1e-3 if dt == "bf16" else 3e-3       # 2 (k V + 1000) u, at most 33,000 terms
+        # 2 (k m + 1000) u for a sum of m terms, k products each; dT over the tokens
+        k = 2 if dt == "bf16" else 3
+        sum_h, sum_t = 2 * (k * V + 1000) * U, 2 * (k * n + 1000) * U
         rel = 2.0 ** -11 if dt == "bf16" else 2.0 ** -22
         drop = 0 if dt == "bf16" else 3.1 * 2.0 ** -22
         B = wt.abs().max() * 2
@@ -277,13 +282,13 @@ def test_pieces_of_the_vocabulary_and_of_the_batch():
             ep = ep + (p.abs() + ep) * rel + 2.0 ** -39 * B
             mag = p.abs() + ep
             rh = p @ T
-            bh = ep @ T.abs() + (mag @ T.abs()) * (sums / 33000 * V + 1e-4 + drop) \
+            bh = ep @ T.abs() + (mag @ T.abs()) * (sum_h + drop) \
                 + mag.sum(1, keepdim=True) * 2.0 ** -39 * T.abs().max()
             bh += HALF[dt] * (rh.abs() + bh) + 1e-30
             bad = (dh[a:b].double() - rh).abs() > bh
             assert not bool(bad.any()), (n, V, d, dt, a, int(bad.sum()))
             rt += p.T.contiguous() @ H
-            bt += ep.T.contiguous() @ H.abs() + (mag.T.contiguous() @ H.abs()) * (sums + drop)
+            bt += ep.T.contiguous() @ H.abs() + (mag.T.contiguous() @ H.abs()) * (sum_t + drop)
         bt += n * 2.0 ** -37 * M
         bt += HALF[dt] * (rt.abs() + bt) + 1e-30
         bad = (dw.double() - rt).abs() > bt
