@@ -13,11 +13,19 @@ namespace {
 // reading the table once, from where it lies and whatever its width. Blocks of
 // up to 64 tokens, those of one tile of the table next to each other. A wave has
 // 32 rows to itself and takes the fragments of 16 x 16 x 32 products straight
-// from memory, 16 rows by 64 bytes a load; the next 128 of K are under way
-// while the last are multiplied. No barrier until the end. (Fragments of
-// 32 x 32 x 16, 32 bytes a row, read at 4.0 TB/s, 64 bytes at 6.1, as whole
-// rows would.) fp32 operands are split in registers into three bf16 planes (24
-// bits), six products for one, so nothing has to be placed or copied.
+// from memory, 16 rows by 64 bytes a load, the 512 bytes of a row (fp32 256) one
+// behind the other; the next ones are under way while the last are multiplied.
+// The tokens' part of a chunk goes through LDS, which the four waves share:
+// fetched by every wave for itself it took as many loads as the table. fp32
+// operands are split in registers into three bf16 planes (24 bits), six products
+// for one, so nothing has to be placed or copied.
+//
+// 32 tokens, 128,000 rows of 2560, bf16: 118 us, 5.5 TB/s (a bare read of the
+// same pattern 107). On the way: fragments of 32 x 32 x 16, 32 bytes a row and
+// load, 162 us; tokens fetched by every wave 160; parts of 16 rows in turn
+// instead of a row's 138; 256 bytes of a row at a time 125; without the barrier
+// it would be 115. From 65 tokens on (fp32 and rows that tiles cannot read in
+// place: 257) the tiles are faster.
 struct FewArgs {
   const void *h, *table;
   int64_t ld, n, V;
@@ -105,7 +113,7 @@ __device__ __forceinline__ void mma_planes(const uint4 (&w)[P], const uint4 (&h)
 template <typename T, int TB, int DZ>
 __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
   constexpr bool F32 = sizeof(T) == 4;
-  constexpr int ST = F32 ? 2 : 4;                    // steps of 32 of K under way
+  constexpr int ST = F32 ? 2 : 8;                    // steps of 32 of K under way
   constexpr int P = F32 ? 3 : 1, KC = 32 * ST;
   constexpr int RB = KC * 2;                         // bytes of a token's row in LDS
   constexpr int CH = 16 * TB * KC / 8;               // its 8-element chunks in all
@@ -128,6 +136,7 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
   // 16-byte chunk c of token x in LDS: the 16 tokens a read serves together
   // meet every bank once
   auto place = [](int x, int c) {
+    if constexpr (RB == 512) return x * 512 + ((c ^ (x & 15)) * 16);
     return RB == 256 ? x * 256 + ((c ^ (x & 15)) * 16) : x * 128 + ((c ^ ((x >> 1) & 7)) * 16);
   };
   const T* hp[HL];
@@ -146,10 +155,11 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
     for (int u = 0; u < HL; ++u)
       if (HL * 256 == CH || u * 256 + (int)threadIdx.x < CH)
         hr[u] = load8(hp[u] + k, all ? 8 : g.d - k - hc[u]);
+    // a row's 64-byte parts one behind the other: the other way round it took 12 us more
 #pragma unroll
-    for (int s = 0; s < ST; ++s)
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int s = 0; s < ST; ++s)
         w[s][r] = load8(wp[r] + k + s * 32, all ? 8 : g.d - k - s * 32 - kq * 8);
   };
   auto stage = [&](int buf) {
@@ -282,14 +292,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_f
   };
   auto load = [&](int k, Step (&to)[ST]) {
     const bool all = k + KC <= g.d;
+    auto left = [&](int s) { return all ? 8 : g.d - k - s * 32 - kq * 8; };
 #pragma unroll
-    for (int s = 0; s < ST; ++s) {
-      const int left = all ? 8 : g.d - k - s * 32 - kq * 8;
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) to[s].w[r] = load8(wp[r] + k + s * 32, left);
+      for (int s = 0; s < ST; ++s) to[s].w[r] = load8(wp[r] + k + s * 32, left(s));
 #pragma unroll
-      for (int t = 0; t < TB; ++t) to[s].h[t] = load8(hp[t] + k + s * 32, left);
-    }
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+      for (int s = 0; s < ST; ++s) to[s].h[t] = load8(hp[t] + k + s * 32, left(s));
   };
   auto multiply = [&](const Step (&x)[ST]) {
 #pragma unroll
