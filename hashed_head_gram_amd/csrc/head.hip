@@ -51,8 +51,15 @@ bool in_place(int32_t dtype, int d, int64_t ld, const void* p) {
          (uintptr_t)p % 16 == 0;
 }
 
-bool big_tiles(int64_t M, int64_t N) {
-  return tiles_of(M, 256) * tiles_of(N, 256) >= kCUs / 2 && M > 128;
+// Whether M x N of K's slots go by large tiles: rounds of tiles over the chip (a
+// large one to a compute unit, or two small ones) times a tile's us, 0.95 or 0.6
+// a slot and its epilogue.
+bool big_tiles(int64_t M, int64_t N, int slots, double epilogue) {
+  const double large = (double)tiles_of(tiles_of(M, 256) * tiles_of(N, 256), kCUs) *
+                       (0.95 * slots + epilogue);
+  const double small = (double)tiles_of(tiles_of(M, 128) * tiles_of(N, 128), 2 * kCUs) *
+                       (0.6 * slots + epilogue / 2);
+  return large <= small;
 }
 
 template <int EPI>
@@ -179,7 +186,7 @@ hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* works
   bool picked = false;
   const bool h_here = in_place(g.dtype, g.d, g.ld_h, g.h);
   const bool w_here = in_place(g.dtype, g.d, g.d, g.table);
-  if (g.n <= (w_here ? kFew : kFewCopied)) {
+  if (g.n <= (w_here ? kFew : f32 ? kFewF32 : kFewOdd)) {
     const int groups = (int)tiles_of(g.n, 64);
     const FewArgs f{g.h, g.table, g.ld_h, g.n, g.V, g.d, groups, t.c2,
                     reinterpret_cast<float2*>(ws + p.off_part)};
@@ -211,7 +218,7 @@ hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* works
       t.A = Side{ws + p.off_hz, dp2, g.n * dp2, g.n};
     }
     const int64_t piece = w_here ? g.V : p.cols;       // all but the last of whole tiles
-    const bool big = big_tiles(g.n, g.V < piece ? g.V : piece);
+    const bool big = big_tiles(g.n, g.V < piece ? g.V : piece, t.slots * t.nseg, 6);
     const int b = big ? 256 : 128;
     picked = g.teacher && tiles_of(g.V, b) <= kMostTiles;
     if (picked) {
@@ -505,7 +512,7 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
         if (f32) launch_few<float, 1>(f, z, blocks, short_table, s);
         else launch_few<uint16_t, 2>(f, z, blocks, short_table, s);
       } else {
-        const bool big = big_tiles(rows, cols);
+        const bool big = big_tiles(rows, cols, t.slots * t.nseg, 9);
         e = wide ? launch_tiles<EPI_DZB>(t, rows, cols, big, false, s)
                  : launch_tiles<EPI_DZ>(t, rows, cols, big, f32, s);
       }

@@ -24,8 +24,7 @@ namespace {
 // same pattern 107). On the way: fragments of 32 x 32 x 16, 32 bytes a row and
 // load, 162 us; tokens fetched by every wave 160; parts of 16 rows in turn
 // instead of a row's 138; 256 bytes of a row at a time 125; without the barrier
-// it would be 115. From 65 tokens on (fp32 and rows that tiles cannot read in
-// place: 257) the tiles are faster.
+// it would be 115.
 struct FewArgs {
   const void *h, *table;
   int64_t ld, n, V;

@@ -305,9 +305,12 @@ __device__ __forceinline__ void put_raw(const uint16_t* src, int d, int c, bool 
   *reinterpret_cast<uint4*>(dst + c) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
 }
 
-// tokens up to which the table's reading is all that counts: read in place, or
-// where tiles would need a copy of it
-constexpr int kFew = 64, kFewCopied = 256;
+// Tokens up to which the forward pass reads the table by fragments, a group of 64
+// after the other: bf16 that tiles can read in place (65 tokens of 128,000 x 2560:
+// 161 us by tiles, 213 by two groups), bf16 that they cannot (385 wide: 53 us for
+// 128, 60 by tiles), fp32, which tiles need split and placed (320 tokens: 1,228 us,
+// 1,600 by tiles; 512: 1,902 and 1,670)
+constexpr int kFew = 64, kFewOdd = 128, kFewF32 = 320;
 // and rows of the table up to which they are read 32 a block, one block a compute
 // unit (2048 wide, 32 tokens: 15 us for 23 at 8,192 rows, 26 for 24 at 16,384)
 constexpr int64_t kFewShort = 8192;
