@@ -274,8 +274,8 @@ hipError_t launch_head_forward(const HeadPlan& p, const HeadArgs& g, void* works
   j.lse = g.lse;
   j.logits = g.logits;
   const bool alone = g.n <= 2 * kCUs;
-  const unsigned grid = (unsigned)(alone ? g.n : tiles_of(g.n, 8)), nt = alone ? 256 : 1024;
-  auto* join = f32 ? head_join_kernel<float, 8, 1024> : head_join_kernel<uint16_t, 8, 1024>;
+  const unsigned grid = (unsigned)(alone ? g.n : tiles_of(g.n, 16)), nt = alone ? 256 : 1024;
+  auto* join = f32 ? head_join_kernel<float, 16, 1024> : head_join_kernel<uint16_t, 16, 1024>;
   if (alone) join = f32 ? head_join_kernel<float, 1, 256> : head_join_kernel<uint16_t, 1, 256>;
   hipLaunchKernelGGL(join, dim3(grid), dim3(nt), 0, s, j);
   return hipGetLastError();

@@ -79,7 +79,7 @@ __device__ __forceinline__ float teacher_shares(const int32_t* ids, const float*
 
 // Joins the tiles' maxima and sums along the vocabulary and forms the losses:
 // blocks of R rows by NT threads, NT / R threads a row for the join, whole waves
-// a row for the dot products that its targets name. Eight rows by 1024 threads,
+// a row for the dot products that its targets name. Sixteen rows by 1024 threads,
 // or, where there are few, one by 256.
 struct JoinArgs {
   const float2* part;
@@ -319,7 +319,7 @@ constexpr int64_t kFewShort = 8192;
 // passes over the table, fall away (65,536 rows of 2048, 8 tokens: 354 us, 430).
 constexpr int kWide = 256;
 constexpr int kScanBlocks = 512;
-constexpr int kRowBlocks = 512;           // most blocks over rows, four waves each
+constexpr int kRowBlocks = 2048;           // most blocks over rows, four waves each
 
 // What all row kernels know of a call's rows (row pieces: of the piece).
 struct RowArgs {
