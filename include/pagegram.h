@@ -751,12 +751,15 @@ PG_API int pg_orthogonalize(const void* G, int32_t dtype, int64_t n_mat,
  *           another type: PG_EUNSUPPORTED); 1 <= V < 2^31 - 1, and tiles of
  *           128 x 128 fewer than 2^31 (PG_ERANGE)
  *   scale   finite (divided by the temperature too)
- * Logits, statistics and losses are fp32. fp32 operands are multiplied as
- * three bf16 planes (24 bits), sums in fp32. For bf16 operands dz is rounded
- * to bf16 once, scaled, before its two products, whose sums are fp32: dh and
- * dT differ from exact ones by about one more rounding of bf16 (2^-9 of their
- * size in the 2-norm), an fp32 dT of bf16 operands by that too.
- * A row whose logits are not all below +infinity, or NaN, has lse NaN.
+ * Logits, statistics and losses are fp32, as all sums. bf16 operands are
+ * multiplied as they are; fp32 ones as two fp16 halves (22 bits, three products
+ * for one), each row of h placed by a power of two and T by another: elements
+ * of T below 2^-17 of its largest lose bits, in steps of 2^-39 of that. dz is
+ * held in fp16 before its two products (11 bits; fp32 operands: two halves, 22),
+ * each row placed by its own bound, |a_n| + |w_n| below: dh and dT of bf16
+ * operands are off by about 3e-4 of their size (2-norm) before their own
+ * rounding, an fp32 dT too.
+ * A row with a NaN, or a logit of +infinity, has lse NaN.
  * A workspace sized for the largest batch serves every smaller one of the
  * same d, V, k and dtype (256-byte aligned).
  * ------------------------------------------------------------------------ */
@@ -787,6 +790,7 @@ PG_API int pg_head_loss(const void* h, int32_t dtype, int64_t n, int32_t d, int6
  * dloss fp32 [n] of loss and dlse fp32 [n] of lse (nullable: zero):
  *   dz_nv = a_n exp(z_nv - lse_n) - w_n [v = targets[n]],
  *   w_n = dloss_n (0 for a target outside [0, V)), a_n = w_n + dlse_n.
+ * lse is the forward pass's: one far below the true value overflows.
  * A row with a_n = w_n = 0 adds nothing to dT, whatever its h holds, and its
  * dh is zero.
  *   dh  [n] rows of d elements of dtype, stride ld_dh (nullable)
