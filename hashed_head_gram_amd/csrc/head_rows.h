@@ -532,7 +532,7 @@ __global__ __launch_bounds__(256) void head_copy_kernel(RowArgs g, PieceArgs w, 
         e = wave_imax(e);
       }
       const int p = placement(e);
-      if (lane == 0) g.rowf[row] = ldexpf(g.c2, min(-p - pw, 100));
+      if (lane == 0) g.rowf[row] = ldexpf(g.c2, -p - pw);
       if (row < g.rows_pad)
         for (int c = lane * 8; c < g.dp; c += 512)
           put_halves(src, g.d, c, in, p, g.hz + row * g.dp, g.rows_pad * g.dp);

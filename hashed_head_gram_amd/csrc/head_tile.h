@@ -120,7 +120,7 @@ struct Side {
 
 struct TileArgs {
   Side A, B;           // A: the index that lies over lanes, B: over accumulators
-  int nseg;            // 1, or 3 products of halves
+  int nseg;            // 1, 2 (dz alone in halves) or 3 products of halves
   int slots;           // slots of 32 of K in all
   int splits;          // K is shared by this many tiles, each with a result of its own
   int nbm, nbn;        // tiles

@@ -750,15 +750,16 @@ PG_API int pg_orthogonalize(const void* G, int32_t dtype, int64_t n_mat,
  *   table   PG_F32 or PG_BF16 data [V][d] of the same type as h (NF4 or
  *           another type: PG_EUNSUPPORTED); 1 <= V < 2^31 - 1, and tiles of
  *           128 x 128 fewer than 2^31 (PG_ERANGE)
- *   scale   finite (divided by the temperature too)
+ *   scale   finite (divided by the temperature too); h_n . T_v itself within
+ *           fp32's range
  * Logits, statistics and losses are fp32, as all sums. bf16 operands are
  * multiplied as they are; fp32 ones as two fp16 halves (22 bits, three products
  * for one), each row of h placed by a power of two and T by another: elements
  * of T below 2^-17 of its largest lose bits, in steps of 2^-39 of that. dz is
  * held in fp16 before its two products (11 bits; fp32 operands: two halves, 22),
- * each row placed by its own bound, |a_n| + |w_n| below: dh and dT of bf16
- * operands are off by about 3e-4 of their size (2-norm) before their own
- * rounding, an fp32 dT too.
+ * each row placed by its own bound, |a_n| + |w_n| below, for up to 256 rows of
+ * bf16 in two bf16 halves (16 bits): dh and dT of bf16 operands are off by up to
+ * about 1.4e-4 of their size (2-norm) before their own rounding, an fp32 dT too.
  * A row with a NaN, or a logit of +infinity, has lse NaN.
  * A workspace sized for the largest batch serves every smaller one of the
  * same d, V, k and dtype (256-byte aligned).

@@ -387,6 +387,29 @@ def test_values_of_very_different_sizes(n, V, d, dt):
     within("dw", o.dw, rt, bt)
 
 
+@pytest.mark.parametrize("n", [30, 400])
+def test_scale_undoes_large_operands(n):
+    """Logits of order one from very large and very small operands; h . T itself
+    has to lie in fp32's range (2^130, say, is no fp32 value, scaled or not)."""
+    V, d = 700, 96
+    c = Case(24, n, V, d, "f32")
+    h0, t0 = c.h.clone(), c.table.clone()
+    tok = some_targets(c.g, n, V)
+    o = Loss(c, tok)
+    o.forward()
+    o.backward()
+    want = o.outputs()
+    # powers of two throughout: the same bits, but for the gradients' exponents
+    for eh, et in ((40, 70), (-60, -50), (70, -75)):
+        c.h.copy_(h0 * 2.0 ** eh)
+        c.table.copy_(t0 * 2.0 ** et)
+        c.scale = 2.0 ** -(eh + et)
+        o.forward()
+        # one more rounding of the scaled logits where they are single dot products
+        for got, ref in zip((o.loss, o.lse), want[:2]):
+            within("loss", got, f64(ref), 1e-5 * np.ones(n))
+
+
 @pytest.mark.parametrize("n", [20, 300])
 def test_flat_and_certain(n):
     """scale 0 makes every token as likely; large logits a certain one."""
