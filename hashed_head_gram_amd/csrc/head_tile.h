@@ -332,9 +332,14 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
   constexpr bool DZ = EPI == EPI_DZ || EPI == EPI_DZB;
   constexpr int NV = (DZ ? 2 : 0) + (EPI != EPI_OUT && F16 ? 1 : 0);
   auto picks_of = [&](const Tile& t, int& count) -> const uint32_t* {
-    const int* s = g.starts + (int64_t)t.bm * (g.tiles + 1) + g.tile0 + t.bn;
-    const int a = __builtin_amdgcn_readfirstlane(s[0]);
-    count = __builtin_amdgcn_readfirstlane(s[1]) - a;
+    // by the scalar cache (written by an earlier launch): a vector load's wait
+    // would drain the ring
+    const int at = __builtin_amdgcn_readfirstlane((int)(g.tile0 + t.bn));
+    const int row = __builtin_amdgcn_readfirstlane((int)t.bm);
+    const int* first = g.starts + (int64_t)row * (g.tiles + 1) + at;
+    const auto* s = (const __attribute__((address_space(4))) int*)first;
+    const int a = s[0];
+    count = s[1] - a;
     return g.list + t.bm * g.cap + a;
   };
   // and its entries, behind which the list has room for a whole load
