@@ -454,9 +454,18 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
     r.hp = reinterpret_cast<uint16_t*>(ws + p.off_h);
     const bool h_here = in_place(g.dtype, g.d, g.ld_h, r.h);
     r.hz = h_here ? nullptr : reinterpret_cast<uint16_t*>(ws + p.off_hz);
+    // dz by fragments (of 128 fp32 tokens two groups of 64 took longer than the
+    // tiles: 2,048 rows of 2048, 111 us and 95); in fp32 that pass finds T's
+    // largest element too, unless other pieces need it first
+    const bool few = n <= kFew && (f32 || wide);
+    if (few && f32) r.hz = nullptr;
+    if (few && f32 && g.n == n && g.V <= p.cols) {
+      r.nparts_w = kTops;
+      r.clear_w = 1;
+    }
     r.c2 = (float)((double)g.scale * (double)g.inv_tau * 1.4426950408889634);
     // T's exponent is the same for every piece of the rows
-    const unsigned grid = r.nparts_h + (first_rows ? r.nparts_w : 0);
+    const unsigned grid = r.nparts_h + (first_rows && !r.clear_w ? r.nparts_w : 0);
     if (f32)
       hipLaunchKernelGGL((head_stats_kernel<float>), dim3(grid), dim3(256), 0, s, r, r.nparts_h);
     else
@@ -481,8 +490,16 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
         copies.rows_pad = odd ? 128 : 0;
         copies.wz = wz;
       }
-      launch_copy(f32, r, copies, first && !wide, s);
       const int64_t ldz = cols, plane = rows * cols;
+      if (few) {
+        const FewArgs f{r.h, w.src, g.ld_h, n, c, g.d, 1, r.c2, nullptr};
+        const FewDz z{r.a, r.lse2, dz, ldz, plane, (int)rows, r.clear_w ? r.part_w : nullptr};
+        const bool short_table = c <= kFewShort;
+        const unsigned blocks = (unsigned)(cols / (short_table ? 32 : 128));
+        if (f32) launch_few<float, 1>(f, z, blocks, short_table, s);
+        else launch_few<uint16_t, 2>(f, z, blocks, short_table, s);
+      }
+      launch_copy(f32, r, copies, first && !wide, s);
 
       TileArgs t{};
       t.A = h_here ? Side{static_cast<const uint8_t*>(r.h), g.ld_h * 2, 0, n}
@@ -504,14 +521,7 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
       t.Mpad = rows;
       t.Vpad = cols;
       hipError_t e = hipSuccess;
-      if (n <= kFew && (f32 || wide)) {
-        const FewArgs f{r.h, w.src, g.ld_h, n, c, g.d, 1, r.c2, nullptr};
-        const FewDz z{r.a, r.lse2, dz, ldz, plane, (int)rows};
-        const bool short_table = c <= kFewShort;
-        const unsigned blocks = (unsigned)(cols / (short_table ? 32 : 128));
-        if (f32) launch_few<float, 1>(f, z, blocks, short_table, s);
-        else launch_few<uint16_t, 2>(f, z, blocks, short_table, s);
-      } else {
+      if (!few) {
         const bool big = big_tiles(rows, cols, t.slots * t.nseg, 9);
         e = wide ? launch_tiles<EPI_DZB>(t, rows, cols, big, false, s)
                  : launch_tiles<EPI_DZ>(t, rows, cols, big, f32, s);

@@ -40,7 +40,27 @@ struct FewDz {
   uint16_t* dz;
   int64_t ldz, plane;      // elements
   int rows_pad;
+  int* top;                // fp32: kTops exponents, raised to T's largest element's (nullable)
 };
+constexpr int kTops = 512;
+
+// Largest finite magnitude of a fragment, and m.
+__device__ __forceinline__ float few_top(const Raw8<float>& v, float m) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const float a = fabsf(v.v[u]);
+    m = a < INFINITY ? fmaxf(m, a) : m;
+  }
+  return m;
+}
+// A wave's share of the exponent of T's largest element, whose rows dz reads in
+// fp32 in any case (65,536 rows of 2048, 8 tokens: 706 us, 811 with a pass of its own).
+__device__ __forceinline__ void few_put_top(const FewDz& z, float m) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  // (a maximum: the order of the waves does not matter)
+  if (z.top && (threadIdx.x & 63) == 0) atomicMax(z.top + blockIdx.x % kTops, exponent_of(m));
+}
 // dz of token tok at four columns from col on, from their logits in base 2; MODE
 // 1: fp16, two halves where F32; 2: two bf16 halves.
 template <int MODE, bool F32>
@@ -147,6 +167,7 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
     hp[u] = static_cast<const T*>(g.h) + (x0 + x < g.n ? x0 + x : g.n - 1) * g.ld + hc[u];
   }
   f32x4_t acc[TB][2] = {};
+  float top = 0.f;
   Raw8<T> hr[HL], wr[2][ST][2];
   auto load = [&](int k, Raw8<T> (&w)[ST][2]) {
     const bool all = k + KC <= g.d;
@@ -179,7 +200,10 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
     for (int s = 0; s < ST; ++s) {
       uint4 wf[2][P];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) planes_of(w[s][r], wf[r]);
+      for (int r = 0; r < 2; ++r) {
+        planes_of(w[s][r], wf[r]);
+        if constexpr (F32 && DZ == 1) top = few_top(w[s][r], top);
+      }
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
         uint4 hf[P];
@@ -246,6 +270,7 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
   }
   if constexpr (DZ != 0) {
     few_dz_zero<DZ, F32>(dz, 16 * TB, (int64_t)tile * 128, 128);
+    if constexpr (F32 && DZ == 1) few_put_top(dz, top);
     return;
   }
   __syncthreads();
@@ -286,6 +311,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_f
     hp[t] = static_cast<const T*>(g.h) + (x < g.n ? x : g.n - 1) * g.ld + kq * 8;
   }
   f32x4_t acc[TB][2] = {};
+  float top = 0.f;
   struct Step {
     Raw8<T> w[2], h[TB];
   };
@@ -306,7 +332,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_f
     for (int s = 0; s < ST; ++s) {
       uint4 wf[2][P];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) planes_of(x[s].w[r], wf[r]);
+      for (int r = 0; r < 2; ++r) {
+        planes_of(x[s].w[r], wf[r]);
+        if constexpr (F32 && DZ == 1) top = few_top(x[s].w[r], top);
+      }
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
         uint4 hf[P];
@@ -364,6 +393,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_f
     }
   }
   if constexpr (DZ != 0) few_dz_zero<DZ, F32>(z, 16 * TB, v0, 32);
+  if constexpr (F32 && DZ == 1) few_put_top(z, top);
 }
 
 }  // namespace

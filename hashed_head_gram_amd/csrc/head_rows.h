@@ -3,7 +3,7 @@
 // sparse positions and the sums of split products.
 #pragma once
 
-#include "head_tile.h"
+#include "head_few.h"
 
 namespace pg {
 namespace {
@@ -319,6 +319,7 @@ constexpr int64_t kFewShort = 8192;
 // passes over the table, fall away (65,536 rows of 2048, 8 tokens: 354 us, 430).
 constexpr int kWide = 256;
 constexpr int kScanBlocks = 512;
+static_assert(kTops <= kScanBlocks, "they share part_w");
 constexpr int kRowBlocks = 2048;           // most blocks over rows, four waves each
 
 // What all row kernels know of a call's rows (row pieces: of the piece).
@@ -341,6 +342,7 @@ struct RowArgs {
   int *part_h, *part_w;             // exponents by block: of 2^row_exp h, of T
   int *all_h, *all_w;               // what dT and dh undo: minus their placements
   int nparts_h, nparts_w;
+  int clear_w;                      // start part_w: a later kernel raises it
   int placed;                       // dz in fp16, placed by powers of two; 0: two bf16 halves
   uint16_t *hp, *hz;                // fp16 h for dT; h for the logits (NULL: read in place)
   float c2;
@@ -349,7 +351,7 @@ struct RowArgs {
 // First kernel of the backward pass. The first `row_blocks` blocks, a wave a
 // row: the weight a of the row's softmax (with scale), its lse in base 2, the
 // gradient at its sparse positions, and the placement of its dz. The others:
-// the exponent of T's largest element.
+// the exponent of T's largest element (with clear_w there are none).
 template <typename T>
 __global__ __launch_bounds__(256) void head_stats_kernel(RowArgs g, int row_blocks) {
   __shared__ int sh[4];
@@ -363,6 +365,8 @@ __global__ __launch_bounds__(256) void head_stats_kernel(RowArgs g, int row_bloc
          i += step)
       top = max(top, exponent_of8(t + i, (int)(count - i < 8 ? count - i : 8)));
   } else {
+    if (g.clear_w && blockIdx.x == 0)
+      for (int i = threadIdx.x; i < g.nparts_w; i += 256) g.part_w[i] = kNone;
     for (int64_t row = (int64_t)blockIdx.x * 4 + wave; row < g.vec_pad; row += row_blocks * 4) {
       const T* hr = static_cast<const T*>(g.h) + row * g.ld;
       float a = 0.f, l2 = 0.f, w = 0.f;
@@ -526,16 +530,18 @@ __global__ __launch_bounds__(256) void head_copy_kernel(RowArgs g, PieceArgs w, 
     const T* src = static_cast<const T*>(g.h) + (in ? row : 0) * g.ld;
     if constexpr (F32) {
       // the logits' copy, and the factor that undoes its placement
-      int e = kNone;
-      if (in) {
-        for (int c = lane * 8; c < g.d; c += 512) e = max(e, exponent_of8(src + c, g.d - c));
-        e = wave_imax(e);
+      if (g.hz) {
+        int e = kNone;
+        if (in) {
+          for (int c = lane * 8; c < g.d; c += 512) e = max(e, exponent_of8(src + c, g.d - c));
+          e = wave_imax(e);
+        }
+        const int p = placement(e);
+        if (lane == 0) g.rowf[row] = ldexpf(g.c2, -p - pw);
+        if (row < g.rows_pad)
+          for (int c = lane * 8; c < g.dp; c += 512)
+            put_halves(src, g.d, c, in, p, g.hz + row * g.dp, g.rows_pad * g.dp);
       }
-      const int p = placement(e);
-      if (lane == 0) g.rowf[row] = ldexpf(g.c2, -p - pw);
-      if (row < g.rows_pad)
-        for (int c = lane * 8; c < g.dp; c += 512)
-          put_halves(src, g.d, c, in, p, g.hz + row * g.dp, g.rows_pad * g.dp);
     } else {
       if (g.hz && row < g.rows_pad)
         for (int c = lane * 8; c < g.dp; c += 512) put_raw(src, g.d, c, in, g.hz + row * g.dp);

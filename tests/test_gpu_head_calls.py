@@ -387,6 +387,32 @@ def test_values_of_very_different_sizes(n, V, d, dt):
     within("dw", o.dw, rt, bt)
 
 
+@pytest.mark.parametrize("at", [0, 0.5, 1])
+@pytest.mark.parametrize("n", [1, 30, 64])
+@pytest.mark.parametrize("V,d", [(1001, 40), (9001, 77)])
+def test_one_element_far_larger_than_the_rest(V, d, n, at):
+    """The table's copies are placed by its largest element, wherever it stands."""
+    c = Case(25, n, V, d, "f32")
+    row, col = int(at * (V - 1)), int(at * (d - 1))
+    c.h[:, col] = 0                                   # the logits do not see it
+    c.table[row, col] = -2.0 ** 20
+    c.H, c.T = f64(c.h), f64(c.table)
+    H, T = np.abs(c.H), np.abs(c.T)
+    c.z = oh.logits(c.H, c.T, 1.0)
+    c.ez = H @ T.T * products("f32", d) + 3 * U * np.abs(c.z) + 2.0 ** -39 * (
+        H.sum(1)[:, None] * T.max() + H.max(1)[:, None] * T.sum(1)[None])
+    o = Loss(c, some_targets(c.g, n, V), zloss=True)
+    o.lse.copy_(f32(oh.log_sum_exp(c.z)))
+    for _ in range(2):
+        o.backward()
+        rh, bh, rt, bt = grad_bounds(o)
+        within("dh", o.dh, rh, bh)
+        within("dw", o.dw, rt, bt)
+        c.table[row, col] = 2.0 ** 3                  # nothing of the call before stays
+        c.T = f64(c.table)
+    assert o.w2.intact()
+
+
 @pytest.mark.parametrize("n", [30, 400])
 def test_scale_undoes_large_operands(n):
     """Logits of order one from very large and very small operands; h . T itself
