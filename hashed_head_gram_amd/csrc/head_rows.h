@@ -160,8 +160,11 @@ __global__ __launch_bounds__(NT) void head_join_kernel(JoinArgs g) {
   if (wave % WR || row >= g.n) return;
   const float l = lse_s[r];
   if (!g.teacher) {
+    // The sum is never below one of its terms; of a certain token the two, summed
+    // in different orders, may come out the other way round (NaN stays).
     const int id = g.ids[row];
-    if (lane == 0) g.loss[row] = id >= 0 && id < g.V ? l - zs[r][0] : 0.f;
+    const float x = id >= 0 && id < g.V ? l - zs[r][0] : 0.f;
+    if (lane == 0) g.loss[row] = x < 0.f ? 0.f : x;
     return;
   }
   int id[kPer];

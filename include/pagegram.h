@@ -777,7 +777,7 @@ PG_API int64_t pg_head_distill_backward_workspace_size(int64_t n, int32_t d, int
 /*
  * pg_head_loss -- cross entropy of each row against a target token:
  *   lse_n  = log sum_v exp(z_nv)
- *   loss_n = lse_n - z_n,targets[n]; 0 for a target outside [0, V)
+ *   loss_n = lse_n - z_n,targets[n], never below 0; 0 for a target outside [0, V)
  * targets int32 [n]; loss, lse fp32 [n] (device), lse written for every row.
  * The mean over a batch is the caller's, by way of dloss.
  */
