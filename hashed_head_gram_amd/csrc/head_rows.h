@@ -46,6 +46,8 @@ constexpr int kPer = kMaxK / 64;           // of them a lane
 
 // The teacher's shares of a row by one wave: q[u] belongs to entry lane + 64 u,
 // 0 where there is none. Returns the sum of q log q; any: an entry has weight.
+// Differences before the division by the temperature: what is divided may leave
+// fp32's range, and they are exact between close values.
 __device__ __forceinline__ float teacher_shares(const int32_t* ids, const float* t, int k,
                                                 int64_t V, float inv_tau, int lane, int (&id)[kPer],
                                                 float (&q)[kPer], bool& any) {
@@ -55,7 +57,7 @@ __device__ __forceinline__ float teacher_shares(const int32_t* ids, const float*
     const int j = lane + 64 * u;
     id[u] = j < k ? ids[j] : -1;
     if (id[u] < 0 || id[u] >= V) id[u] = -1;
-    x[u] = id[u] >= 0 ? t[j] * inv_tau : -INFINITY;
+    x[u] = id[u] >= 0 ? t[j] : -INFINITY;
     m = fmaxf(m, x[u]);
   }
   m = wave_max(m);
@@ -63,7 +65,7 @@ __device__ __forceinline__ float teacher_shares(const int32_t* ids, const float*
   float s = 0.f;
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    q[u] = id[u] >= 0 ? expf(x[u] - ref) : 0.f;
+    q[u] = id[u] >= 0 ? expf((x[u] - ref) * inv_tau) : 0.f;
     s += q[u];
   }
   s = wave_sum(s);

@@ -1,5 +1,5 @@
 """The head's losses at values where a rounding, or the range of a number format,
-decides.
+decides: certain tokens, teachers at the ends of fp32.
 Helpers are those of test_gpu_head.py and test_gpu_head_calls.py."""
 import numpy as np
 import pytest
@@ -7,7 +7,7 @@ import torch
 
 from oracle import head as oh
 from tests.test_gpu_head import U, Case, dev, f64, within
-from tests.test_gpu_head_calls import Loss
+from tests.test_gpu_head_calls import Distill, Loss
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +34,40 @@ def test_no_cross_entropy_below_zero(dt, n, scale):
         H, T = np.abs(c.H), np.abs(c.T)
         ez += 2.0 ** -39 * (H.sum(1)[:, None] * T.max() + H.max(1)[:, None] * T.sum(1)[None])
     within("loss", o.loss, ref, c.lse_bound(z, ez, lse) + ez.max(1) + 2 * U * np.abs(z).max(1))
+
+
+@pytest.mark.parametrize("n", [40, 300])
+def test_teachers_at_the_ends_of_fp32(n):
+    """Shares depend on the differences of a teacher's logits over the
+    temperature: masks of the type's lowest value, rows of nothing else, and
+    values that leave fp32's range when divided."""
+    V, d, k, tau = 900, 96, 5, 0.25
+    low, high = np.finfo(np.float32).min, np.finfo(np.float32).max
+    c = Case(32, n, V, d, "bf16")
+    ids = np.argsort(c.g.random((n, V)), axis=1)[:, :k]
+    teacher = c.g.normal(size=(n, k)).astype(np.float32)
+    teacher[0::6, 2:] = low                # masked entries
+    teacher[1::6] = low                    # all the same: equal shares
+    teacher[2::6] = high
+    teacher[3::6, 0] = high                # one takes all
+    teacher[4::6] = -np.inf                # none at all
+    o = Distill(c, ids, teacher, tau)
+    o.forward()
+    o.backward()
+    ref, lse, zk = oh.distill(c.H, c.T, ids, teacher, tau)
+    # shares to 2^-20: differences of at most 20 over tau, exponentials, a sum of 5
+    b = tau ** 2 * (c.lse_bound(c.z / tau, c.ez / tau, lse) + c.ez.max(1) / tau
+                    + 2.0 ** -20 * (10 + np.abs(c.z).max(1) / tau + np.abs(lse)))
+    within("loss", o.loss, ref, b)
+    assert bool((o.loss[4::6] == 0).all()) and bool((o.dh[4::6] == 0).all())
+    # the gradient of equal shares is not zero
+    assert bool((o.dh[1::6] != 0).any(1).all()) and bool((o.dh[2::6] != 0).any(1).all())
+    dz = oh.distill_dz(c.z, ids, teacher, f64(o.lse), f64(o.dl), tau)
+    rh, _ = oh.grads(dz, c.H, c.T)
+    err = np.linalg.norm(f64(o.dh) - rh, axis=1)
+    # half a step of bf16, dz's 2^-12 and the exponentials' error, in the 2-norm of a row
+    p = np.abs(f64(o.dl))[:, None] * tau * np.exp(c.z / tau - f64(o.lse)[:, None])
+    ez = np.expm1(c.ez / tau + 6 * U * np.abs(c.z) / tau + 2.0 ** -18)
+    bound = 2.0 ** -8 * np.linalg.norm(rh, axis=1) + np.linalg.norm(
+        (p * ez + np.abs(dz) * (2.0 ** -11 + 2.0 ** -18)) @ np.abs(c.T), axis=1) + 1e-30
+    assert np.all(err <= bound), (err / bound).max()
