@@ -184,7 +184,8 @@ __global__ __launch_bounds__(NT) void head_join_kernel(JoinArgs g) {
     }
   }
   x = wave_sum(x);
-  if (lane == 0) g.loss[row] = any ? (ent + x) / (g.inv_tau * g.inv_tau) : 0.f;
+  // (the square may leave fp32's range)
+  if (lane == 0) g.loss[row] = any ? (ent + x) / g.inv_tau / g.inv_tau : 0.f;
 }
 
 // Sorts the entries of each row tile by column tile: a block a row tile, counts,

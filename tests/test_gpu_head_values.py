@@ -1,5 +1,5 @@
 """The head's losses at values where a rounding, or the range of a number format,
-decides: certain tokens, teachers at the ends of fp32.
+decides: certain tokens, teachers at the ends of fp32, extreme temperatures.
 Helpers are those of test_gpu_head.py and test_gpu_head_calls.py."""
 import numpy as np
 import pytest
@@ -71,3 +71,17 @@ def test_teachers_at_the_ends_of_fp32(n):
     bound = 2.0 ** -8 * np.linalg.norm(rh, axis=1) + np.linalg.norm(
         (p * ez + np.abs(dz) * (2.0 ** -11 + 2.0 ** -18)) @ np.abs(c.T), axis=1) + 1e-30
     assert np.all(err <= bound), (err / bound).max()
+
+
+def test_extreme_temperatures():
+    """tau^2 and its reciprocal may leave fp32's range where the loss does not:
+    tau = 2^-65, logits of about 2^-45, a loss of about 2^-110."""
+    n, V, d, k = 30, 500, 64, 4
+    tau = 2.0 ** -65
+    c = Case(33, n, V, d, "bf16", 2.0 ** -45)
+    ids = np.argsort(c.g.random((n, V)), axis=1)[:, :k]
+    o = Distill(c, ids, np.zeros((n, k), np.float32), tau)
+    o.forward()
+    ref = oh.distill(c.H, c.T, ids, np.zeros((n, k)), tau, 2.0 ** -45)[0]
+    assert np.all(ref > 2.0 ** -126)
+    within("loss", o.loss, ref, 1e-4 * ref + tau * (c.ez.max(1) * 2))
