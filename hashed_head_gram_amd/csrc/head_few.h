@@ -41,6 +41,13 @@ struct FewDz {
   int64_t ldz, plane;      // elements
   int rows_pad;
   int* top;                // fp32: kTops exponents, raised to T's largest element's (nullable)
+  // fp16: levels of the columns, and what they need of the sparse positions
+  const int32_t* sidx;
+  const float* sval;
+  int count;
+  int64_t v0;              // vocabulary row of column 0
+  uint8_t* level;          // [ldz]: all tokens are one group
+  int* any;
 };
 constexpr int kTops = 512;
 
@@ -61,32 +68,67 @@ __device__ __forceinline__ void few_put_top(const FewDz& z, float m) {
   // (a maximum: the order of the waves does not matter)
   if (z.top && (threadIdx.x & 63) == 0) atomicMax(z.top + blockIdx.x % kTops, exponent_of(m));
 }
-// dz of token tok at four columns from col on, from their logits in base 2; MODE
-// 1: fp16, two halves where F32; 2: two bf16 halves.
-template <int MODE, bool F32>
-__device__ __forceinline__ void few_dz(const FewDz& z, int64_t tok, int64_t n, int64_t col,
-                                       const float (&v)[4]) {
-  using H = Half<MODE == 1>;
+// dz of token tok at four columns from their logits in base 2.
+__device__ __forceinline__ void few_exp(const FewDz& z, int64_t tok, int64_t n, float (&v)[4]) {
   const float a = tok < n ? z.a[tok] : 0.f, l = tok < n ? z.lse2[tok] : 0.f;
-  float f[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) f[q] = a == 0.f ? 0.f : a * __builtin_amdgcn_exp2f(v[q] - l);
+  for (int q = 0; q < 4; ++q) v[q] = a == 0.f ? 0.f : a * __builtin_amdgcn_exp2f(v[q] - l);
+}
+// Largest |dz| at the sparse positions of the block's COLS columns from col on, as bits.
+template <int COLS>
+__device__ __forceinline__ void few_stops(const FewDz& z, int64_t col, uint32_t* stop) {
+  if (threadIdx.x < COLS) stop[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll 4
+  for (int i = threadIdx.x; i < z.count; i += 256) {
+    const int64_t v = z.sidx[i] - z.v0 - col;
+    if (v >= 0 && v < COLS) atomicMax(stop + v, __float_as_uint(z.sval[i]) & 0x7FFFFFFFu);
+  }
+  __syncthreads();
+}
+// Stores it; MODE 1: fp16, two halves (fp32 operands); 2: two bf16 halves.
+template <int MODE>
+__device__ __forceinline__ void few_dz(const FewDz& z, int64_t tok, int64_t col,
+                                       const float (&f)[4]) {
+  using H = Half<MODE == 1>;
   const uint2 w = make_uint2(H::pack(f[0], f[1]), H::pack(f[2], f[3]));
   uint16_t* to = z.dz + tok * z.ldz + col;
   *reinterpret_cast<uint2*>(to) = w;
-  if constexpr (F32 || MODE == 2)
-    *reinterpret_cast<uint2*>(to + z.plane) =
-        make_uint2(H::pack(f[0] - H::lo(w.x), f[1] - H::hi(w.x)),
-                   H::pack(f[2] - H::lo(w.y), f[3] - H::hi(w.y)));
+  *reinterpret_cast<uint2*>(to + z.plane) =
+      make_uint2(H::pack(f[0] - H::lo(w.x), f[1] - H::hi(w.x)),
+                 H::pack(f[2] - H::lo(w.y), f[3] - H::hi(w.y)));
 }
 // Zeros in dz's rows from `from` on, `cols` (a multiple of 4) from col on; by the block.
-template <int MODE, bool F32>
 __device__ __forceinline__ void few_dz_zero(const FewDz& z, int from, int64_t col, int cols) {
   const int per = cols / 4;
   for (int i = threadIdx.x; i < (z.rows_pad - from) * per; i += 256) {
     uint16_t* to = z.dz + (from + i / per) * z.ldz + col + i % per * 4;
     *reinterpret_cast<uint2*>(to) = make_uint2(0, 0);
-    if constexpr (F32 || MODE == 2) *reinterpret_cast<uint2*>(to + z.plane) = make_uint2(0, 0);
+    *reinterpret_cast<uint2*>(to + z.plane) = make_uint2(0, 0);
+  }
+}
+
+// Lifts four columns of one row block: from col on, their largest |dz| in m as bits
+// of fp32 (of this lane's tokens; the 16 lanes fr have the others), f(t, q) theirs.
+template <int TB, typename F>
+__device__ __forceinline__ void few_lift(const FewDz& z, int64_t col, uint32_t (&m)[4], int fr,
+                                         F f) {
+  uint32_t l[4];
+  bool lifted = false;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) m[q] = max(m[q], (uint32_t)__shfl_xor((int)m[q], o));
+    l[q] = level_of(m[q] >> 16);
+    const bool some = l[q] != kFlat && l[q] != kEmpty;
+    lifted |= some;
+    const float by = __uint_as_float((127u + (some ? l[q] : 0u)) << 23);
+#pragma unroll
+    for (int t = 0; t < TB; ++t) f(t, q) *= by;
+  }
+  if (fr == 0) {
+    *reinterpret_cast<uint32_t*>(z.level + col) = l[0] | l[1] << 8 | l[2] << 16 | l[3] << 24;
+    if (lifted) *z.any = 1;
   }
 }
 
@@ -131,6 +173,7 @@ __device__ __forceinline__ void mma_planes(const uint4 (&w)[P], const uint4 (&h)
 
 template <typename T, int TB, int DZ>
 __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
+  static_assert(DZ == 0 || (DZ == 1) == (sizeof(T) == 4), "dz of fp32 operands is fp16");
   constexpr bool F32 = sizeof(T) == 4;
   constexpr int ST = F32 ? 2 : 8;                    // steps of 32 of K under way
   constexpr int P = F32 ? 3 : 1, KC = 32 * ST;
@@ -139,6 +182,7 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
   constexpr int HL = (CH + 255) / 256;               // of them a thread
   __shared__ __attribute__((aligned(256))) uint8_t hs[2][P][16 * TB * RB];
   __shared__ float2 red[4][16 * TB];
+  __shared__ uint32_t stop[DZ == 1 ? 128 : 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, fr = lane & 15, kq = lane >> 4;
   // a tile's groups run 8 blocks apart: on one XCD, where they share its L2
   const uint32_t id = blockIdx.x;
@@ -236,19 +280,41 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
   }
 
   // a lane has rows 16 r + 4 kq + q of the wave's 32, token 16 t + fr
+  if constexpr (DZ != 0) {
+    float f[TB][2][4];
 #pragma unroll
-  for (int t = 0; t < TB; ++t) {
-    float z[2][4], m = -INFINITY;
-    if constexpr (DZ != 0) {
+    for (int t = 0; t < TB; ++t)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          z[r][q] = v0 + r * 16 + 4 * kq + q < g.V ? acc[t][r][q] * g.c2 : -INFINITY;
-        few_dz<DZ, F32>(dz, t * 16 + fr, g.n, v0 + r * 16 + 4 * kq, z[r]);
+          f[t][r][q] = v0 + r * 16 + 4 * kq + q < g.V ? acc[t][r][q] * g.c2 : -INFINITY;
+        few_exp(dz, t * 16 + fr, g.n, f[t][r]);
       }
-      continue;
+    if constexpr (DZ == 1) few_stops<128>(dz, (int64_t)tile * 128, stop);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int64_t col = v0 + r * 16 + 4 * kq;
+      if constexpr (DZ == 1) {
+        uint32_t m[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          m[q] = stop[wave * 32 + r * 16 + 4 * kq + q];
+#pragma unroll
+          for (int t = 0; t < TB; ++t) m[q] = max(m[q], __float_as_uint(fabsf(f[t][r][q])));
+        }
+        few_lift<TB>(dz, col, m, fr, [&](int t, int q) -> float& { return f[t][r][q]; });
+      }
+#pragma unroll
+      for (int t = 0; t < TB; ++t) few_dz<DZ>(dz, t * 16 + fr, col, f[t][r]);
     }
+    few_dz_zero(dz, 16 * TB, (int64_t)tile * 128, 128);
+    if constexpr (F32 && DZ == 1) few_put_top(dz, top);
+    return;
+  }
+#pragma unroll
+  for (int t = 0; t < TB; ++t) {
+    float z[2][4], m = -INFINITY;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -267,11 +333,6 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
     if (kq == 0) red[wave][t * 16 + fr] = make_float2(m, s);
-  }
-  if constexpr (DZ != 0) {
-    few_dz_zero<DZ, F32>(dz, 16 * TB, (int64_t)tile * 128, 128);
-    if constexpr (F32 && DZ == 1) few_put_top(dz, top);
-    return;
   }
   __syncthreads();
   const int x = threadIdx.x;
@@ -296,7 +357,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_f
     FewArgs g, FewDz z) {
   constexpr bool F32 = sizeof(T) == 4;
   constexpr int ST = F32 ? 2 : 4, P = F32 ? 3 : 1, KC = 32 * ST;
+  static_assert(DZ == 0 || (DZ == 1) == F32, "dz of fp32 operands is fp16");
   __shared__ f32x4_t join[4][TB * 2][64];
+  __shared__ uint32_t stop[DZ == 1 ? 32 : 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, fr = lane & 15, kq = lane >> 4;
   const int64_t v0 = (int64_t)blockIdx.x * 32;
   const T *wp[2], *hp[TB];
@@ -362,9 +425,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_f
     for (int r = 0; r < 2; ++r) join[wave][t * 2 + r][lane] = acc[t][r];
   __syncthreads();
   // wave t has token block t from here on: rows 16 r + 4 kq + q, token 16 t + fr
+  const int64_t tok = wave * 16 + fr;
+  float v[2][4], m = -INFINITY;
   if (wave < TB) {
-    const int64_t tok = wave * 16 + fr;
-    float v[2][4], m = -INFINITY;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const f32x4_t sum = (join[0][wave * 2 + r][lane] + join[1][wave * 2 + r][lane]) +
@@ -389,10 +452,34 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_f
       if (kq == 0 && tok < g.n) g.part[(int64_t)blockIdx.x * g.n + tok] = make_float2(m, s);
     } else {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) few_dz<DZ, F32>(z, tok, g.n, v0 + r * 16 + 4 * kq, v[r]);
+      for (int r = 0; r < 2; ++r) few_exp(z, tok, g.n, v[r]);
     }
   }
-  if constexpr (DZ != 0) few_dz_zero<DZ, F32>(z, 16 * TB, v0, 32);
+  if constexpr (DZ == 1) {
+    // the token blocks' largest meet where the sparse positions' are
+    few_stops<32>(z, v0, stop);
+    if (wave < TB)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          atomicMax(stop + r * 16 + 4 * kq + q, __float_as_uint(fabsf(v[r][q])));
+    __syncthreads();
+    if (wave < TB)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        uint32_t m4[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) m4[q] = stop[r * 16 + 4 * kq + q];
+        few_lift<1>(z, v0 + r * 16 + 4 * kq, m4, fr, [&](int, int q) -> float& { return v[r][q]; });
+      }
+  }
+  if constexpr (DZ != 0) {
+    if (wave < TB)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) few_dz<DZ>(z, tok, v0 + r * 16 + 4 * kq, v[r]);
+    few_dz_zero(z, 16 * TB, v0, 32);
+  }
   if constexpr (F32 && DZ == 1) few_put_top(z, top);
 }
 

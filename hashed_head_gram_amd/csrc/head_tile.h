@@ -76,6 +76,35 @@ __device__ __forceinline__ int exponent_of(float x) {
   return a > 0.f && a < INFINITY ? ilogbf(a) : kNone;
 }
 
+// Levels of dz. A row of dz in fp16 is placed by its own bound, which leaves 28
+// bits above fp16's smallest normal number; a vocabulary row that no token finds
+// likely lies below them. Its column is then lifted by a power of two, the level:
+// by the largest |dz| of a group of rows, kFlat where that is 2^kRare or more (fp16
+// steps are 2^-19 of it at most), else in steps of kLift, so that the groups of a
+// column mostly agree; kEmpty for zeros alone. One byte a group and column. Later
+// all groups of a column come to its lowest level, dT undoes it, and T's copy for
+// dh carries its inverse.
+constexpr int kFlat = 0, kEmpty = 255;
+constexpr int kRare = -6;                 // against bounds of 2^kTop
+constexpr int kLift = 20;                 // a lifted column's largest: 2^kRare to 2^(kRare + kLift)
+static_assert(kRare + kLift <= kTop && 126 + kLift < kEmpty, "in fp16, and in a byte");
+// of the upper 16 bits of the largest |dz| in fp32
+__device__ __forceinline__ uint32_t level_of(uint32_t top16) {
+  if (top16 == 0) return kEmpty;
+  const int e = (int)(top16 >> 7) - 127;             // NaN and infinity: 128
+  return e < kRare ? (uint32_t)((kRare - (e < -126 ? -126 : e) + kLift - 1) / kLift * kLift) : kFlat;
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  typedef uint16_t u16v2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16v2_t, a),
+                                                                __builtin_bit_cast(u16v2_t, b)));
+}
+// x of another lane of the 16, by a DPP control word.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, false);
+}
+
 // s_waitcnt with only a vmcnt limit (vmcnt[3:0], expcnt[6:4], lgkmcnt[11:8],
 // vmcnt[5:4] in bits [15:14]).
 template <int N>
@@ -143,6 +172,9 @@ struct TileArgs {
   uint16_t* dz;
   int64_t ldz, dz_plane;   // elements
   int64_t Mpad, Vpad;      // rows and columns of dz that exist
+  const uint32_t* stop;    // largest |dz| at the sparse positions by column, as bits of fp32
+  uint8_t* level;          // [groups of rows of a wave's tiles][ldz]
+  int* any;                // set where a level is neither kFlat nor kEmpty
   // products
   void* out;
   int64_t ld_out, split_out;   // elements; between the results of two splits
@@ -331,6 +363,8 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
   constexpr bool LSE = EPI == EPI_LSE || EPI == EPI_PICK;
   constexpr bool DZ = EPI == EPI_DZ || EPI == EPI_DZB;
   constexpr int NV = (DZ ? 2 : 0) + (EPI != EPI_OUT && F16 ? 1 : 0);
+  constexpr int NC = EPI == EPI_DZ ? BN / 64 : 0;    // loads of a vector along the columns
+  static_assert(2 * NC * 256 <= G::kRed, "it lies where maxima and sums do");
   auto picks_of = [&](const Tile& t, int& count) -> const uint32_t* {
     // by the scalar cache (written by an earlier launch): a vector load's wait
     // would drain the ring
@@ -356,8 +390,13 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
     constexpr int per = BM / 64;                     // loads of 64 rows
     if constexpr (NV > 0)
 #pragma unroll
-      for (int q = 0; q < (NV * per + NW - 1) / NW; ++q) {
+      for (int q = 0; q < (NV * per + NC + NW - 1) / NW; ++q) {
         const int x = q * NW + wave, v = x / per;
+        if (NC > 0 && x >= NV * per && x < NV * per + NC) {
+          const int y = x - NV * per;
+          load_to_lds4(g.stop + (int64_t)t.bn * BN + y * 64, (uint32_t)lane * 4,
+                       lds0 + G::kRingBytes + G::kRows + parity * (BN * 4) + y * 256);
+        }
         if (x < NV * per) {
           const float* src = NV == 1 || v == 2 ? g.rowf : v == 0 ? g.a : g.lse2;
           load_to_lds4(src + (int64_t)t.bm * BM + (x % per) * 64, (uint32_t)lane * 4,
@@ -594,6 +633,7 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
         if (row < g.M) g.part[(int64_t)cur.bn * g.M + row] = make_float2(m, sum);
       }
     } else if constexpr (DZ) {
+      constexpr bool kApart = F16 || EPI == EPI_DZB;  // stored in halves
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const float a = rows[wm * G::WTM + i * 32 + fr];
@@ -615,9 +655,68 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
             for (int q = 0; q < 16; ++q)
               if (j * 32 + 8 * (q >> 2) + (q & 3) >= past) acc[i][j][q] = 0.f;
         }
+      }
+      if constexpr (EPI == EPI_DZ) {
+        // largest |dz| of each of the wave's columns: two columns' upper 16 bits a
+        // word, halved over the lanes' rows until a pair of lanes has one word,
+        // columns (fr / 16) 32 + (fr / 4 % 4) 8 + 4 half + fr / 2 % 2 2 and the next
+        uint32_t w[16];
 #pragma unroll
-        for (int p = 0; p < (F16 || EPI == EPI_DZB ? 2 : 1); ++p) {
-          if (i + p > 0) wave_sync();
+        for (int t = 0; t < 16; ++t) {
+          float m[2] = {0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) m[u] = fmaxf(m[u], fabsf(acc[i][t >> 3][(t & 7) * 2 + u]));
+          w[t] = (__float_as_uint(m[0]) >> 16) | (__float_as_uint(m[1]) & 0xFFFF0000u);
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {                // lanes 16 apart
+          const auto x = __builtin_amdgcn_permlane16_swap(w[t], w[t + 8], false, false);
+          w[t] = max_u16x2(x[0], x[1]);
+        }
+        auto halve = [&](auto n, auto ctrl, int bit) {
+          const bool up = (fr >> bit) & 1;
+#pragma unroll
+          for (int t = 0; t < decltype(n)::value; ++t) {
+            const uint32_t x = w[t], y = w[t + decltype(n)::value];
+            w[t] = max_u16x2(up ? y : x, dpp<decltype(ctrl)::value>(up ? x : y));
+          }
+        };
+        halve(std::integral_constant<int, 4>{}, std::integral_constant<int, 0x128>{}, 3);  // 8 apart
+        halve(std::integral_constant<int, 2>{}, std::integral_constant<int, 0x141>{}, 2);  // 8 mirrored
+        halve(std::integral_constant<int, 1>{}, std::integral_constant<int, 0x4E>{}, 1);   // 2 apart
+        w[0] = max_u16x2(w[0], dpp<0xB1>(w[0]));                                           // next
+        const int col = (fr >> 4) * 32 + ((fr >> 2) & 3) * 8 + half * 4 + ((fr >> 1) & 1) * 2;
+        const auto* stop = reinterpret_cast<const uint32_t*>(extra + G::kRows) + (jt & 1) * BN +
+                           wn * 64 + col;
+        w[0] = max_u16x2(w[0], (stop[0] >> 16) | (stop[1] & 0xFFFF0000u));
+        const uint32_t l0 = level_of(w[0] & 0xFFFFu), l1 = level_of(w[0] >> 16);
+        const uint16_t both = (uint16_t)(l0 | l1 << 8);
+        if ((fr & 1) == 0 && n0 < g.Vpad)
+          *reinterpret_cast<uint16_t*>(g.level + ((int64_t)cur.bm * WGM + wm) * g.ldz + n0 + col) =
+              both;
+        if (__any((l0 != kFlat && l0 != kEmpty) || (l1 != kFlat && l1 != kEmpty))) {
+          if (lane == 0) *g.any = 1;
+          wave_sync();
+          *reinterpret_cast<uint16_t*>(patch + col) = both;
+          wave_sync();
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const uint32_t l = patch[j * 32 + 8 * (q >> 2) + 4 * half + (q & 3)];
+              const float f = __uint_as_float((127u + (l == kEmpty ? 0u : l)) << 23);
+#pragma unroll
+              for (int i = 0; i < FM; ++i) acc[i][j][q] *= f;
+            }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int p = 0; p < (kApart ? 2 : 1); ++p) {
+          wave_sync();
           // rows of 128 bytes, 16-byte chunk c of row r at c ^ r % 8
 #pragma unroll
           for (int j = 0; j < FN; ++j)
@@ -626,7 +725,7 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
               using H = Half<EPI != EPI_DZB>;
               const uint32_t lo = H::pack(acc[i][j][4 * q], acc[i][j][4 * q + 1]);
               const uint32_t hi = H::pack(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
-              if (F16 || EPI == EPI_DZB) {           // what the high half leaves
+              if (kApart) {           // what the high half leaves
                 acc[i][j][4 * q] -= H::lo(lo);
                 acc[i][j][4 * q + 1] -= H::hi(lo);
                 acc[i][j][4 * q + 2] -= H::lo(hi);

@@ -188,7 +188,8 @@ struct HeadPlan {
   int64_t rows, cols;
   int64_t off_parts, off_rowf, off_hz, off_wz, off_part, off_list, off_starts;
   int64_t off_a, off_lse, off_exp, off_sidx, off_sval, off_h, off_w, off_dz, off_dh,
-      off_dw, off_split;
+      off_dw, off_split, off_stop, off_level, off_cexp;
+  int64_t pieces;             // of the vocabulary
   int64_t bytes;
 };
 HeadPlan head_plan(int64_t n, int d, int64_t V, int32_t dtype, int k, bool backward);

@@ -755,11 +755,18 @@ PG_API int pg_orthogonalize(const void* G, int32_t dtype, int64_t n_mat,
  * Logits, statistics and losses are fp32, as all sums. bf16 operands are
  * multiplied as they are; fp32 ones as two fp16 halves (22 bits, three products
  * for one), each row of h placed by a power of two and T by another: elements
- * of T below 2^-17 of its largest lose bits, in steps of 2^-39 of that. dz is
- * held in fp16 before its two products (11 bits; fp32 operands: two halves, 22),
- * each row placed by its own bound, |a_n| + |w_n| below, for up to 256 rows of
- * bf16 in two bf16 halves (16 bits): dh and dT of bf16 operands are off by up to
- * about 1.4e-4 of their size (2-norm) before their own rounding, an fp32 dT too.
+ * below 2^-17 of the row's (T's) largest lose bits, in steps of 2^-39 of that;
+ * up to 320 rows forward and 64 backward as three bf16 parts (24 bits) instead,
+ * unplaced. An infinity among fp32 operands counts as NaN.
+ * dz is held in fp16 before its two products, each row placed by its own bound,
+ * |a_n| + |w_n| below, and each vocabulary row by the largest of its placed dz:
+ * an element is off by up to 2^-12 of itself (fp32 operands: two halves, 2^-22)
+ * and 2^-19 of that largest, also where every dz of a vocabulary row is small.
+ * T for dh, and h times its row's bound for dT, are placed in fp16 by their
+ * largest element, exact for bf16 elements down to 2^-31 of it. For up to 256
+ * rows of bf16 dz is two bf16 halves (16 bits), and T and h as they are. dh and
+ * dT of bf16 operands are off by up to about 1.4e-4 of their size (2-norm) before
+ * their own rounding, an fp32 dT too.
  * A row with a NaN, or a logit of +infinity, has lse NaN.
  * A workspace sized for the largest batch serves every smaller one of the
  * same d, V, k and dtype (256-byte aligned).
