@@ -561,7 +561,12 @@ __global__ __launch_bounds__(256) void head_copy_kernel(RowArgs g, PieceArgs w, 
           e = wave_imax(e);
         }
         const int p = placement(e);
-        if (lane == 0) g.rowf[row] = ldexpf(g.c2, -p - pw);
+        // (where the largest elements of h and T never meet, the power may leave
+        // fp32's range; the products it scales are zeros then)
+        if (lane == 0) {
+          const float f = ldexpf(g.c2, -p - pw);
+          g.rowf[row] = fminf(fmaxf(f, -3.4028235e38f), 3.4028235e38f);
+        }
         if (row < g.rows_pad)
           for (int c = lane * 8; c < g.dp; c += 512)
             put_halves(src, g.d, c, in, p, g.hz + row * g.dp, g.rows_pad * g.dp);

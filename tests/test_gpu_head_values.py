@@ -1,5 +1,6 @@
 """The head's losses at values where a rounding, or the range of a number format,
-decides: certain tokens, teachers at the ends of fp32, extreme temperatures.
+decides: certain tokens, teachers at the ends of fp32, extreme temperatures,
+largest elements that never meet.
 Helpers are those of test_gpu_head.py and test_gpu_head_calls.py."""
 import numpy as np
 import pytest
@@ -85,3 +86,31 @@ def test_extreme_temperatures():
     ref = oh.distill(c.H, c.T, ids, np.zeros((n, k)), tau, 2.0 ** -45)[0]
     assert np.all(ref > 2.0 ** -126)
     within("loss", o.loss, ref, 1e-4 * ref + tau * (c.ez.max(1) * 2))
+
+
+@pytest.mark.parametrize("n", [40, 400])
+@pytest.mark.parametrize("scale", [1.0, -1.0])
+def test_largest_elements_that_never_meet(n, scale):
+    """A column of h where T is zero, and one of T where h is, both of 2^90: what
+    undoes their placements is no fp32 number, and the logits are zero all the same."""
+    V, d = 700, 96
+    c = Case(34, n, V, d, "f32", scale)
+    c.h.zero_()
+    c.table.zero_()
+    c.h[:, 5] = 2.0 ** 90
+    c.table[:, 7] = 2.0 ** 90
+    tok = c.g.integers(0, V, n)
+    o = Loss(c, tok)
+    o.forward()
+    within("lse", o.lse, np.full(n, np.log(V)), np.full(n, 230 * U + 8 * U))
+    o.backward()
+    # dz = dloss (1 / V - [target]); dh = dz T, dT = dz^T h, each in its own column
+    dz = f64(o.dl)[:, None] * (np.full((n, V), 1.0 / V) - np.eye(V)[tok])
+    dh, dw = np.zeros((n, d)), np.zeros((V, d))
+    dh[:, 7], dw[:, 5] = scale * 2.0 ** 90 * dz.sum(1), scale * 2.0 ** 90 * dz.sum(0)
+    # exponents of 2 ln V at most, sums of V (n) terms
+    e = 2.0 ** 90 * np.abs(dz) * 300 * U
+    within("dh", o.dh, dh, (2.0 ** 90 * np.abs(dz).sum(1) * 2 * (3 * V + 1000) * U)[:, None]
+           + e.sum(1)[:, None])
+    within("dw", o.dw, dw, (2.0 ** 90 * np.abs(dz).sum(0) * 2 * (3 * n + 1000) * U)[:, None]
+           + e.sum(0)[:, None])
