@@ -111,6 +111,8 @@ int head_backward(pg::HeadArgs& g, const pg_table* table, int32_t d, float tempe
   g.V = table->n_rows;
   g.inv_tau = 1.f / temperature;
   if (g.n > 0 && (!g.dloss || !aligned(g.dloss, 4) || !aligned(g.dlse, 4))) return PG_EINVAL;
+  // later pieces read h again, and dh reads T while dT is written
+  if (g.n > 0 && ((g.dh && g.dh == g.h) || (g.dw && g.dw == g.table))) return PG_EINVAL;
   const pg::HeadPlan p = pg::head_plan(g.n, d, g.V, g.dtype, g.k, true);
   if (g.n > 0 && (!ws || ws_bytes < p.bytes || !aligned(ws, 256))) return PG_EINVAL;
   return hip_status(pg::launch_head_backward(p, g, ws, stream));

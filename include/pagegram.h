@@ -805,7 +805,8 @@ PG_API int pg_head_loss(const void* h, int32_t dtype, int64_t n, int32_t d, int6
  *   dw  dT, [V][d] of dw_dtype, PG_F32 or PG_BF16, written whole, or with
  *       accumulate = 1 (fp32 only, PG_EUNSUPPORTED for bf16) added to: after
  *       pg_embed_backward_dense the gradient of a tied table (nullable)
- * Not both dh and dw may be NULL. n = 0 writes zeros to dw unless accumulate.
+ * Not both dh and dw may be NULL; dh may not be h, nor dw the table's data
+ * (PG_EINVAL). n = 0 writes zeros to dw unless accumulate.
  */
 PG_API int pg_head_loss_backward(const void* h, int32_t dtype, int64_t n, int32_t d, int64_t ld_h,
                                  const pg_table* table, float scale, const int32_t* targets,
