@@ -56,6 +56,9 @@ bool in_place(int32_t dtype, int d, int64_t ld, const void* p) {
          (uintptr_t)p % 16 == 0;
 }
 
+// The same of a table, whose rows are packed and aligned.
+bool table_in_place(int32_t dtype, int d) { return in_place(dtype, d, d, nullptr); }
+
 // Whether M x N of K's slots go by large tiles: rounds of tiles over the chip (a
 // large one to a compute unit, or two small ones) times a tile's us, 0.95 or 0.6
 // a slot and its epilogue.
@@ -136,7 +139,7 @@ HeadPlan head_plan(int64_t n, int d, int64_t V, int32_t dtype, int k, bool backw
     if (p.cols > most) p.cols = most > 256 ? most : 256;
     p.off_rowf = take(pad(n, 256) * 4);
     p.off_hz = take(n * row);
-    p.off_wz = take(p.cols * row);
+    p.off_wz = take(table_in_place(dtype, d) ? 0 : p.cols * row);
     const int64_t few = tiles_of(V < kFewShort ? V : kFewShort, 32) * (n < kFew ? n : kFew);
     const int64_t parts = tiles_of(V, 128) * n;
     p.off_part = take((parts > few ? parts : few) * 8);
@@ -162,14 +165,15 @@ HeadPlan head_plan(int64_t n, int d, int64_t V, int32_t dtype, int k, bool backw
     p.off_sval = take(p.rows * k * 4);
     p.off_h = take(p.rows * row);
     p.off_hz = take(p.rows * row);
-    p.off_w = take(p.cols * row);
+    const bool wide = p.planes == 1 && n <= kWide;       // dz in bf16, T as it is
+    p.off_w = take(wide ? 0 : p.cols * row);
     // bf16 rows that cannot be read in place: all, or the last ones
-    p.off_wz = p.planes == 2 ? at : take((d % 32 == 0 && d >= 128 ? 128 : p.cols) * row);
+    p.off_wz = p.planes == 2 ? at : take((table_in_place(dtype, d) ? 128 : p.cols) * row);
     p.off_dz = take(p.rows * p.cols * 2 * halves);
-    p.off_dh = take(p.rows * d * 4);
+    p.off_dh = take(p.planes == 2 ? 0 : p.rows * d * 4);  // fp32 adds up in dh
     p.off_dw = n > 32768 ? take(V * d * 4) : at;
     p.off_split = take((int64_t)kCUs * 256 * 256 * 4);   // most tiles at once
-    if (!(p.planes == 1 && n <= kWide)) {                // dz in fp16
+    if (!wide) {
       p.pieces = (V + p.cols - 1) / p.cols;
       p.off_stop = take((pad(V, 256) + p.pieces) * 4);
       p.off_level = take(p.rows / 64 * p.cols);
