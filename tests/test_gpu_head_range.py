@@ -4,7 +4,8 @@ gradient's own size needs them as it needs the others, so every row of dT is
 held to its own size here, not to the largest one's.
 
 dz's error, element by element: the exponential's, a rounding to 11 bits (fp32
-operands 22), and steps of at most 2^-19 of the largest dz of its vocabulary row.
+operands 22), and steps of at most 2^-19 of the largest dz of its vocabulary row,
+both in units of their rows' bounds, |a| + |w| rounded down to a power of two.
 u = 2^-24 and the products' errors are those of test_gpu_head.py."""
 import numpy as np
 import pytest
@@ -42,20 +43,20 @@ def unlikely(seed, n, V, d, dt, depth, mixed, pad=0):
     return c, rare
 
 
-def row_bounds(c, dz, p, ez, lse):
-    """dT and its bound, each vocabulary row by its own dz."""
+def row_bounds(c, dz, p, ez, lse, bound):
+    """dT and its bound, each vocabulary row by its own dz; bound: |a| + |w| by row."""
+    unit = 2.0 ** np.floor(np.log2(np.where(bound > 0, bound, 1.0)))[:, None]
     one = c.dt == "bf16"
     H = np.abs(c.H)
     edz = p * np.expm1(ez + 6 * U * (np.abs(c.z) + np.abs(lse)[:, None]) + 16 * U)
     edz += 8 * U * (np.abs(dz) + p)
     edz += (np.abs(dz) + edz) * (2.0 ** -11 if one else 2.0 ** -22)
-    edz += 2.0 ** -19 * (np.abs(dz) + edz).max(0) + 3 * 2.0 ** -126
+    edz += 2.0 ** -19 * unit * ((np.abs(dz) + edz) / unit).max(0) + 3 * 2.0 ** -126
     mag = np.abs(dz) + edz
     _, ref = oh.grads(dz, c.H, c.T, 1.0)
     b = edz.T @ H + (mag.T @ H) * (2 * (3 * c.n + 1000) * U + (0 if one else 3.1 * 2.0 ** -22))
-    # h's copy: steps of 2^-39 of its largest element times its row's weight, the
-    # weights here within a factor of 4
-    b += mag.sum(0)[:, None] * 2.0 ** -36 * H.max()
+    # h's copy: half steps of 2^-39 of the largest of its elements times their row's unit
+    b += ((mag / unit).sum(0) * 2.0 ** -38 * (H.max(1) * unit[:, 0]).max())[:, None]
     return ref, b + HALF[c.dt] * (np.abs(ref) + b) + 2.0 ** -124
 
 
@@ -84,7 +85,8 @@ def test_rows_unlikely_everywhere(n, V, d, dt, depth, mixed):
     dl, ds = f64(o.dl), f64(o.ds)
     dz = oh.loss_dz(c.z, tok, lse, dl, ds)
     p = np.abs(np.where(tok >= 0, dl, 0) + ds)[:, None] * np.exp(c.z - lse[:, None])
-    ref, b = row_bounds(c, dz, p, c.ez, lse)
+    wt = np.where((tok >= 0) & (tok < V), dl, 0)
+    ref, b = row_bounds(c, dz, p, c.ez, lse, np.abs(wt + ds) + np.abs(wt))
     own = np.abs(ref).max(1)
     assert own[rare].min() < 2.0 ** -35 * own.max()     # what the test is about
     within("dw", o.dw, ref, b)
@@ -123,7 +125,7 @@ def test_entries_among_unlikely_rows(n, V, d, dt, mixed):
     r, j = np.nonzero(ok)
     np.add.at(share, (r, ids[r, j]), a[r] * q[r, j])
     # p and the shares, each with its error: the shares' from logits of at most 64
-    ref, b = row_bounds(c, dz, p + share, c.ez + 2.0 ** -16, lse)
+    ref, b = row_bounds(c, dz, p + share, c.ez + 2.0 ** -16, lse, 2 * a)
     within("dw", o.dw, ref, b)
     rh, bh, _, _ = c.grad_bounds(dz, p + share, 2 * a, c.ez + 2.0 ** -16, c.z, lse, dt)
     within("dh", o.dh, rh, bh)
