@@ -199,8 +199,8 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
   // 16-byte chunk c of token x in LDS: the 16 tokens a read serves together
   // meet every bank once
   auto place = [](int x, int c) {
-    if constexpr (RB == 512) return x * 512 + ((c ^ (x & 15)) * 16);
-    return RB == 256 ? x * 256 + ((c ^ (x & 15)) * 16) : x * 128 + ((c ^ ((x >> 1) & 7)) * 16);
+    static_assert(RB == 512 || RB == 128, "chunks of a row over the banks");
+    return RB == 512 ? x * 512 + ((c ^ (x & 15)) * 16) : x * 128 + ((c ^ ((x >> 1) & 7)) * 16);
   };
   const T* hp[HL];
   int hc[HL];

@@ -194,14 +194,15 @@ template <int BX, bool TR, int NW>
 struct Walk {
   static constexpr int DMA = BX / 16 / NW;           // loads of 1 KiB a wave and slot
   static_assert(DMA >= 1 && BX % (16 * NW) == 0, "whole loads");
+  static_assert(BX >= 128, "the places of a transposed slot's units");
   const uint8_t* base;
   uint32_t off[DMA];
   int64_t step;
 
   // A slot's row is 64 bytes of K (plain; four 16-byte chunks, chunk c of row r
   // at c ^ (r / 4) % 4) or BX elements (transposed; 64-byte units, unit u of
-  // row k at u ^ k % 4, or u ^ (k / 2) % 2 where a row has only two): a
-  // fragment read then meets every bank of a 256-byte line once.
+  // row k at u ^ k % 4): a fragment read then meets every bank of a 256-byte
+  // line once.
   __device__ __forceinline__ void start(const Side& s, int64_t outer0, int slot0, int wave,
                                         int lane) {
     if constexpr (!TR) {
@@ -223,8 +224,7 @@ struct Walk {
 #pragma unroll
       for (int q = 0; q < DMA; ++q) {
         const int k = (wave * DMA + q) * RPI + kr;
-        const int f = BX >= 128 ? (k & 3) : ((k >> 1) & 1);
-        int64_t col = outer0 + (cp ^ (f * 4)) * 8;
+        int64_t col = outer0 + (cp ^ ((k & 3) * 4)) * 8;
         if (col > s.outer - 8) col = s.outer - 8;
         off[q] = (uint32_t)(k * s.ld + (col - outer0) * 2);
       }
@@ -246,9 +246,8 @@ struct Walk {
     } else {
       // a transposing read gives lane i of 16 the i-th of 16 columns, four rows of K
       const int k = t * 16 + 8 * (lane >> 5) + ((lane & 15) >> 2);
-      const int f = BX >= 128 ? ((lane & 15) >> 2) : ((lane & 15) >> 3);
-      const uint8_t* p = slot + k * BX * 2 + (((w0 >> 5) ^ f) * 64) + ((lane >> 4) & 1) * 32 +
-                         (lane & 3) * 8;
+      const uint8_t* p = slot + k * BX * 2 + (((w0 >> 5) ^ ((lane & 15) >> 2)) * 64) +
+                         ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
       const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)p);
       const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + 4 * BX * 2));
       const s16x8_t v = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
