@@ -524,6 +524,10 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
         const unsigned blocks = (unsigned)(cols / (short_table ? 32 : 128));
         if (f32) launch_few<float, 1>(f, z, blocks, short_table, s);
         else launch_few<uint16_t, 2>(f, z, blocks, short_table, s);
+        if (!wide) {
+          copies.level = level;
+          copies.any = any;
+        }
       }
       launch_copy(f32, r, copies, first && !wide, s);
 
@@ -569,11 +573,11 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
       const int cb = wide ? 0 : blocks_for(cols, 2048);
       hipLaunchKernelGGL(head_sparse_kernel, dim3(cb + blocks_for(n * g.k, 8192)), dim3(256), 0, s,
                          z, cb);
-      if (!wide) {
+      ++any;
+      if (!wide && !few) {
         const int db = blocks_for(z.groups * tiles_of(cols, 256) * 256, 1024);
         const int tb = blocks_for(cols * p.dp / 8, 2048);
         hipLaunchKernelGGL(head_level_kernel, dim3(db + tb), dim3(256), 0, s, z, db);
-        ++any;
       }
 
       // dT of the piece: [c x d], K over the rows
@@ -586,6 +590,7 @@ hipError_t launch_head_backward(const HeadPlan& p, const HeadArgs& g, void* work
       tw.V = g.d;
       if (!wide) {
         tw.row_exp = z.col_exp;
+        tw.row_any = z.any;
         tw.all_exp = r.all_h;
       }
       if (g.dw) {

@@ -74,17 +74,35 @@ __device__ __forceinline__ void few_exp(const FewDz& z, int64_t tok, int64_t n, 
 #pragma unroll
   for (int q = 0; q < 4; ++q) v[q] = a == 0.f ? 0.f : a * __builtin_amdgcn_exp2f(v[q] - l);
 }
-// Largest |dz| at the sparse positions of the block's COLS columns from col on, as bits.
-template <int COLS>
-__device__ __forceinline__ void few_stops(const FewDz& z, int64_t col, uint32_t* stop) {
-  if (threadIdx.x < COLS) stop[threadIdx.x] = 0;
-  __syncthreads();
-#pragma unroll 4
-  for (int i = threadIdx.x; i < z.count; i += 256) {
-    const int64_t v = z.sidx[i] - z.v0 - col;
-    if (v >= 0 && v < COLS) atomicMax(stop + v, __float_as_uint(z.sval[i]) & 0x7FFFFFFFu);
+// Largest |dz| at the sparse positions of the block's COLS columns from col on, as
+// bits. The first ones, all of cross entropy's, are under way from the kernel's start.
+struct FewStops {
+  int32_t id;
+  float val;
+  __device__ __forceinline__ void start(const FewDz& z) {
+    const int i = threadIdx.x;
+    id = i < z.count ? z.sidx[i] : -1;
+    val = i < z.count ? z.sval[i] : 0.f;
   }
-  __syncthreads();
+  template <int COLS>
+  __device__ __forceinline__ void join(const FewDz& z, int64_t col, uint32_t* stop) const {
+    auto put = [&](int32_t at, float x) {
+      const int64_t v = at - z.v0 - col;
+      if (v >= 0 && v < COLS) atomicMax(stop + v, __float_as_uint(x) & 0x7FFFFFFFu);
+    };
+    if (threadIdx.x < COLS) stop[threadIdx.x] = 0;
+    __syncthreads();
+    put(id, val);
+#pragma unroll 4
+    for (int i = threadIdx.x + 256; i < z.count; i += 256) put(z.sidx[i], z.sval[i]);
+  }
+};
+// Largest of the 16 lanes' values.
+__device__ __forceinline__ uint32_t max_of16(uint32_t x) {
+  x = max(x, dpp<0x128>(x));                         // 8 apart
+  x = max(x, dpp<0x141>(x));                         // 8 mirrored
+  x = max(x, dpp<0x4E>(x));                          // 2 apart
+  return max(x, dpp<0xB1>(x));                       // next
 }
 // Stores it; MODE 1: fp16, two halves (fp32 operands); 2: two bf16 halves.
 template <int MODE>
@@ -108,17 +126,15 @@ __device__ __forceinline__ void few_dz_zero(const FewDz& z, int from, int64_t co
   }
 }
 
-// Lifts four columns of one row block: from col on, their largest |dz| in m as bits
-// of fp32 (of this lane's tokens; the 16 lanes fr have the others), f(t, q) theirs.
+// Lifts four columns from col on, their largest |dz| in m as bits of fp32, f(t, q)
+// this lane's tokens'.
 template <int TB, typename F>
-__device__ __forceinline__ void few_lift(const FewDz& z, int64_t col, uint32_t (&m)[4], int fr,
-                                         F f) {
+__device__ __forceinline__ void few_lift(const FewDz& z, int64_t col, const uint32_t (&m)[4],
+                                         int fr, F f) {
   uint32_t l[4];
   bool lifted = false;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-#pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) m[q] = max(m[q], (uint32_t)__shfl_xor((int)m[q], o));
     l[q] = level_of(m[q] >> 16);
     const bool some = l[q] != kFlat && l[q] != kEmpty;
     lifted |= some;
@@ -183,6 +199,8 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
   __shared__ __attribute__((aligned(256))) uint8_t hs[2][P][16 * TB * RB];
   __shared__ float2 red[4][16 * TB];
   __shared__ uint32_t stop[DZ == 1 ? 128 : 1];
+  FewStops stops;
+  if constexpr (DZ == 1) stops.start(dz);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, fr = lane & 15, kq = lane >> 4;
   // a tile's groups run 8 blocks apart: on one XCD, where they share its L2
   const uint32_t id = blockIdx.x;
@@ -291,7 +309,10 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
           f[t][r][q] = v0 + r * 16 + 4 * kq + q < g.V ? acc[t][r][q] * g.c2 : -INFINITY;
         few_exp(dz, t * 16 + fr, g.n, f[t][r]);
       }
-    if constexpr (DZ == 1) few_stops<128>(dz, (int64_t)tile * 128, stop);
+    if constexpr (DZ == 1) {
+      stops.template join<128>(dz, (int64_t)tile * 128, stop);
+      __syncthreads();
+    }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int64_t col = v0 + r * 16 + 4 * kq;
@@ -299,9 +320,10 @@ __global__ __launch_bounds__(256, 2) void head_few_kernel(FewArgs g, FewDz dz) {
         uint32_t m[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          m[q] = stop[wave * 32 + r * 16 + 4 * kq + q];
+          m[q] = 0;
 #pragma unroll
           for (int t = 0; t < TB; ++t) m[q] = max(m[q], __float_as_uint(fabsf(f[t][r][q])));
+          m[q] = max(max_of16(m[q]), stop[wave * 32 + r * 16 + 4 * kq + q]);
         }
         few_lift<TB>(dz, col, m, fr, [&](int t, int q) -> float& { return f[t][r][q]; });
       }
@@ -360,6 +382,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_f
   static_assert(DZ == 0 || (DZ == 1) == F32, "dz of fp32 operands is fp16");
   __shared__ f32x4_t join[4][TB * 2][64];
   __shared__ uint32_t stop[DZ == 1 ? 32 : 1];
+  FewStops stops;
+  if constexpr (DZ == 1) stops.start(z);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, fr = lane & 15, kq = lane >> 4;
   const int64_t v0 = (int64_t)blockIdx.x * 32;
   const T *wp[2], *hp[TB];
@@ -457,13 +481,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && TB == 4 ? 1 : 2) void head_f
   }
   if constexpr (DZ == 1) {
     // the token blocks' largest meet where the sparse positions' are
-    few_stops<32>(z, v0, stop);
+    stops.template join<32>(z, v0, stop);
     if (wave < TB)
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          atomicMax(stop + r * 16 + 4 * kq + q, __float_as_uint(fabsf(v[r][q])));
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t m4 = max_of16(__float_as_uint(fabsf(v[r][q])));
+          if (fr == 0) atomicMax(stop + r * 16 + 4 * kq + q, m4);
+        }
     __syncthreads();
     if (wave < TB)
 #pragma unroll

@@ -507,6 +507,8 @@ struct PieceArgs {
   const void* src;
   int64_t rows, rows_pad;
   uint16_t *wp, *wz;
+  const uint8_t* level;    // by row, of columns that dz has already (nullable)
+  const int* any;          // whether some of them are lifted
 };
 
 template <typename T>
@@ -519,12 +521,16 @@ __global__ __launch_bounds__(256) void head_copy_kernel(RowArgs g, PieceArgs w, 
   if ((int)blockIdx.x >= row_blocks) {
     const int per = g.dp / 8;
     const int64_t total = w.rows_pad * per, step = (int64_t)(gridDim.x - row_blocks) * 256;
+    const uint8_t* level = w.level && *w.any ? w.level : nullptr;
     for (int64_t i = ((int64_t)blockIdx.x - row_blocks) * 256 + threadIdx.x; i < total; i += step) {
       const int64_t r = i / per;
       const int c = (int)(i - r * per) * 8;
       const bool in = r < w.rows;
       const T* src = static_cast<const T*>(w.src) + (in ? r : 0) * g.d;
-      if (w.wp) put_halves(src, g.d, c, in, pw, w.wp + r * g.dp, w.rows_pad * g.dp);
+      if (w.wp) {
+        const int l = level && level[r] != kEmpty ? level[r] : kFlat;
+        put_halves(src, g.d, c, in, pw - l, w.wp + r * g.dp, w.rows_pad * g.dp);
+      }
       if constexpr (!F32)
         if (w.wz) put_raw(src, g.d, c, in, w.wz + r * g.dp);
     }
@@ -598,7 +604,7 @@ struct DzArgs {
   const uint8_t* level;
   int group, groups;       // rows of a group, how many
   const int* any;
-  int* col_exp;            // [ldz] what dT's rows undo: minus the columns' own level
+  int* col_exp;            // [ldz] where any: what dT's rows undo, minus the columns' own level
   uint16_t* wp;            // [ldz][dp] T's copy, its halves `wplane` elements apart
   int dp;
   int64_t wplane;
@@ -609,12 +615,11 @@ struct DzArgs {
 // own levels, the lowest of their groups.
 __global__ __launch_bounds__(256) void head_sparse_kernel(DzArgs g, int col_blocks) {
   if ((int)blockIdx.x < col_blocks) {
-    const bool some = *g.any != 0;
+    if (*g.any == 0) return;
     for (int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x; v < g.ldz; v += col_blocks * 256) {
-      int l = some ? kEmpty : kFlat;
-      if (some)
+      int l = kEmpty;
 #pragma unroll 8
-        for (int i = 0; i < g.groups; ++i) l = min(l, (int)g.level[i * g.ldz + v]);
+      for (int i = 0; i < g.groups; ++i) l = min(l, (int)g.level[i * g.ldz + v]);
       g.col_exp[v] = l == kEmpty ? 0 : -l;
     }
     return;
@@ -674,8 +679,8 @@ __device__ __forceinline__ void scale_at(uint16_t* p, int64_t step, int64_t plan
   }
 }
 
-// Where columns are lifted: their groups of rows to their own level, and T's rows in
-// the copy for dh down by as much. The first `dz_blocks` blocks take dz, 256 columns
+// Where columns are lifted and dz has more than one group: their groups of rows to
+// their own level, and T's rows in the copy for dh down by as much. The first `dz_blocks` blocks take dz, 256 columns
 // of a group at a time. One load a block where nothing is lifted (5 us); all of
 // 16,384 x 25,152 columns read and written in 340 us, 4.8 TB/s.
 __global__ __launch_bounds__(256) void head_level_kernel(DzArgs g, int dz_blocks) {

@@ -182,6 +182,7 @@ struct TileArgs {
   const float* prev;   // added (nullable); may be out
   int64_t ld_prev;
   const int* row_exp;  // results times 2^(row_exp[row] + *all_exp); each nullable
+  const int* row_any;  // row_exp counts where this is not 0 (nullable: always)
   const int* all_exp;
 };
 
@@ -750,6 +751,7 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
     } else {
       const int64_t so = (int64_t)cur.split * g.split_out;
       const int all_exp = g.all_exp ? *g.all_exp : 0;
+      const bool by_row = g.row_exp && !(g.row_any && *g.row_any == 0);
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -769,7 +771,7 @@ __device__ __forceinline__ void walk_tiles(const TileArgs& g, uint8_t* smem, Nex
             const int64_t row = m0 + i * 32 + r, col = n0 + j * 32 + c * 4;
             const int left = (int)(g.V - col < 4 ? g.V - col : 4);
             if (row >= g.M || left <= 0) continue;
-            const int e = all_exp + (g.row_exp ? g.row_exp[row] : 0);
+            const int e = all_exp + (by_row ? g.row_exp[row] : 0);
             float v[4] = {ldexpf(f.x, e), ldexpf(f.y, e), ldexpf(f.z, e), ldexpf(f.w, e)};
             if (g.prev) {
               const float* pv = g.prev + row * g.ld_prev + col;
