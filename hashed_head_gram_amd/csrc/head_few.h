@@ -61,7 +61,8 @@ __device__ __forceinline__ float few_top(const Raw8<float>& v, float m) {
   return m;
 }
 // A wave's share of the exponent of T's largest element, whose rows dz reads in
-// fp32 in any case (65,536 rows of 2048, 8 tokens: 706 us, 811 with a pass of its own).
+// fp32 in any case (65,536 rows of 2048, 8 tokens: 712 us; a pass of its own took 105
+// more).
 __device__ __forceinline__ void few_put_top(const FewDz& z, float m) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));

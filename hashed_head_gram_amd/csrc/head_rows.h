@@ -191,8 +191,8 @@ __global__ __launch_bounds__(NT) void head_join_kernel(JoinArgs g) {
 // Sorts the entries of each row tile by column tile: a block a row tile, counts,
 // a running sum, places. The order inside a tile is free: every entry has a
 // place of its own to write to. Fetched as dot products of their own, 8,192
-// tokens' 64 entries at width 2,560 took 520 of 5,200 us; sorted, and picked
-// from the tiles' accumulators, 30.
+// tokens' 64 entries at width 2,560 took 520 of 4,900 us; sorted, 18, and picked
+// from the tiles' accumulators.
 constexpr int kMostTiles = 8192;
 __global__ __launch_bounds__(1024) void head_bin_kernel(const int32_t* ids, int64_t n, int k,
                                                         int64_t V, int b, int tiles, int64_t cap,
@@ -322,7 +322,8 @@ constexpr int kFew = 64, kFewOdd = 128, kFewF32 = 320;
 constexpr int64_t kFewShort = 8192;
 // Tokens up to which bf16 tables are used as they are for dh too: dz is then two
 // bf16 halves (16 bits), two products for one, and the fp16 copies, three more
-// passes over the table, fall away (65,536 rows of 2048, 8 tokens: 354 us, 430).
+// passes over the table, fall away (65,536 rows of 2048, 8 tokens: 295 us; a fifth
+// more with them).
 constexpr int kWide = 256;
 constexpr int kScanBlocks = 512;
 static_assert(kTops <= kScanBlocks, "they share part_w");

@@ -11,8 +11,8 @@
 // time, so no transposed copy of h, T or dz is ever made).
 //
 // What bounds it: power. The large products run at 1,070 to 1,290 TFLOP/s (a
-// large library product: 1,155), the clock at 1.4 to 1.75 GHz with the matrix
-// units busy 47 to 70 % of the time; with zeros for dz the same launch is 12 %
+// large library product: 1,155), the clock at 1.4 to 1.7 GHz with the matrix
+// units busy 53 to 75 % of the time; with zeros for dz the same launch is 12 %
 // faster. Four waves of 128 x 128, which read a third less from LDS, were 4 %
 // slower (nothing runs through barriers and epilogues), K walks a slot apart on
 // neighbouring tiles within 1 % either way.

@@ -763,10 +763,10 @@ PG_API int pg_orthogonalize(const void* G, int32_t dtype, int64_t n_mat,
  * an element is off by up to 2^-12 of itself (fp32 operands: two halves, 2^-22)
  * and 2^-19 of that largest, also where every dz of a vocabulary row is small.
  * T for dh, and h times its row's bound for dT, are placed in fp16 by their
- * largest element, exact for bf16 elements down to 2^-31 of it. For up to 256
- * rows of bf16 dz is two bf16 halves (16 bits), and T and h as they are. dh and
- * dT of bf16 operands are off by up to about 1.4e-4 of their size (2-norm) before
- * their own rounding, an fp32 dT too.
+ * largest element: exact for bf16 elements down to 2^-31 of it, fp32 ones as
+ * above. For up to 256 rows of bf16 dz is two bf16 halves (16 bits), and T and h
+ * as they are. dh and dT of bf16 operands are off by up to about 1.4e-4 of their
+ * size (2-norm) before their own rounding, an fp32 dT too.
  * A row with a NaN, or a logit of +infinity, has lse NaN.
  * A workspace sized for the largest batch serves every smaller one of the
  * same d, V, k and dtype (256-byte aligned).
@@ -823,7 +823,8 @@ PG_API int pg_head_loss_backward(const void* h, int32_t dtype, int64_t n, int32_
  *   lse_n  = log sum_v exp(z_nv / tau), over the whole vocabulary
  *   loss_n = tau^2 sum_j q_nj (log q_nj - (z_n,id_j / tau - lse_n)),
  * the Kullback-Leibler divergence, 0 for a row without entries or whose
- * entries are all -infinity. An id may be named twice; its shares add up.
+ * entries are all -infinity. An id may be named twice: the loss sums its entries
+ * one by one, its gradient their shares.
  *   ids int32 [n][k], teacher fp32 [n][k], 1 <= k <= 256 (PG_EUNSUPPORTED
  *   beyond); loss, lse fp32 [n]; logits fp32 [n][k]: z at the ids, 0 where
  *   there is none, what the backward pass takes

@@ -312,3 +312,10 @@ def test_graphs_that_share_a_workspace(n, V, d, dt):
         assert all(calls.same(want[i], made[i].outputs()) for i in order)
         del junk
     assert shared.intact()
+
+
+@pytest.mark.parametrize("n,V,d,dt", [(64, 3001, 64, "f32"), (63, 9001, 40, "f32"),
+                                      (64, 3001, 128, "bf16"), (20, 8193, 33, "f32")])
+def test_few_tokens_with_the_most_entries(n, V, d, dt):
+    basic.test_distill(n, V, d, dt, 256, 2.0, 1.0, 0)
+    basic.test_distill_backward(n, V, d, dt, 256, 2.0, 1.0, 0)
