@@ -25,11 +25,11 @@
 // 2^-31 of the largest. Columns of dz that lie below fp16's normal numbers in every
 // row (tokens that no position finds likely, whose rows of dT are as small) are
 // lifted by powers of two of their own, which dT undoes and T's copy takes back:
-// 1 to 2 % of a call where there are none (16,384 x 768 of 50,304: 3,650 us, 3,590
-// without; 16,384 x 2,560 of 128,000: 28.1 ms, 28.0), up to a quarter where most
-// columns change from one group of rows to the next. fp32 operands, and dz with them, are two fp16 halves
-// (22 bits), multiplied as hi lo, lo hi and hi hi, one K three times as long;
-// h for the logits is placed row by row.
+// 1 % of a call where there are none (16,384 x 768 of 50,304: 3,740 us, 3,700
+// without; 16,384 x 2,560 of 128,000: 28.86 ms, 28.76), up to a quarter where most
+// columns change from one group of rows to the next. fp32 operands, and dz with
+// them, are two fp16 halves (22 bits), multiplied as hi lo, lo hi and hi hi, one K
+// three times as long; h for the logits is placed row by row.
 #include <math.h>
 
 #include "head_few.h"

@@ -130,3 +130,43 @@ def test_entries_among_unlikely_rows(n, V, d, dt, mixed):
     rh, bh, _, _ = c.grad_bounds(dz, p + share, 2 * a, c.ez + 2.0 ** -16, c.z, lse, dt)
     within("dh", o.dh, rh, bh)
     assert o.w2.intact()
+
+
+@pytest.mark.parametrize("n,V,d,dt", [(300, 900, 128, "bf16"), (50, 900, 72, "f32"),
+                                      (300, 900, 72, "f32")])
+def test_a_graph_with_and_without_unlikely_rows(n, V, d, dt):
+    """What one replay lifted is of no account in the next, nor is the workspace."""
+    c, rare = unlikely(43, n, V, d, dt, 30.0, True)
+    with_rare = c.h.clone()
+    without = c.h.clone()
+    without[:, 0] = 0
+    o = Loss(c, c.g.choice(np.nonzero(~rare)[0], n), zloss=True)
+
+    def step():
+        o.forward()
+        o.backward()
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    seen = []
+    for i, h in enumerate((with_rare, without, without, with_rare, without)):
+        c.h.copy_(h)
+        o.w2.ws.fill_(0xFF if i % 2 else 0)
+        step()
+        want = o.outputs()
+        o.w2.ws.fill_(0x3C if i % 2 else 0xFF)
+        for t in (o.loss, o.lse, o.dh, o.dw):
+            t.fill_(-1)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = o.outputs()
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(want, got)), i
+        seen.append(got)
+    for i, j in ((0, 3), (1, 2), (1, 4)):
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+                   for a, b in zip(seen[i], seen[j]))
+    size = f64(seen[0][3])[rare]
+    assert 0 < np.abs(size).max(1).min() < 1e-12
+    assert o.w1.intact() and o.w2.intact()
